@@ -490,6 +490,104 @@ lte_status lte_gla_decode_step(int32_t B, int32_t H, int32_t dk, int32_t dv, int
                                const void* q_t, const void* k_t, const void* v_t,
                                const float* a_t, void* o_t, float* state, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: the linear layer whose state forgets by key.  It stands
+ * beside the gated linear layer above: the same state equation ["Background:
+ * Linear attention"], with the value written under a key replaced and not only
+ * added to.  Per value head, with a_t = exp(g_t):
+ *   S_t = a_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
+ *   o_t = scale S_t q_t                                    (S_t: dv x dk).
+ * Value head h uses query/key head h / (H / Hk).  Keys are taken as given: for
+ * a state that does not grow, |k_t| <= 1 and 0 <= beta_t <= 2 (lte_qk_norm_rope
+ * with LTE_NORM_L2 makes unit keys).
+ * q, k: [B,T,Hk,dk]; v, o: [B,T,H,dv] (dtype); strides as everywhere (NULL =
+ * contiguous); g (<= 0; -inf forgets everything), beta: fp32 [B,T,H]
+ * contiguous; states: fp32 [B,H,dv,dk] contiguous.
+ * lens (nullable): int32 [B] on the device, sequence b has the tokens
+ * 0 .. lens[b] - 1 (clamped to [0, T]); later rows of the inputs are not read
+ * and later rows of the outputs are left as they were; the state is the one
+ * after the last token.
+ * Supported: dk, dv in {64, 128}, Hk dividing H, bf16 or fp32.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, T, H, Hk, dk, dv;
+  float scale;
+  int32_t dtype;
+} lte_gdr_dims;
+
+enum { LTE_GDR_WS_PREFILL = 0, LTE_GDR_WS_BACKWARD = 1 };
+
+/* Bytes of workspace that a call needs (0 on invalid dims). */
+size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which);
+
+/* lte_gdr_prefill -- T tokens per sequence.  state_in (nullable: zeros) and
+ * state_out (may be the same buffer) are S before the first and after the last
+ * token.  bf16: chunks of 64 tokens on tensor cores; the products behind the
+ * state take fp32 operands as bf16 hi + lo pairs (relative error about 2^-17),
+ * so the fp32 state keeps about 1e-5; o is rounded once to bf16.  fp32, and
+ * bf16 with few tokens: token by token in fp32.  No atomics: results repeat
+ * bit by bit.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
+                           const lte_strides* q_strides, const lte_strides* k_strides,
+                           const lte_strides* v_strides, const float* g, const float* beta,
+                           const int32_t* lens, const float* state_in, void* o,
+                           const lte_strides* o_strides, float* state_out, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* lte_gdr_decode_step -- one token per sequence (d->T is ignored): q_t, k_t
+ * [B,Hk,dk], v_t, o_t [B,H,dv], g_t, beta_t fp32 [B,H], all contiguous; state is
+ * updated in place.  fp32 arithmetic for both dtypes. */
+lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,
+                               const void* v_t, const float* g_t, const float* beta_t, void* o_t,
+                               float* state, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * lte_qk_norm_rope -- norms of queries and keys per head and the rotation by
+ * position, in one pass, in front of a mixer (LTE attention: RMS norm and
+ * rotation; the delta rule: LTE_NORM_L2).  For a row x (one token and head):
+ *   n = x (c sum x^2 + eps)^(-1/2) w, c = 1/D (LTE_NORM_RMS) or 1 (LTE_NORM_L2),
+ *   n = x for LTE_NORM_NONE;
+ *   y = n with channel pairs turned by the row's position p: for i < rot_dim/2
+ *   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin), cos = table[p][i], sin =
+ *   table[p][rot_dim/2 + i]; (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) if
+ *   interleaved; channels from rot_dim on are not turned.
+ * q: [B,T,Hq,D], k: [B,T,Hkv,D] (strides as everywhere); outputs contiguous,
+ * may be the inputs if those are contiguous.  wq, wk: fp32 [D], NULL = ones.
+ * positions: int32 [B,T] on the device, NULL = 0 .. T-1; table: fp32
+ * [n_pos, rot_dim]; a row whose position is not in [0, n_pos) comes out as NaN
+ * on its rotated channels.  rot_dim = 0 needs neither.  D in {64, 128},
+ * rot_dim a multiple of 16 up to D, eps > 0 unless LTE_NORM_NONE.
+ * Arithmetic: fp32, outputs rounded once.
+ * ------------------------------------------------------------------------- */
+typedef enum { LTE_NORM_NONE = 0, LTE_NORM_RMS = 1, LTE_NORM_L2 = 2 } lte_norm_kind;
+
+typedef struct {
+  int32_t B, T, Hq, Hkv, D;
+  int32_t dtype;          /* of q, k, their outputs and gradients */
+  int32_t kind;           /* lte_norm_kind */
+  float eps;
+  int32_t rot_dim, interleaved, n_pos;
+  const float *wq, *wk;   /* device, fp32 [D], nullable */
+  const float* table;     /* device, fp32 [n_pos, rot_dim] */
+} lte_qk_norm;
+
+lte_status lte_qk_norm_rope(const lte_qk_norm* p, const void* q, const void* k,
+                            const lte_strides* q_strides, const lte_strides* k_strides,
+                            const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+/* lte_qk_norm_rope_backward -- given dq_out, dk_out (gradients of the outputs,
+ * contiguous, in grad_dtype: fp32, or the dtype), writes dq, dk (contiguous,
+ * dtype) and, where not NULL, dwq, dwk (fp32 [D], summed over all rows in a
+ * fixed order).  q, k: the forward's inputs.  Workspace:
+ * lte_qk_norm_backward_workspace_bytes(p) bytes. */
+size_t lte_qk_norm_backward_workspace_bytes(const lte_qk_norm* p);
+lte_status lte_qk_norm_rope_backward(const lte_qk_norm* p, const void* q, const void* k,
+                                     const lte_strides* q_strides, const lte_strides* k_strides,
+                                     const int32_t* positions, const void* dq_out,
+                                     const void* dk_out, int32_t grad_dtype, void* dq, void* dk,
+                                     float* dwq, float* dwk, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
 /* Library version string (static storage). */
 const char* lte_version(void);
 

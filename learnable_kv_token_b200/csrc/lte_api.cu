@@ -70,6 +70,66 @@ inline int cnn_past(const lte_cnn* c) { return c->past1 + c->past2; }
 
 inline lte_status from_cuda(cudaError_t e) { return e == cudaSuccess ? LTE_OK : LTE_ERR_CUDA; }
 
+lte_status check_gdr(const lte_gdr_dims* d) {
+  if (d == nullptr) return LTE_ERR_INVALID_ARG;
+  if (d->B < 1 || d->T < 1 || d->H < 1 || d->Hk < 1 || d->dk < 1 || d->dv < 1 || d->H % d->Hk != 0)
+    return LTE_ERR_INVALID_ARG;
+  if (d->dtype != LTE_F32 && d->dtype != LTE_BF16) return LTE_ERR_INVALID_ARG;
+  if (!std::isfinite(d->scale)) return LTE_ERR_INVALID_ARG;
+  if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128)) return LTE_ERR_UNSUPPORTED;
+  // grids of one or more CTAs per unit, per slice of its values and per chunk
+  if ((long long)d->B * d->H * 8 * ((d->T + 63) / 64) >= (1ll << 31) || d->T >= (1 << 30))
+    return LTE_ERR_UNSUPPORTED;
+  return LTE_OK;
+}
+
+// strides of a [B,T,heads,D] tensor: NULL -> contiguous, otherwise 16-byte multiples
+lte_status strides_of(const lte_strides* s, int T, int heads, int D, int dtype, Strides4* out) {
+  if (s == nullptr) {
+    *out = Strides4{(long long)T * heads * D, (long long)heads * D, D};
+    return LTE_OK;
+  }
+  const int per16 = 16 / elt_size(dtype);
+  if (s->b % per16 || s->t % per16 || s->h % per16 || s->b < 0 || s->t < 0 || s->h < 0)
+    return LTE_ERR_INVALID_ARG;
+  *out = Strides4{s->b, s->t, s->h};
+  return LTE_OK;
+}
+
+lte_status check_norm(const lte_qk_norm* p) {
+  if (p == nullptr) return LTE_ERR_INVALID_ARG;
+  if (p->B < 1 || p->T < 1 || p->Hq < 1 || p->Hkv < 1 || p->D < 1) return LTE_ERR_INVALID_ARG;
+  if (p->dtype != LTE_F32 && p->dtype != LTE_BF16) return LTE_ERR_INVALID_ARG;
+  if (p->kind != LTE_NORM_NONE && p->kind != LTE_NORM_RMS && p->kind != LTE_NORM_L2)
+    return LTE_ERR_INVALID_ARG;
+  if (p->kind != LTE_NORM_NONE && (!(p->eps > 0.f) || !std::isfinite(p->eps))) return LTE_ERR_INVALID_ARG;
+  if (p->rot_dim < 0 || p->rot_dim > p->D || p->rot_dim % 16 != 0) return LTE_ERR_INVALID_ARG;
+  if (p->rot_dim > 0 && (p->table == nullptr || p->n_pos < 1 || !aligned16(p->table)))
+    return LTE_ERR_INVALID_ARG;
+  if ((p->wq != nullptr && !aligned16(p->wq)) || (p->wk != nullptr && !aligned16(p->wk)))
+    return LTE_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return LTE_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->T * ((long long)p->Hq + p->Hkv) >= (1ll << 34)) return LTE_ERR_UNSUPPORTED;
+  return LTE_OK;
+}
+
+lte_status norm_args(const lte_qk_norm* p, const void* q, const void* k, const lte_strides* qs,
+                     const lte_strides* ks, const int32_t* positions, lte::QkNormArgs* n) {
+  lte_status st = check_norm(p);
+  if (st != LTE_OK) return st;
+  if (!q || !k || !aligned16(q) || !aligned16(k)) return LTE_ERR_INVALID_ARG;
+  // without positions, row t takes position t
+  if (p->rot_dim > 0 && positions == nullptr && p->T > p->n_pos) return LTE_ERR_INVALID_ARG;
+  *n = lte::QkNormArgs{};
+  if ((st = strides_of(qs, p->T, p->Hq, p->D, p->dtype, &n->xs[0])) != LTE_OK) return st;
+  if ((st = strides_of(ks, p->T, p->Hkv, p->D, p->dtype, &n->xs[1])) != LTE_OK) return st;
+  n->B = p->B; n->T = p->T; n->H[0] = p->Hq; n->H[1] = p->Hkv; n->D = p->D;
+  n->dtype = p->dtype; n->kind = p->kind; n->eps = p->eps;
+  n->rot = p->rot_dim; n->inter = p->interleaved != 0; n->n_pos = p->n_pos;
+  n->x[0] = q; n->x[1] = k; n->w[0] = p->wq; n->w[1] = p->wk; n->table = p->table; n->pos = positions;
+  return LTE_OK;
+}
+
 constexpr size_t kErrBytes = 256;   // error word + padding (keeps scratch 256-aligned)
 
 }  // namespace
@@ -488,6 +548,91 @@ lte_status lte_gla_decode_step(int32_t B, int32_t H, int32_t dk, int32_t dv, int
   if (dk != 128 || dv != 128) return LTE_ERR_UNSUPPORTED;
   return from_cuda(lte::gla_decode(B, H, dk, dv, dtype, q_t, k_t, v_t, a_t, o_t, state,
                                    as_stream(stream)));
+}
+
+size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which) {
+  if (check_gdr(d) != LTE_OK) return 0;
+  if (which == LTE_GDR_WS_PREFILL) return 16;
+  return 0;
+}
+
+lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
+                           const lte_strides* q_strides, const lte_strides* k_strides,
+                           const lte_strides* v_strides, const float* g, const float* beta,
+                           const int32_t* lens, const float* state_in, void* o,
+                           const lte_strides* o_strides, float* state_out, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  lte_status st = check_gdr(d);
+  if (st != LTE_OK) return st;
+  if (!q || !k || !v || !g || !beta || !o || !state_out) return LTE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state_out) ||
+      !aligned16(state_in) || !aligned16(workspace))
+    return LTE_ERR_INVALID_ARG;
+  lte::DeltaArgs a{};
+  if ((st = strides_of(q_strides, d->T, d->Hk, d->dk, d->dtype, &a.qs)) != LTE_OK ||
+      (st = strides_of(k_strides, d->T, d->Hk, d->dk, d->dtype, &a.ks)) != LTE_OK ||
+      (st = strides_of(v_strides, d->T, d->H, d->dv, d->dtype, &a.vs)) != LTE_OK ||
+      (st = strides_of(o_strides, d->T, d->H, d->dv, d->dtype, &a.os)) != LTE_OK)
+    return st;
+  if (workspace == nullptr || ws_bytes < lte_gdr_workspace_bytes(d, LTE_GDR_WS_PREFILL))
+    return LTE_ERR_WORKSPACE;
+  a.d = d; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lens = lens;
+  a.s_in = state_in; a.o = o; a.s_out = state_out; a.scratch = workspace;
+  return from_cuda(lte::delta_recurrent(a, as_stream(stream)));
+}
+
+lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,
+                               const void* v_t, const float* g_t, const float* beta_t, void* o_t,
+                               float* state, void* stream) {
+  if (d == nullptr) return LTE_ERR_INVALID_ARG;
+  lte_gdr_dims one = *d;
+  one.T = 1;
+  const lte_status st = check_gdr(&one);
+  if (st != LTE_OK) return st;
+  if (!q_t || !k_t || !v_t || !g_t || !beta_t || !o_t || !state) return LTE_ERR_INVALID_ARG;
+  if (!aligned16(q_t) || !aligned16(k_t) || !aligned16(v_t) || !aligned16(o_t) || !aligned16(state))
+    return LTE_ERR_INVALID_ARG;
+  return from_cuda(lte::delta_step(&one, q_t, k_t, v_t, g_t, beta_t, o_t, state, as_stream(stream)));
+}
+
+lte_status lte_qk_norm_rope(const lte_qk_norm* p, const void* q, const void* k,
+                            const lte_strides* q_strides, const lte_strides* k_strides,
+                            const int32_t* positions, void* q_out, void* k_out, void* stream) {
+  lte::QkNormArgs n;
+  const lte_status st = norm_args(p, q, k, q_strides, k_strides, positions, &n);
+  if (st != LTE_OK) return st;
+  if (!q_out || !k_out || !aligned16(q_out) || !aligned16(k_out)) return LTE_ERR_INVALID_ARG;
+  n.y[0] = q_out; n.y[1] = k_out;
+  return from_cuda(lte::qk_norm(n, as_stream(stream)));
+}
+
+size_t lte_qk_norm_backward_workspace_bytes(const lte_qk_norm* p) {
+  if (check_norm(p) != LTE_OK) return 0;
+  return lte::qk_norm_backward_bytes(p->B, p->T, p->Hq, p->Hkv, p->D);
+}
+
+lte_status lte_qk_norm_rope_backward(const lte_qk_norm* p, const void* q, const void* k,
+                                     const lte_strides* q_strides, const lte_strides* k_strides,
+                                     const int32_t* positions, const void* dq_out,
+                                     const void* dk_out, int32_t grad_dtype, void* dq, void* dk,
+                                     float* dwq, float* dwk, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  lte::QkNormArgs n;
+  const lte_status st = norm_args(p, q, k, q_strides, k_strides, positions, &n);
+  if (st != LTE_OK) return st;
+  if (!dq_out || !dk_out || !dq || !dk || !aligned16(dq_out) || !aligned16(dk_out) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(workspace))
+    return LTE_ERR_INVALID_ARG;
+  if (grad_dtype != LTE_F32 && grad_dtype != p->dtype) return LTE_ERR_INVALID_ARG;
+  // a norm without that weight has no gradient for it
+  if (p->kind == LTE_NORM_NONE && (dwq != nullptr || dwk != nullptr)) return LTE_ERR_INVALID_ARG;
+  if (workspace == nullptr || ws_bytes < lte_qk_norm_backward_workspace_bytes(p))
+    return LTE_ERR_WORKSPACE;
+  strides_of(nullptr, p->T, p->Hq, p->D, p->dtype, &n.ds[0]);
+  strides_of(nullptr, p->T, p->Hkv, p->D, p->dtype, &n.ds[1]);
+  n.dy[0] = dq_out; n.dy[1] = dk_out; n.y[0] = dq; n.y[1] = dk; n.grad_dtype = grad_dtype;
+  n.part = (float*)workspace; n.dwq = dwq; n.dwk = dwk;
+  return from_cuda(lte::qk_norm_backward(n, as_stream(stream)));
 }
 
 }  // extern "C"

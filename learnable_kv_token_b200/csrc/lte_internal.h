@@ -124,4 +124,35 @@ cudaError_t gla_decode(int B, int H, int dk, int dv, int dtype, const void* q, c
                        const void* v, const float* a, void* o, float* state,
                        cudaStream_t stream);
 
+// qk_norm.cu
+struct QkNormArgs {
+  int B, T, H[2], D, dtype, grad_dtype, kind, rot, inter, n_pos;
+  float eps;
+  const void *x[2], *dy[2];   // q, k; gradients of the outputs (backward)
+  void* y[2];                 // q', k' or dq, dk (contiguous)
+  Strides4 xs[2], ds[2];
+  const float *w[2], *table;
+  const int32_t* pos;
+  float *part, *dwq, *dwk;    // backward: workspace, weight gradients
+};
+size_t qk_norm_backward_bytes(int B, int T, int Hq, int Hkv, int D);
+cudaError_t qk_norm(const QkNormArgs& n, cudaStream_t stream);
+cudaError_t qk_norm_backward(const QkNormArgs& n, cudaStream_t stream);
+
+// delta.cu, delta_chunk.cu: the gated delta rule
+struct DeltaArgs {
+  const lte_gdr_dims* d;
+  const void *q, *k, *v;
+  Strides4 qs, ks, vs, os;
+  const float *g, *beta;
+  const int32_t* lens;
+  const float* s_in;          // NULL = zeros
+  void* o;
+  float* s_out;
+  void* scratch;              // workspace
+};
+cudaError_t delta_recurrent(const DeltaArgs& a, cudaStream_t stream);
+cudaError_t delta_step(const lte_gdr_dims* d, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, void* o, float* state, cudaStream_t stream);
+
 }  // namespace lte

@@ -1,12 +1,15 @@
 """Thin host-side helpers over the C ABI: allocate the caller-owned buffers
 (torch device memory) and chain the entry points of one LTE layer.
 
-Nothing here computes: prefill = lte_score (when a CNN is given) ->
-lte_evict_compact -> lte_sparse_attn_prefill; a decode step is one
-lte_decode_step call on a DecodeCache.
+Nothing here computes: prefill = lte_qk_norm_rope (when a norm is given) ->
+lte_score (when a CNN is given) -> lte_evict_compact -> lte_sparse_attn_prefill;
+a decode step is one lte_decode_step call on a DecodeCache, behind an
+lte_qk_norm_rope call when the decoder has a norm.  The delta-rule layer of a
+hybrid is delta_prefill, delta_step and delta_backward.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -48,6 +51,8 @@ class PrefillOut:
     v_col: torch.Tensor
     n_scored: int
     death: torch.Tensor | None = None      # retained lifetimes (LTE_CAP_LOWEST)
+    q: torch.Tensor | None = None          # the normed, rotated q and k that were attended
+    k: torch.Tensor | None = None          # (prefill with a norm): cache set-up and backward take these
 
 
 class PrefillBuffers:
@@ -72,11 +77,15 @@ class PrefillBuffers:
 
 
 def prefill(q, k, v, p: LayerParams, mask=None, cnn=None, bufs: PrefillBuffers | None = None,
-            stream=None, scores=None) -> PrefillOut:
+            stream=None, scores=None, norm: QKNorm | None = None, positions=None) -> PrefillOut:
     """One LTE layer prefill.  Either a fed retention `mask` [B,Hkv,T] (uint8),
     fed `scores` [B,Hkv,T] (fp32, retained iff >= tau), or `cnn` = (w1, b1,
     w2, b2) device tensors for live scoring.  LTE_CAP_LOWEST needs scores
-    (fed or live): they rank the retained tokens."""
+    (fed or live): they rank the retained tokens.  `norm`: q and k go through
+    qk_norm_rope first (`positions` [B,T] int32, default 0 .. T-1); the result's
+    q and k are what was scored and attended."""
+    if norm is not None:
+        q, k = qk_norm_rope(q, k, norm, positions=positions, stream=stream)
     B, T, Hq, D = q.shape
     Hkv = k.shape[2]
     dims = p.dims(B, T, Hq, Hkv, D, q.dtype)
@@ -108,7 +117,8 @@ def prefill(q, k, v, p: LayerParams, mask=None, cnn=None, bufs: PrefillBuffers |
                               bufs.ws, stream, death=bufs.death if lowest else None)
     return PrefillOut(bufs.o, bufs.lse, r, bufs.mask if cnn is not None else mask, bufs.idx,
                       bufs.nret, bufs.cnt, bufs.k_col, bufs.v_col, n_scored,
-                      bufs.death if lowest else None)
+                      bufs.death if lowest else None,
+                      *((q, k) if norm is not None else (None, None)))
 
 
 def prefill_relaxed(q, k, v, out: PrefillOut, r, p: LayerParams, stream=None):
@@ -225,9 +235,12 @@ class DecodeCache:
 
 
 class Decoder:
-    """Runs lte_decode_step with fixed output buffers (graph-capturable)."""
+    """Runs lte_decode_step with fixed output buffers (graph-capturable).
+    norm: every step's q_t and k_t go through qk_norm_rope first."""
 
-    def __init__(self, dims, cnn, past1, past2, cache: DecodeCache, score_batch, device="cuda"):
+    def __init__(self, dims, cnn, past1, past2, cache: DecodeCache, score_batch, device="cuda",
+                 norm: QKNorm | None = None):
+        self.norm = norm
         self.dims = dims
         w1, b1, w2, b2 = cnn
         self.cnn, self._keep = L.make_cnn(w1, b1, w2, b2, past1, past2)
@@ -240,7 +253,14 @@ class Decoder:
         ws = L.lte_workspace_bytes(dims, L.LTE_WS_DECODE)
         self.ws = torch.zeros((ws + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
-    def step(self, q_t, k_t, v_t, stream=None):
+    def step(self, q_t, k_t, v_t, stream=None, positions=None):
+        """positions [B] int32: the tokens' positions (a norm with rotation)."""
+        if self.norm is not None:
+            if self.norm.rot_dim and positions is None:
+                raise ValueError("a rotation needs the tokens' positions")
+            pos = None if positions is None else positions[:, None]
+            q_t, k_t = (x[:, 0] for x in qk_norm_rope(q_t[:, None], k_t[:, None], self.norm,
+                                                      positions=pos, stream=stream))
         L.lte_decode_step(self.dims, self.cnn, self.cache.struct, q_t, k_t, v_t, self.o, self.lse,
                           self.score_batch, self.ws, stream)
         return self.o, self.lse
@@ -248,6 +268,171 @@ class Decoder:
     def device_error(self, stream=None):
         """(code, where) of this decoder's workspace error word (synchronises)."""
         return L.lte_read_device_error(self.ws, stream)
+
+
+# ---------------------------------------------------------------- q, k norms and rotation
+@dataclass
+class QKNorm:
+    """Norm of every query and key head, then the rotation by position: kind "rms", "l2" or
+    "none"; wq, wk fp32 [D] or None (ones); table from rope_table when rot_dim > 0."""
+    kind: str = "rms"
+    eps: float = 1e-6
+    wq: torch.Tensor | None = None
+    wk: torch.Tensor | None = None
+    rot_dim: int = 0
+    interleaved: bool = False
+    table: torch.Tensor | None = None
+
+    KINDS = {"none": L.LTE_NORM_NONE, "rms": L.LTE_NORM_RMS, "l2": L.LTE_NORM_L2}
+
+    def struct(self, q, k) -> L.lte_qk_norm:
+        B, T, Hq, D = q.shape
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != D or k.dtype != q.dtype:
+            raise ValueError("q [B,T,Hq,D] and k [B,T,Hkv,D] of one dtype")
+        if self.kind not in self.KINDS:
+            raise ValueError(f"kind is one of {tuple(self.KINDS)}")
+        for w in (self.wq, self.wk):
+            if w is not None:
+                _check(w, "norm weight", (D,), torch.float32, q.device)
+        if self.rot_dim:
+            if self.table is None:
+                raise ValueError("a rotation needs a table (rope_table)")
+            _check(self.table, "table", (self.table.shape[0], self.rot_dim), torch.float32, q.device)
+        return L.make_qk_norm(B, T, Hq, k.shape[2], D, q.dtype, self.KINDS[self.kind], self.eps,
+                              self.rot_dim, self.interleaved, self.wq, self.wk,
+                              self.table if self.rot_dim else None)
+
+
+def rope_table(n_pos, rot_dim, base=10000.0, device="cuda") -> torch.Tensor:
+    """fp32 [n_pos, rot_dim]: cos(p base^(-2i/rot_dim)), then the sines, i < rot_dim / 2.  The
+    angles are formed in 64 bits, so far positions keep their phase."""
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / max(rot_dim, 1))
+    ang = torch.arange(n_pos, dtype=torch.float64)[:, None] * f
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(device)
+
+
+def _check(t, name, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+@contextlib.contextmanager
+def _on(t, stream):
+    """The device of t, and `stream` (default: that device's current stream) for the launches and
+    for the memory that they use."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is not None and stream.device != t.device:
+        raise ValueError("the stream and the tensors are on different devices")
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield torch.cuda.current_stream()
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def qk_norm_rope(q, k, p: QKNorm, positions=None, q_out=None, k_out=None, stream=None):
+    """Normed and rotated q [B,T,Hq,D] and k [B,T,Hkv,D] (bf16 or fp32; strided views with
+    contiguous channels are fine).  positions: int32 [B,T], default 0 .. T-1."""
+    with _on(q, stream) as st:
+        c = p.struct(q, k)
+        if k.device != q.device:
+            raise ValueError("q and k are on different devices")
+        if positions is not None:
+            _check(positions, "positions", q.shape[:2], torch.int32, q.device)
+        outs = []
+        for x, y in ((q, q_out), (k, k_out)):
+            if y is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            else:
+                _check(y, "output", x.shape, x.dtype, x.device)
+            outs.append(y)
+        L.lte_qk_norm_rope(c, q, k, *outs, positions, st)
+    return tuple(outs)
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, p: QKNorm, positions=None, stream=None):
+    """Gradients through qk_norm_rope for those of its outputs (fp32, as the attention backward
+    gives them, or q's dtype): dq, dk in q's dtype and dwq, dwk fp32 [D] (None without a weight)."""
+    with _on(q, stream) as st:
+        c = p.struct(q, k)
+        if k.device != q.device:
+            raise ValueError("q and k are on different devices")
+        if positions is not None:
+            _check(positions, "positions", q.shape[:2], torch.int32, q.device)
+        if dq_out.dtype not in (torch.float32, q.dtype):
+            raise ValueError("gradients are fp32 or of q's dtype")
+        _check(dq_out, "dq_out", q.shape, dq_out.dtype, q.device)
+        _check(dk_out, "dk_out", k.shape, dq_out.dtype, q.device)
+        dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+        normed = p.kind != "none"
+        dwq, dwk = (torch.empty_like(w) if normed and w is not None else None for w in (p.wq, p.wk))
+        ws = torch.empty(L.lte_qk_norm_backward_workspace_bytes(c), dtype=torch.uint8, device=q.device)
+        L.lte_qk_norm_rope_backward(c, q, k, dq_out, dk_out, dq, dk, dwq, dwk, ws, positions, st)
+    return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------- gated delta rule
+def _delta_dims(q, k, v, scale):
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    if k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+        raise ValueError("q, k [B,T,Hk,dk] and v [B,T,H,dv]")
+    if not (q.dtype == k.dtype == v.dtype) or not (q.device == k.device == v.device):
+        raise ValueError("q, k and v share dtype and device")
+    return L.make_gdr_dims(B, T, H, Hk, dk, dv, dk ** -0.5 if scale is None else scale, q.dtype)
+
+
+def _delta_gates(v, g, beta, lens):
+    for t, name in ((g, "g"), (beta, "beta")):
+        _check(t, name, v.shape[:3], torch.float32, v.device)
+    if lens is not None:
+        _check(lens, "lens", v.shape[:1], torch.int32, v.device)
+
+
+def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out=None, stream=None):
+    """The gated delta rule over T tokens: q, k [B,T,Hk,dk], v [B,T,H,dv] (bf16 or fp32, strided
+    views with contiguous channels are fine), g (log decay, <= 0) and beta fp32 [B,T,H], state
+    fp32 [B,H,dv,dk] (default zeros), lens int32 [B]: sequence b has lens[b] tokens; the rows of o
+    behind them are zero.  scale defaults to dk^-1/2.  Returns o and the state after the last
+    token (in state_out, which may be `state`; by default a new tensor)."""
+    with _on(q, stream) as st:
+        d = _delta_dims(q, k, v, scale)
+        _delta_gates(v, g, beta, lens)
+        B, T, H, dv = v.shape
+        shape = (B, H, dv, q.shape[3])
+        if state is not None:
+            _check(state, "state", shape, torch.float32, q.device)
+        if state_out is None:
+            state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        else:
+            _check(state_out, "state_out", shape, torch.float32, q.device)
+        make = torch.empty if lens is None else torch.zeros
+        o = make(v.shape, dtype=v.dtype, device=v.device)
+        ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL), dtype=torch.uint8, device=q.device)
+        L.lte_gdr_prefill(d, q, k, v, g, beta, o, state_out, ws, state, lens, st)
+    return o, state_out
+
+
+def delta_step(q_t, k_t, v_t, g_t, beta_t, state, scale=None, out=None, stream=None):
+    """One token per sequence: q_t, k_t [B,Hk,dk], v_t [B,H,dv], g_t, beta_t fp32 [B,H]; `state`
+    is updated in place.  Returns o_t [B,H,dv]."""
+    with _on(q_t, stream) as st:
+        d = _delta_dims(q_t[:, None], k_t[:, None], v_t[:, None], scale)
+        B, H, dv = v_t.shape
+        _check(state, "state", (B, H, dv, q_t.shape[2]), torch.float32, q_t.device)
+        for t, name, shape, dt in ((q_t, "q_t", q_t.shape, q_t.dtype), (k_t, "k_t", q_t.shape, q_t.dtype),
+                                   (v_t, "v_t", v_t.shape, q_t.dtype), (g_t, "g_t", (B, H), torch.float32),
+                                   (beta_t, "beta_t", (B, H), torch.float32)):
+            _check(t, name, shape, dt, q_t.device)
+        if out is None:
+            out = torch.empty_like(v_t)
+        else:
+            _check(out, "out", v_t.shape, v_t.dtype, v_t.device)
+        L.lte_gdr_decode_step(d, q_t, k_t, v_t, g_t, beta_t, out, state, st)
+    return out
 
 
 class HostPrefill:

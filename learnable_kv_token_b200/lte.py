@@ -23,6 +23,8 @@ _lib = C.CDLL(LIB_PATH)
 LTE_F32, LTE_BF16 = 0, 1
 LTE_CAP_RECENT, LTE_CAP_FIRST, LTE_CAP_LOWEST = 0, 1, 2
 LTE_WS_PREFILL, LTE_WS_DECODE, LTE_WS_BACKWARD, LTE_WS_RELAXED = 0, 1, 2, 3
+LTE_GDR_WS_PREFILL, LTE_GDR_WS_BACKWARD = 0, 1
+LTE_NORM_NONE, LTE_NORM_RMS, LTE_NORM_L2 = 0, 1, 2
 LTE_KERNEL_TCGEN05, LTE_KERNEL_MMA_SYNC, LTE_KERNEL_SIMT = 1, 2, 3
 STATUS = {0: "LTE_OK", 1: "LTE_ERR_INVALID_ARG", 2: "LTE_ERR_UNSUPPORTED", 3: "LTE_ERR_CUDA",
           4: "LTE_ERR_TIMEOUT", 5: "LTE_ERR_WORKSPACE", 6: "LTE_ERR_DEVICE"}
@@ -54,6 +56,18 @@ class lte_cnn(C.Structure):
 class lte_cache(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("pos", C.c_void_p), ("win_r", C.c_void_p),
                 ("ret_total", C.c_void_p), ("meta", C.c_void_p), ("ret_r", C.c_void_p)]
+
+
+class lte_gdr_dims(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("H", C.c_int32), ("Hk", C.c_int32),
+                ("dk", C.c_int32), ("dv", C.c_int32), ("scale", C.c_float), ("dtype", C.c_int32)]
+
+
+class lte_qk_norm(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32),
+                ("D", C.c_int32), ("dtype", C.c_int32), ("kind", C.c_int32), ("eps", C.c_float),
+                ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("n_pos", C.c_int32),
+                ("wq", C.c_void_p), ("wk", C.c_void_p), ("table", C.c_void_p)]
 
 
 _P = C.c_void_p
@@ -88,6 +102,12 @@ _SIG = {
     "lte_wait_probe": [_P, _I, C.c_int64, _P, _P],
     "lte_gla_prefill": [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
     "lte_gla_decode_step": [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
+    "lte_gdr_prefill": [C.POINTER(lte_gdr_dims), _P, _P, _P] + [C.POINTER(lte_strides)] * 3
+                       + [_P] * 5 + [C.POINTER(lte_strides), _P, _P, C.c_size_t, _P],
+    "lte_gdr_decode_step": [C.POINTER(lte_gdr_dims)] + [_P] * 8,
+    "lte_qk_norm_rope": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2 + [_P] * 4,
+    "lte_qk_norm_rope_backward": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2
+                                 + [_P] * 3 + [_I] + [_P] * 5 + [C.c_size_t, _P],
 }
 for _name, _args in _SIG.items():
     _f = getattr(_lib, _name)
@@ -97,10 +117,16 @@ _lib.lte_workspace_bytes.argtypes = [C.POINTER(lte_dims), _I]
 _lib.lte_workspace_bytes.restype = C.c_size_t
 _lib.lte_score_backward_workspace_bytes.argtypes = [C.POINTER(lte_dims), C.POINTER(lte_cnn)]
 _lib.lte_score_backward_workspace_bytes.restype = C.c_size_t
+_lib.lte_gdr_workspace_bytes.argtypes = [C.POINTER(lte_gdr_dims), _I]
+_lib.lte_gdr_workspace_bytes.restype = C.c_size_t
+_lib.lte_qk_norm_backward_workspace_bytes.argtypes = [C.POINTER(lte_qk_norm)]
+_lib.lte_qk_norm_backward_workspace_bytes.restype = C.c_size_t
 _lib.lte_version.argtypes = []
 _lib.lte_version.restype = C.c_char_p
 
-EXPORTED = tuple(_SIG) + ("lte_workspace_bytes", "lte_score_backward_workspace_bytes", "lte_version")
+EXPORTED = tuple(_SIG) + ("lte_workspace_bytes", "lte_score_backward_workspace_bytes",
+                         "lte_gdr_workspace_bytes", "lte_qk_norm_backward_workspace_bytes",
+                         "lte_version")
 
 
 def _call(name, *args):
@@ -295,3 +321,52 @@ def lte_gla_decode_step(q_t, k_t, v_t, a_t, o_t, state, stream=None):
     dv = v_t.shape[2]
     _call("lte_gla_decode_step", B, H, dk, dv, dtype_code(q_t.dtype), _ptr(q_t), _ptr(k_t),
           _ptr(v_t), _ptr(a_t), _ptr(o_t), _ptr(state), _stream(stream))
+
+
+def make_gdr_dims(B, T, H, Hk, dk, dv, scale, dtype) -> lte_gdr_dims:
+    return lte_gdr_dims(B, T, H, Hk, dk, dv, float(scale),
+                        dtype_code(dtype) if isinstance(dtype, torch.dtype) else int(dtype))
+
+
+def lte_gdr_workspace_bytes(dims: lte_gdr_dims, which: int) -> int:
+    return int(_lib.lte_gdr_workspace_bytes(C.byref(dims), which))
+
+
+def lte_gdr_prefill(dims, q, k, v, g, beta, o, state_out, workspace, state_in=None, lens=None,
+                    stream=None):
+    _call("lte_gdr_prefill", C.byref(dims), _ptr(q), _ptr(k), _ptr(v), C.byref(_strides(q)),
+          C.byref(_strides(k)), C.byref(_strides(v)), _ptr(g), _ptr(beta), _ptr(lens),
+          _ptr(state_in), _ptr(o), C.byref(_strides(o)), _ptr(state_out), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def lte_gdr_decode_step(dims, q_t, k_t, v_t, g_t, beta_t, o_t, state, stream=None):
+    _call("lte_gdr_decode_step", C.byref(dims), _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(g_t),
+          _ptr(beta_t), _ptr(o_t), _ptr(state), _stream(stream))
+
+
+def make_qk_norm(B, T, Hq, Hkv, D, dtype, kind, eps, rot_dim=0, interleaved=False, wq=None,
+                 wk=None, table=None) -> lte_qk_norm:
+    """lte_qk_norm over device tensors wq, wk [D] and table [n_pos, rot_dim]
+    (fp32, contiguous; the caller keeps them alive)."""
+    ptr = (lambda t: None if t is None else t.data_ptr())
+    return lte_qk_norm(B, T, Hq, Hkv, D, dtype_code(dtype), int(kind), float(eps), rot_dim,
+                       int(interleaved), 0 if table is None else table.shape[0], ptr(wq), ptr(wk),
+                       ptr(table))
+
+
+def lte_qk_norm_rope(norm, q, k, q_out, k_out, positions=None, stream=None):
+    _call("lte_qk_norm_rope", C.byref(norm), _ptr(q), _ptr(k), C.byref(_strides(q)),
+          C.byref(_strides(k)), _ptr(positions), _ptr(q_out), _ptr(k_out), _stream(stream))
+
+
+def lte_qk_norm_backward_workspace_bytes(norm) -> int:
+    return int(_lib.lte_qk_norm_backward_workspace_bytes(C.byref(norm)))
+
+
+def lte_qk_norm_rope_backward(norm, q, k, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                              positions=None, stream=None):
+    _call("lte_qk_norm_rope_backward", C.byref(norm), _ptr(q), _ptr(k), C.byref(_strides(q)),
+          C.byref(_strides(k)), _ptr(positions), _ptr(dq_out), _ptr(dk_out),
+          dtype_code(dq_out.dtype), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream(stream))

@@ -1,0 +1,241 @@
+"""GPU parity of the gated delta rule (prompt, step, gradients) with the float64 oracle.
+
+Tolerances, as the 2-norm of the error over the 2-norm of the reference:
+ - fp32 arithmetic (fp32 inputs, the step, few tokens): a token rounds every state entry about
+   dk + 8 times (the dot product, the update), each by at most 2^-24, independent from token to
+   token: 2^-24 (dk + 8) sqrt(T).
+ - bf16 prompts, fp32 outputs (states, gate gradients): a product with one or both operands as bf16
+   hi + lo pairs is off by at most (2^-8)^2 per split operand; the states pass three such products
+   per chunk (S k, T r, u k^T) with five split operands between them, random in sign from entry to
+   entry, so by less than their root sum: sqrt(5) 2^-16 = 3.4e-5 at most, and a third of it at the
+   rounding's mean size (2^-8 / sqrt(3) per split): 1.2e-5.  The bound taken is 2e-5.  Gradients of
+   the gates pass the chain twice, forwards and backwards: 4e-5.
+ - bf16 outputs: rounded once (at most 2^-8), behind products that round one operand to bf16 (at
+   most 2^-8, independent): sqrt(2) 2^-8; gradients of q and k sum four such terms behind products
+   of two rounded operands: sqrt(3) 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import delta_oracle as DO
+
+pytestmark = pytest.mark.gpu
+
+STATE_TOL, GATE_TOL = 2e-5, 4e-5
+BF16_TOL, GRAD_TOL = 2 ** 0.5 * 2.0 ** -8, 3 ** 0.5 * 2.0 ** -8
+
+
+def tol32(T, dk):
+    return 2.0 ** -24 * (dk + 8) * T ** 0.5
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def rel(got, ref):
+    n = np.linalg.norm(ref)
+    d = np.linalg.norm(f64(got) - ref)
+    return d / n if n else d
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from learnable_kv_token_b200 import layer
+    return layer
+
+
+def inputs(seed, B, T, H, Hk, dk, dv, dtype=torch.bfloat16, init=True, lens=None, fused=False):
+    """Unit keys; each head has its own pace; on the device.  Rows behind `lens` hold NaN."""
+    g = torch.Generator().manual_seed(seed)
+    randn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    q, k, v = randn(B, T, Hk, dk), randn(B, T, Hk, dk), randn(B, T, H, dv)
+    q, k = (x / x.norm(dim=-1, keepdim=True) for x in (q, k))
+    gate = -torch.exp(torch.linspace(-1.2, -8, H)) * torch.nn.functional.softplus(1 + randn(B, T, H))
+    beta = torch.sigmoid(randn(B, T, H))
+    S0 = 0.3 * randn(B, H, dv, dk) if init else None
+    if lens is not None:
+        for i, n in enumerate(lens):
+            for x in (q, k, v, gate, beta):
+                x[i, n:] = float("nan")
+        lens = torch.tensor(lens, dtype=torch.int32).cuda()
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    if fused:
+        flat = torch.cat([x.reshape(B, T, -1) for x in (q, k, v)], 2).cuda()
+        q, k, v = (x.unflatten(2, (-1, d)) for x, d in zip(flat.split([Hk * dk, Hk * dk, H * dv], 2), (dk, dk, dv)))
+    return dict(q=q.cuda(), k=k.cuda(), v=v.cuda(), g=gate.cuda(), beta=beta.cuda(),
+                state=None if S0 is None else S0.cuda(), lens=lens)
+
+
+def oracle(x, scale=None):
+    return DO.delta(f64(x["q"]), f64(x["k"]), f64(x["v"]), f64(x["g"]), f64(x["beta"]), f64(x["state"]),
+                    None if x["lens"] is None else x["lens"].cpu().numpy(), scale)
+
+
+def check_prefill(layer, x, scale=None):
+    o, S = layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"], lens=x["lens"],
+                               scale=scale)
+    torch.cuda.synchronize()
+    o_ref, S_ref = oracle(x, scale)
+    T, dk = x["q"].shape[1], x["q"].shape[3]
+    bf16 = x["q"].dtype == torch.bfloat16
+    assert torch.isfinite(o).all() and torch.isfinite(S).all()
+    assert rel(S, S_ref) <= max(tol32(T, dk), STATE_TOL if bf16 else 0)
+    assert rel(o, o_ref) <= (BF16_TOL if bf16 else tol32(T, dk))
+    if x["lens"] is not None:
+        for i, n in enumerate(x["lens"].tolist()):
+            assert (o[i, n:] == 0).all()
+    return o, S
+
+
+SHAPES = [(2, 1, 2, 2, 64, 64), (1, 5, 4, 1, 128, 128), (2, 17, 4, 2, 64, 128), (1, 63, 2, 2, 128, 64),
+          (3, 64, 2, 1, 128, 128), (1, 65, 8, 8, 64, 64), (2, 200, 4, 4, 128, 128), (1, 333, 2, 1, 64, 128)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_prefill(layer, dtype, shape):
+    check_prefill(layer, inputs(sum(shape), *shape, dtype=dtype, init=shape[1] % 2 == 1))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[0, 1, 130], [64, 130, 63], [129, 0, 65]], ids=str)
+def test_prefill_padded_batch(layer, dtype, lens):
+    """Rows behind a sequence hold NaN and are not read; a sequence of no tokens keeps its state."""
+    x = inputs(9, 3, 130, 4, 2, 128, 128, dtype=dtype, lens=lens, fused=True)
+    _, S = check_prefill(layer, x)
+    for i, n in enumerate(lens):
+        if n == 0:
+            assert torch.equal(S[i], x["state"][i])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["same-key", "beta-0", "beta-1", "beta-2", "forget", "forget-all", "no-decay",
+                                  "scaled", "zero-key"])
+def test_prefill_extreme_gates(layer, dtype, kind):
+    x = inputs(21, 2, 150, 4, 2, 128, 128, dtype=dtype)
+    scale = None
+    if kind == "same-key":                     # every token writes under one key: the chunk's system is dense
+        x["k"][:] = x["k"][:, :1].clone()
+        x["beta"][:] = 0.9
+    elif kind.startswith("beta"):
+        x["beta"][:] = float(kind[-1])
+        if kind == "beta-2":                   # reflections: the state keeps its size
+            x["g"][:] = -0.01
+    elif kind == "forget":                     # resets inside a chunk, some of them exact
+        x["g"][:, 10::37] = -30.0
+        x["g"][:, 70] = float("-inf")
+    elif kind == "forget-all":
+        x["g"][:] = float("-inf")
+    elif kind == "no-decay":
+        x["g"][:] = 0.0
+    elif kind == "zero-key":
+        x["k"][:, ::3] = 0
+    else:
+        scale = 1.5
+    check_prefill(layer, x, scale)
+
+
+def test_prefill_continues(layer):
+    """A prompt in three calls, in place on one state, equals the prompt in one call."""
+    x = inputs(4, 2, 300, 4, 4, 128, 128)
+    o, S = check_prefill(layer, x)
+    st, parts = x["state"].clone(), []
+    for a, b in ((0, 100), (100, 103), (103, 300)):
+        part, _ = layer.delta_prefill(x["q"][:, a:b], x["k"][:, a:b], x["v"][:, a:b],
+                                      x["g"][:, a:b].contiguous(), x["beta"][:, a:b].contiguous(), state=st,
+                                      state_out=st)
+        parts.append(part)
+    assert rel(st, f64(S)) <= 2 * STATE_TOL
+    assert rel(torch.cat(parts, 1), f64(o)) <= 2 * BF16_TOL
+
+
+def test_prefill_repeats(layer):
+    x = inputs(5, 3, 190, 4, 2, 64, 128, lens=[190, 3, 100])
+    a, b = (layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"], lens=x["lens"])
+            for _ in range(2))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(1, 2, 1, 64, 64), (3, 4, 2, 128, 64), (5, 16, 16, 64, 128), (2, 6, 2, 128, 128)],
+                         ids=str)
+def test_step(layer, dtype, shape):
+    B, H, Hk, dk, dv = shape
+    T = 6
+    x = inputs(30 + B, B, T, H, Hk, dk, dv, dtype=dtype)
+    x["g"][:, 3] = float("-inf")
+    o_ref, S_ref = oracle(x)
+    st = x["state"].clone()
+    for t in range(T):
+        o = layer.delta_step(*(x[n][:, t].contiguous() for n in ("q", "k", "v", "g", "beta")), st)
+        assert rel(o, o_ref[:, t]) <= (tol32(T, dk) if dtype == torch.float32 else 2.0 ** -8)
+    assert rel(st, S_ref) <= tol32(T, dk)
+
+
+def test_step_in_a_graph(layer):
+    """A captured step, replayed with new inputs in its buffers, goes on from the state."""
+    B, H, D, T = 4, 8, 128, 5
+    x = inputs(77, B, T, H, H, D, D)
+    buf = {n: x[n][:, 0].clone() for n in ("q", "k", "v", "g", "beta")}
+    st, out = x["state"].clone(), torch.empty(B, H, D, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.delta_step(*buf.values(), st.clone(), out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.delta_step(*buf.values(), st, out=out)
+    o_ref, S_ref = oracle(x)
+    for t in range(T):
+        for n in buf:
+            buf[n].copy_(x[n][:, t])
+        graph.replay()
+        assert rel(out, o_ref[:, t]) <= 2.0 ** -8
+    assert rel(st, S_ref) <= tol32(T, D)
+
+
+def test_prefill_on_another_stream_and_in_graphs(layer):
+    """The workspace belongs to the call: two captured prompts and one on a side stream do not disturb
+    one another."""
+    xs = [inputs(50 + i, 2, 130 + 70 * i, 4, 4, 128, 128) for i in range(2)]
+    want = [layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"]) for x in xs]
+    graphs, got = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"]))
+        graphs.append(graph)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        x = xs[0]
+        o, S = layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"], stream=side)
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0][0]) and torch.equal(S, want[0][1])
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_refusals(layer):
+    x = inputs(1, 1, 8, 2, 2, 64, 64)
+    call = lambda **c: layer.delta_prefill(**{**{n: x[n] for n in ("q", "k", "v", "g", "beta", "state")}, **c})  # noqa: E731
+    bad = [dict(g=x["g"].bfloat16()), dict(beta=x["beta"][:, :4]), dict(k=x["k"][:, :4]), dict(q=x["q"].float()),
+           dict(state=x["state"].bfloat16()), dict(lens=torch.tensor([8])), dict(g=x["g"].cpu()),
+           dict(q=x["q"].transpose(2, 3).contiguous().transpose(2, 3)), dict(state=x["state"][..., :32])]
+    for c in bad:
+        with pytest.raises(ValueError):
+            call(**c)
+    y = inputs(1, 1, 8, 3, 2, 64, 64)                          # 3 value heads, 2 key heads
+    with pytest.raises(layer.L.LteError) as e:
+        layer.delta_prefill(y["q"], y["k"], y["v"], y["g"], y["beta"])
+    assert e.value.status == 1
+    z = torch.zeros(1, 8, 2, 32, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(layer.L.LteError) as e:
+        layer.delta_prefill(z, z, z, x["g"], x["beta"])
+    assert e.value.status == 2
+    with pytest.raises(ValueError):
+        layer.delta_step(x["q"][:, 0], x["k"][:, 0], x["v"][:, 0], x["g"][:, 0], x["beta"][:, 0], None or x["g"])
