@@ -1,0 +1,130 @@
+// The chunk form of the gated delta rule and what its kernels share.
+//
+// Within a chunk of L = 64 tokens, with G_t = sum_{i<=t} g_i from its first
+// token on and S_0 the state before it, the corrections u_t = b_t (v_t - a_t
+// S_{t-1} k_t) solve a unit lower triangular system:
+//   (I + M) U = diag(b) R,   M_ts = b_t e^{G_t - G_s} k_t.k_s  (s < t),
+//   R = V - diag(e^G) K S_0^T,
+// so with T = (I + M)^{-1} diag(b):
+//   U   = T R
+//   O   = scale diag(e^G) Q S_0^T + A U,  A_ts = scale e^{G_t - G_s} q_t.k_s  (s <= t)
+//   S_L = e^{G_L} S_0 + U^T diag(e^{G_L - G}) K.
+// T and A depend on no state: one launch computes them for every chunk at
+// once (delta_prepare_kernel).  Every exponent is a difference taken forwards
+// in time, so with g <= 0 no factor exceeds 1, whatever the decay.
+//
+// Precision.  q, k, v and their gradients are bf16, exact as operands.  Where a
+// state or a correction is an operand of a product that feeds the state, it
+// goes in as a bf16 pair hi + lo (two products; relative error about 2^-17),
+// so the fp32 state keeps fp32-like accuracy on the bf16 tensor path.
+#pragma once
+
+#include "lte_common.cuh"
+#include "lte_internal.h"
+#include "mma_sync.cuh"
+
+namespace lte {
+namespace delta {
+
+constexpr int L = 64;
+// up to this many tokens the recurrent kernel runs instead of the chunk form
+constexpr int kFewTokens = 16;
+
+// Per-chunk record in the workspace: T as hi and lo, A as hi (and lo, for the
+// gradients), each a [64][64] bf16 image in the swizzled order in which it lies
+// in shared memory, then five rows of 64 floats.
+constexpr int kImg = L * L * 2;
+constexpr int kScal = 5 * L * 4;
+constexpr int kEG = 0, kLam = 1, kBeta = 2, kGhi = 3, kGlo = 4;   // e^G, e^{G_L - G}, b, G as a float pair
+__host__ __device__ constexpr int rec_bytes(bool a_lo) { return (a_lo ? 4 : 3) * kImg + kScal; }
+
+// A correction of b = 0 is exactly zero; it is carried as u = 2^-60 e instead,
+// far below what fp32 sums beside it can see, so that e = u / b always exists
+// (the gradient of b is y.e).
+__device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-60f ? 0x1p-60f : b; }
+
+// Order of 16-byte pieces in a tile of `16 * W` columns of 2 bytes: the eight
+// rows that one ldmatrix reads lie in eight different bank groups.
+template <int W>
+__device__ __forceinline__ uint32_t swz_cols(int r, int c) {
+  if (W >= 4) return (uint32_t)(r * 32 * W + ((c ^ (r & 7)) << 4));
+  if (W == 2) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// (x0, x1) as bf16 pairs: hi rounded to nearest, lo the rounded remainder
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  lo = pack_bf16(x0 - bf_lo(hi), x1 - bf_hi(hi));
+}
+// accumulator tiles c0, c1 (columns 16 kk .. + 7, + 8 .. + 15) as the A operand of k-step kk
+__device__ __forceinline__ void split_a(const float* c0, const float* c1, uint32_t* hi, uint32_t* lo) {
+  split2(c0[0], c0[1], hi[0], lo[0]);
+  split2(c0[2], c0[3], hi[1], lo[1]);
+  split2(c1[0], c1[1], hi[2], lo[2]);
+  split2(c1[2], c1[3], hi[3], lo[3]);
+}
+
+// B operand pair from [n][k] rows: n-tiles n0, n0 + 8 of k-step at 16-byte piece c
+__device__ __forceinline__ int ldn_row(int lane) { return (lane & 7) + ((lane >> 4) & 1) * 8; }
+__device__ __forceinline__ int ldn_col(int lane) { return (lane >> 3) & 1; }
+// B operand pair from [k][n] rows (transposed load): k-step rows, n-tiles at pieces c, c + 1
+__device__ __forceinline__ int ldt_row(int lane) { return (lane & 7) + ((lane >> 3) & 1) * 8; }
+__device__ __forceinline__ int ldt_col(int lane) { return (lane >> 4) & 1; }
+
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r0),
+               "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// rows [t0, t0 + 64) of a [T][D] tensor (row stride `ts`) -> a swizzled tile,
+// zeros from row `len` on
+template <int D, int THREADS>
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* src, long long ts, int t0, int len) {
+#pragma unroll
+  for (int i = threadIdx.x; i < L * (D / 8); i += THREADS) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const bool ok = t0 + r < len;
+    cp_async16(dst + swz<D>(r, c), src + (long long)(ok ? t0 + r : t0) * ts + c * 8, ok);
+  }
+}
+template <int BYTES, int THREADS>
+__device__ __forceinline__ void load_linear(uint32_t dst, const uint8_t* src) {
+  for (int i = threadIdx.x; i < BYTES / 16; i += THREADS) cp_async16(dst + i * 16, src + i * 16, true);
+}
+
+__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
+  return lens == nullptr ? T : min(max(lens[b], 0), T);
+}
+
+// Images of [rows][cols] bf16 in blocks of 8 x 8 (128 bytes: row g at 16 g): an
+// accumulator register of a warp is one block, so a warp stores and loads it as
+// 32 consecutive words, and ldmatrix reads blocks without bank conflicts.
+__device__ __forceinline__ long long block_word(int rb, int cb, int cbs, int lane) {
+  return ((long long)rb * cbs + cb) * 32 + lane;
+}
+
+struct ChunkArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  Strides4 qs, ks, vs, os;
+  const float *g, *beta;
+  const int32_t* lens;
+  const float* s_in;
+  float* s_out;
+  __nv_bfloat16* o;
+  uint8_t* rec;          // [units][chunks] records
+  uint32_t *s0, *u;      // images of S_0 (hi, lo) and U (hi, lo) per chunk, for the gradients
+  int T, H, Hk, dv, chunks;
+  float scale;
+};
+
+// delta_chunk.cu
+cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t stream);
+// the chain of states; with s0 and u, writes their images instead of o
+cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
+
+}  // namespace delta
+}  // namespace lte

@@ -552,7 +552,7 @@ lte_status lte_gla_decode_step(int32_t B, int32_t H, int32_t dk, int32_t dv, int
 
 size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which) {
   if (check_gdr(d) != LTE_OK) return 0;
-  if (which == LTE_GDR_WS_PREFILL) return 16;
+  if (which == LTE_GDR_WS_PREFILL) return lte::delta_prefill_bytes(d);
   return 0;
 }
 
@@ -578,7 +578,7 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
     return LTE_ERR_WORKSPACE;
   a.d = d; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lens = lens;
   a.s_in = state_in; a.o = o; a.s_out = state_out; a.scratch = workspace;
-  return from_cuda(lte::delta_recurrent(a, as_stream(stream)));
+  return from_cuda(lte::delta_prefill(a, as_stream(stream)));
 }
 
 lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,

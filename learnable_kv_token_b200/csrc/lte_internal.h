@@ -152,6 +152,8 @@ struct DeltaArgs {
   void* scratch;              // workspace
 };
 cudaError_t delta_recurrent(const DeltaArgs& a, cudaStream_t stream);
+size_t delta_prefill_bytes(const lte_gdr_dims* d);
+cudaError_t delta_prefill(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t delta_step(const lte_gdr_dims* d, const void* q, const void* k, const void* v, const float* g,
                        const float* beta, void* o, float* state, cudaStream_t stream);
 
