@@ -534,6 +534,23 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
                            const lte_strides* o_strides, float* state_out, void* workspace,
                            size_t ws_bytes, void* stream);
 
+/* lte_gdr_backward -- gradients of lte_gdr_prefill for given dO (gradient of o)
+ * and dstate_out (gradient of the final state; nullable: zeros), from the
+ * forward's inputs (the states are computed again in the workspace).  dq, dk
+ * [B,T,Hk,dk] (summed over the value heads that share them) and dv [B,T,H,dv]:
+ * dtype, contiguous; dg, dbeta fp32 [B,T,H]; dstate_in (nullable) fp32
+ * [B,H,dv,dk].  Rows behind lens are left as they were.  dq, dk and dv are
+ * rounded once behind bf16 products with fp32 sums; dg, dbeta and dstate_in
+ * come from the hi + lo products of the forward.  bf16 only.  No atomics.
+ * Workspace: lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD). */
+lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
+                            const lte_strides* q_strides, const lte_strides* k_strides,
+                            const lte_strides* v_strides, const float* g, const float* beta,
+                            const int32_t* lens, const float* state_in, const void* dO,
+                            const lte_strides* do_strides, const float* dstate_out, void* dq,
+                            void* dk, void* dv, float* dg, float* dbeta, float* dstate_in,
+                            void* workspace, size_t ws_bytes, void* stream);
+
 /* lte_gdr_decode_step -- one token per sequence (d->T is ignored): q_t, k_t
  * [B,Hk,dk], v_t, o_t [B,H,dv], g_t, beta_t fp32 [B,H], all contiguous; state is
  * updated in place.  fp32 arithmetic for both dtypes. */

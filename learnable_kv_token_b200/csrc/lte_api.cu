@@ -553,6 +553,7 @@ lte_status lte_gla_decode_step(int32_t B, int32_t H, int32_t dk, int32_t dv, int
 size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which) {
   if (check_gdr(d) != LTE_OK) return 0;
   if (which == LTE_GDR_WS_PREFILL) return lte::delta_prefill_bytes(d);
+  if (which == LTE_GDR_WS_BACKWARD && d->dtype == LTE_BF16) return lte::delta_backward_bytes(d);
   return 0;
 }
 
@@ -579,6 +580,38 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
   a.d = d; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lens = lens;
   a.s_in = state_in; a.o = o; a.s_out = state_out; a.scratch = workspace;
   return from_cuda(lte::delta_prefill(a, as_stream(stream)));
+}
+
+lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
+                            const lte_strides* q_strides, const lte_strides* k_strides,
+                            const lte_strides* v_strides, const float* g, const float* beta,
+                            const int32_t* lens, const float* state_in, const void* dO,
+                            const lte_strides* do_strides, const float* dstate_out, void* dq,
+                            void* dk, void* dv, float* dg, float* dbeta, float* dstate_in,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  lte_status st = check_gdr(d);
+  if (st != LTE_OK) return st;
+  if (!q || !k || !v || !g || !beta || !dO || !dq || !dk || !dv || !dg || !dbeta)
+    return LTE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state_in) || !aligned16(dO) ||
+      !aligned16(dstate_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      !aligned16(dstate_in) || !aligned16(workspace))
+    return LTE_ERR_INVALID_ARG;
+  if (d->dtype != LTE_BF16) return LTE_ERR_UNSUPPORTED;
+  lte::DeltaArgs a{};
+  lte::DeltaGradArgs n{};
+  if ((st = strides_of(q_strides, d->T, d->Hk, d->dk, d->dtype, &a.qs)) != LTE_OK ||
+      (st = strides_of(k_strides, d->T, d->Hk, d->dk, d->dtype, &a.ks)) != LTE_OK ||
+      (st = strides_of(v_strides, d->T, d->H, d->dv, d->dtype, &a.vs)) != LTE_OK ||
+      (st = strides_of(do_strides, d->T, d->H, d->dv, d->dtype, &n.dos)) != LTE_OK)
+    return st;
+  if (workspace == nullptr || ws_bytes < lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD))
+    return LTE_ERR_WORKSPACE;
+  a.d = d; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lens = lens;
+  a.s_in = state_in; a.scratch = workspace;
+  n.dO = dO; n.ds_out = dstate_out; n.dq = dq; n.dk = dk; n.dv = dv;
+  n.dg = dg; n.db = dbeta; n.ds_in = dstate_in;
+  return from_cuda(lte::delta_backward(a, n, as_stream(stream)));
 }
 
 lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,

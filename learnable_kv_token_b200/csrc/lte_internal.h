@@ -154,6 +154,16 @@ struct DeltaArgs {
 cudaError_t delta_recurrent(const DeltaArgs& a, cudaStream_t stream);
 size_t delta_prefill_bytes(const lte_gdr_dims* d);
 cudaError_t delta_prefill(const DeltaArgs& a, cudaStream_t stream);
+// delta_backward.cu
+struct DeltaGradArgs {
+  const void* dO;
+  Strides4 dos;
+  const float* ds_out;        // NULL = zeros
+  void *dq, *dk, *dv;         // contiguous
+  float *dg, *db, *ds_in;
+};
+size_t delta_backward_bytes(const lte_gdr_dims* d);
+cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStream_t stream);
 cudaError_t delta_step(const lte_gdr_dims* d, const void* q, const void* k, const void* v, const float* g,
                        const float* beta, void* o, float* state, cudaStream_t stream);
 

@@ -416,6 +416,28 @@ def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out
     return o, state_out
 
 
+def delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lens=None, scale=None, stream=None):
+    """Gradients of delta_prefill (bf16) for the gradients `do` of o and `dstate` of the final state
+    (default zeros): dq, dk [B,T,Hk,dk], dv [B,T,H,dv] in bf16, dg, dbeta fp32 [B,T,H], and that of
+    the initial state, fp32 [B,H,dv,dk].  Rows behind `lens` are zero."""
+    with _on(q, stream) as st:
+        d = _delta_dims(q, k, v, scale)
+        _delta_gates(v, g, beta, lens)
+        B, T, H, dv = v.shape
+        shape = (B, H, dv, q.shape[3])
+        for t, name in ((state, "state"), (dstate, "dstate")):
+            if t is not None:
+                _check(t, name, shape, torch.float32, q.device)
+        if do.shape != v.shape or do.dtype != v.dtype or do.device != v.device:
+            raise ValueError("do has v's shape, dtype and device")
+        make = torch.empty if lens is None else torch.zeros
+        grads = [make(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v, g, beta)]
+        ds = torch.empty(shape, dtype=torch.float32, device=q.device)
+        ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD), dtype=torch.uint8, device=q.device)
+        L.lte_gdr_backward(d, q, k, v, g, beta, do, *grads, ws, state, lens, dstate, ds, st)
+    return (*grads, ds)
+
+
 def delta_step(q_t, k_t, v_t, g_t, beta_t, state, scale=None, out=None, stream=None):
     """One token per sequence: q_t, k_t [B,Hk,dk], v_t [B,H,dv], g_t, beta_t fp32 [B,H]; `state`
     is updated in place.  Returns o_t [B,H,dv]."""

@@ -104,6 +104,8 @@ _SIG = {
     "lte_gla_decode_step": [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P],
     "lte_gdr_prefill": [C.POINTER(lte_gdr_dims), _P, _P, _P] + [C.POINTER(lte_strides)] * 3
                        + [_P] * 5 + [C.POINTER(lte_strides), _P, _P, C.c_size_t, _P],
+    "lte_gdr_backward": [C.POINTER(lte_gdr_dims), _P, _P, _P] + [C.POINTER(lte_strides)] * 3
+                        + [_P] * 5 + [C.POINTER(lte_strides)] + [_P] * 8 + [C.c_size_t, _P],
     "lte_gdr_decode_step": [C.POINTER(lte_gdr_dims)] + [_P] * 8,
     "lte_qk_norm_rope": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2 + [_P] * 4,
     "lte_qk_norm_rope_backward": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2
@@ -337,6 +339,15 @@ def lte_gdr_prefill(dims, q, k, v, g, beta, o, state_out, workspace, state_in=No
     _call("lte_gdr_prefill", C.byref(dims), _ptr(q), _ptr(k), _ptr(v), C.byref(_strides(q)),
           C.byref(_strides(k)), C.byref(_strides(v)), _ptr(g), _ptr(beta), _ptr(lens),
           _ptr(state_in), _ptr(o), C.byref(_strides(o)), _ptr(state_out), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def lte_gdr_backward(dims, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, workspace, state_in=None,
+                     lens=None, dstate_out=None, dstate_in=None, stream=None):
+    _call("lte_gdr_backward", C.byref(dims), _ptr(q), _ptr(k), _ptr(v), C.byref(_strides(q)),
+          C.byref(_strides(k)), C.byref(_strides(v)), _ptr(g), _ptr(beta), _ptr(lens),
+          _ptr(state_in), _ptr(do), C.byref(_strides(do)), _ptr(dstate_out), _ptr(dq), _ptr(dk),
+          _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dstate_in), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream(stream))
 
 

@@ -157,6 +157,80 @@ def test_prefill_repeats(layer):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def check_backward(layer, x, dstate=True, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    do = torch.randn(x["v"].shape, generator=g).bfloat16().cuda()
+    B, T, H, dv = x["v"].shape
+    dS = torch.randn(B, H, dv, x["q"].shape[3], generator=g).cuda() * 0.2 if dstate else None
+    if x["lens"] is not None:
+        for i, n in enumerate(x["lens"].tolist()):
+            do[i, n:] = float("nan")
+    args = (x["q"], x["k"], x["v"], x["g"], x["beta"], do)
+    got = layer.delta_backward(*args, state=x["state"], dstate=dS, lens=x["lens"])
+    again = layer.delta_backward(*args, state=x["state"], dstate=dS, lens=x["lens"])
+    lens = None if x["lens"] is None else x["lens"].cpu().numpy()
+    ref = DO.delta_backward(*(f64(t) for t in args), f64(x["state"]), f64(dS), lens)
+    for a, b, r, name, tol in zip(got, again, ref, ("dq", "dk", "dv", "dg", "dbeta", "dstate"),
+                                  (GRAD_TOL, GRAD_TOL, BF16_TOL, GATE_TOL, GATE_TOL, STATE_TOL)):
+        assert torch.equal(a, b), name
+        assert torch.isfinite(a).all(), name
+        assert rel(a, r) <= tol, f"{name}: {rel(a, r):.3g} > {tol:.3g}"
+    if lens is not None:
+        for i, n in enumerate(lens):
+            assert all((t[i, n:] == 0).all() for t in got[:5])
+    return got
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(layer, shape):
+    check_backward(layer, inputs(100 + sum(shape), *shape, init=shape[1] % 2 == 1), dstate=shape[0] == 1)
+
+
+@pytest.mark.parametrize("lens", [[0, 1, 130], [64, 130, 63], [129, 0, 65]], ids=str)
+def test_backward_padded_batch(layer, lens):
+    x = inputs(10, 3, 130, 4, 2, 128, 128, lens=lens, fused=True)
+    check_backward(layer, x)
+
+
+@pytest.mark.parametrize("kind", ["same-key", "beta-0", "beta-1", "forget", "no-decay"])
+def test_backward_extreme_gates(layer, kind):
+    x = inputs(22, 2, 150, 4, 2, 128, 128)
+    if kind == "same-key":
+        x["k"][:] = x["k"][:, :1].clone()
+        x["beta"][:] = 0.9
+    elif kind.startswith("beta"):
+        x["beta"][:] = float(kind[-1])
+    elif kind == "forget":
+        x["g"][:, 10::37] = -30.0
+        x["g"][:, 70] = -200.0
+    else:
+        x["g"][:] = 0.0
+    check_backward(layer, x)
+
+
+def test_backward_by_differences(layer):
+    """The gradient of every input along a random direction against a central difference of the
+    forward pass.  The forward's outputs are off by 2^-8 |o| per entry at random, so the difference
+    over 2 h |direction| = 0.2 of the inputs' size carries about 2^-8 |do| |o| / (0.1 sqrt(n)) ..., far
+    below the 5 % of the slope's own size (norm of the gradient times that of the step) allowed."""
+    x = inputs(200, 1, 70, 2, 1, 64, 64)
+    g = torch.Generator().manual_seed(1)
+    do = torch.randn(x["v"].shape, generator=g).bfloat16().cuda()
+    names = ("q", "k", "v", "g", "beta", "state")
+    got = dict(zip(names, layer.delta_backward(*(x[n] for n in names[:5]), do, state=x["state"])))
+
+    def loss(y):
+        o, _ = layer.delta_prefill(*(y[n] for n in names[:5]), state=y["state"])
+        return float((o.double() * do.double()).sum())
+
+    for n in names:
+        step = got[n].float() / got[n].float().norm() * x[n].float().norm() * 0.05
+        up, down = ({**x, n: (x[n].float() + s * step).to(x[n].dtype)} for s in (1, -1))
+        real = (up[n].double() - down[n].double())           # the step as rounded to the input's type
+        want = float((got[n].double() * real).sum())
+        assert abs(loss(up) - loss(down) - want) <= 0.05 * abs(want), n
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("shape", [(1, 2, 1, 64, 64), (3, 4, 2, 128, 64), (5, 16, 16, 64, 128), (2, 6, 2, 128, 128)],
                          ids=str)
