@@ -109,7 +109,9 @@ lte_status check_norm(const lte_qk_norm* p) {
   if ((p->wq != nullptr && !aligned16(p->wq)) || (p->wk != nullptr && !aligned16(p->wk)))
     return LTE_ERR_INVALID_ARG;
   if (p->D != 64 && p->D != 128) return LTE_ERR_UNSUPPORTED;
-  if ((long long)p->B * p->T * ((long long)p->Hq + p->Hkv) >= (1ll << 34)) return LTE_ERR_UNSUPPORTED;
+  // 32-bit row indices
+  if ((long long)p->B * p->T >= (1ll << 31) || (long long)p->B * p->T * ((long long)p->Hq + p->Hkv) >= (1ll << 31))
+    return LTE_ERR_UNSUPPORTED;
   return LTE_OK;
 }
 
@@ -661,8 +663,6 @@ lte_status lte_qk_norm_rope_backward(const lte_qk_norm* p, const void* q, const 
   if (p->kind == LTE_NORM_NONE && (dwq != nullptr || dwk != nullptr)) return LTE_ERR_INVALID_ARG;
   if (workspace == nullptr || ws_bytes < lte_qk_norm_backward_workspace_bytes(p))
     return LTE_ERR_WORKSPACE;
-  strides_of(nullptr, p->T, p->Hq, p->D, p->dtype, &n.ds[0]);
-  strides_of(nullptr, p->T, p->Hkv, p->D, p->dtype, &n.ds[1]);
   n.dy[0] = dq_out; n.dy[1] = dk_out; n.y[0] = dq; n.y[1] = dk; n.grad_dtype = grad_dtype;
   n.part = (float*)workspace; n.dwq = dwq; n.dwk = dwk;
   return from_cuda(lte::qk_norm_backward(n, as_stream(stream)));

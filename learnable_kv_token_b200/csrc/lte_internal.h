@@ -130,7 +130,7 @@ struct QkNormArgs {
   float eps;
   const void *x[2], *dy[2];   // q, k; gradients of the outputs (backward)
   void* y[2];                 // q', k' or dq, dk (contiguous)
-  Strides4 xs[2], ds[2];
+  Strides4 xs[2];
   const float *w[2], *table;
   const int32_t* pos;
   float *part, *dwq, *dwk;    // backward: workspace, weight gradients

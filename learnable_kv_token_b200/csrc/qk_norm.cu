@@ -24,11 +24,11 @@ struct Args {
   const void *x[2];            // q, k
   const void *dy[2];           // gradients of the outputs (backward)
   void* y[2];                  // outputs: q', k' or dq, dk
-  Strides4 xs[2], ds[2];       // strides of x, dy
+  Strides4 xs[2];              // strides of x
   const float* w[2];
   const int32_t* pos;          // [B,T] or NULL (position t)
   const float* table;          // [n_pos][R]
-  float* part;                 // [blocks][2][D] partial weight gradients
+  float* part;                 // [blocks][D] partial weight gradients
   long long tokens;            // B * T
   int T, H[2], n_pos, rot, norm, inter;   // norm: 0 none, 1 on
   float c, eps;
@@ -38,15 +38,32 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// eight channels as they lie in memory: rows in flight take 4 registers in bf16, 8 in fp32
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
   }
-}
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -75,7 +92,7 @@ struct Turn {
   int src;                     // lane that holds the partner channels ((i, i + R/2) pairs)
 };
 template <int LPR>
-__device__ __forceinline__ void load_turn(const Args& a, int lg, long long token, float dir, Turn& t) {
+__device__ __forceinline__ void load_turn(const Args& a, int lg, unsigned token, int pos, float dir, Turn& t) {
   const int lane = threadIdx.x & 31, e0 = lg * 8, R = a.rot;
   t.src = lane;
 #pragma unroll
@@ -84,7 +101,7 @@ __device__ __forceinline__ void load_turn(const Args& a, int lg, long long token
     t.s[i] = 0.f;
   }
   if (e0 >= R) return;
-  const int p = a.pos != nullptr ? a.pos[token] : (int)(token % a.T);
+  const int p = a.pos != nullptr ? a.pos[token] : pos;
   const bool ok = p >= 0 && p < a.n_pos;
   const float* row = a.table + (long long)(ok ? p : 0) * R;
   const float bad = __int_as_float(0x7fc00000);
@@ -119,179 +136,193 @@ __device__ __forceinline__ void turn8(const Turn& t, bool inter, float (&v)[8]) 
   for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], t.c[i], o[i] * t.s[i]);
 }
 
-// rows [RPG part, RPG part + RPG) of a token's Hq + Hkv rows per group of lanes
+// A group of lanes takes rows [h0, h0 + rows) of one token's queries or keys.
+// The group index is 32 bits (host check), so its divisions are short.
+struct Group {
+  long long b, t;
+  unsigned token;
+  int h0, rows;
+};
+template <int RPG>
+__device__ __forceinline__ Group group_of(const Args& a, unsigned gi, int which, unsigned parts, unsigned part0) {
+  Group g;
+  g.token = gi / parts;
+  const int part = (int)(gi - g.token * parts) - (int)part0;
+  g.h0 = part * RPG;
+  g.rows = min(RPG, a.H[which] - g.h0);
+  g.b = g.token / (unsigned)a.T;
+  g.t = g.token - (unsigned)g.b * (unsigned)a.T;
+  return g;
+}
+
 template <typename T, int D, int RPG>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_kernel(const Args a) {
   constexpr int LPR = D / 8, kGroups = kThreads / LPR;
-  const int lg = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const int heads = a.H[0] + a.H[1], parts = (heads + RPG - 1) / RPG;
-  const long long gi = (long long)blockIdx.x * kGroups + grp;
-  long long token = gi / parts;
-  const int row0 = (int)(gi % parts) * RPG;
-  const bool live = token < a.tokens;
-  if (!live) token = 0;
-  const long long b = token / a.T, t = token % a.T;
-  float x[RPG][8];
+  const int lg = threadIdx.x % LPR;
+  const unsigned partsq = (a.H[0] + RPG - 1) / RPG, parts = partsq + (a.H[1] + RPG - 1) / RPG;
+  unsigned gi = blockIdx.x * (unsigned)kGroups + threadIdx.x / LPR;
+  const bool live = gi < (unsigned)a.tokens * parts;
+  if (!live) gi = 0;                                       // the lanes stay for the shuffles
+  const int which = gi % parts >= partsq;
+  const Group g = group_of<RPG>(a, gi, which, parts, which ? partsq : 0);
+  const T* x = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h + lg * 8;
+  T* y = (T*)a.y[which] + ((long long)g.token * a.H[which] + g.h0) * D + lg * 8;
+  Raw8<T> raw[RPG];
 #pragma unroll
   for (int i = 0; i < RPG; ++i) {
-    const int row = row0 + i, which = row >= a.H[0], h = which ? row - a.H[0] : row;
-    if (live && row < heads)
-      load8((const T*)a.x[which] + b * a.xs[which].b + t * a.xs[which].t + h * a.xs[which].h + lg * 8, x[i]);
-    else
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+    if (i < g.rows) raw[i].load(x + i * a.xs[which].h);
+    else raw[i].zero();
   }
   Turn turn;
-  load_turn<LPR>(a, lg, token, 1.f, turn);
+  load_turn<LPR>(a, lg, g.token, (int)g.t, 1.f, turn);
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  if (a.norm && a.w[which] != nullptr) load8(a.w[which] + lg * 8, w);
 #pragma unroll
   for (int i = 0; i < RPG; ++i) {
-    const int row = row0 + i, which = row >= a.H[0], h = which ? row - a.H[0] : row;
+    float v[8];
+    raw[i].get(v);
     if (a.norm) {
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
       const float r = rsqrtf(fmaf(a.c, row_sum<LPR>(ss), a.eps));
-      const float* w = a.w[which];
-      if (w != nullptr) {
-        float w8[8];
-        load8(w + lg * 8, w8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= r * w8[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= r;
-      }
+      for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
     }
-    if (a.rot) turn8(turn, a.inter, x[i]);
-    if (live && row < heads)
-      store8((T*)a.y[which] + ((b * a.T + t) * a.H[which] + h) * D + lg * 8, x[i]);
+    if (a.rot) turn8(turn, a.inter, v);
+    if (live && i < g.rows) store8(y + i * D, v);
   }
 }
 
-// Gradients: the blocks walk the groups; a lane sums its channels' weight
-// gradients over all its rows in fp32 and the block's lanes add theirs in a
-// fixed order, so the result does not change from run to run.
+// Gradients: a block takes groups of queries or groups of keys only (blocks
+// [0, blocks_q) and the rest), so a lane holds one set of weight gradients: its
+// channels' sums over all its rows, in fp32.  The block's lanes are added in a
+// fixed order, and so are the blocks, so the result repeats bit by bit.
 template <typename T, typename TG, int D, int RPG>
-__global__ void __launch_bounds__(kThreads) qk_norm_backward_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_backward_kernel(const Args a, int blocks_q) {
   constexpr int LPR = D / 8, kGroups = kThreads / LPR;
-  __shared__ float red[kGroups][2 * D];
+  __shared__ float red[kGroups][D];
   const int lg = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const int heads = a.H[0] + a.H[1], parts = (heads + RPG - 1) / RPG;
-  const long long total = a.tokens * parts, step = (long long)gridDim.x * kGroups;
-  float dw[2][8], w8[2][8];
+  const int which = (int)blockIdx.x >= blocks_q;
+  const unsigned block = which ? blockIdx.x - blocks_q : blockIdx.x, blocks = which ? gridDim.x - blocks_q : blocks_q;
+  const unsigned parts = (a.H[which] + RPG - 1) / RPG, total = (unsigned)a.tokens * parts;
+  float dw[8], w[8];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[n][e] = 0.f;
-      w8[n][e] = 1.f;
-    }
-    if (a.norm && a.w[n] != nullptr) load8(a.w[n] + lg * 8, w8[n]);
+  for (int e = 0; e < 8; ++e) {
+    dw[e] = 0.f;
+    w[e] = 1.f;
   }
-  for (long long g0 = (long long)blockIdx.x * kGroups; g0 < total; g0 += step) {
-    const long long gi = g0 + grp;
-    long long token = gi / parts;
-    const int row0 = (int)(gi % parts) * RPG;
-    const bool live = gi < total;
-    if (!live) token = 0;
-    const long long b = token / a.T, t = token % a.T;
-    float x[RPG][8], dn[RPG][8];
+  if (a.norm && a.w[which] != nullptr) load8(a.w[which] + lg * 8, w);
+  for (unsigned g0 = block * kGroups; g0 < total; g0 += blocks * kGroups) {
+    const bool live = g0 + grp < total;
+    const Group g = group_of<RPG>(a, live ? g0 + grp : 0, which, parts, 0);
+    const T* xp = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h + lg * 8;
+    const long long at = ((long long)g.token * a.H[which] + g.h0) * D + lg * 8;
+    const TG* dp = (const TG*)a.dy[which] + at;
+    Raw8<T> rx[RPG];
+    Raw8<TG> rd[RPG];
 #pragma unroll
     for (int i = 0; i < RPG; ++i) {
-      const int row = row0 + i, which = row >= a.H[0], h = which ? row - a.H[0] : row;
-      if (live && row < heads) {
-        load8((const TG*)a.dy[which] + b * a.ds[which].b + t * a.ds[which].t + h * a.ds[which].h + lg * 8, dn[i]);
-        load8((const T*)a.x[which] + b * a.xs[which].b + t * a.xs[which].t + h * a.xs[which].h + lg * 8, x[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = dn[i][e] = 0.f;
+      if (live && i < g.rows) {
+        rd[i].load(dp + i * D);
+        rx[i].load(xp + i * a.xs[which].h);
+      } else {                                             // zeros add nothing to the weight gradients
+        rd[i].zero();
+        rx[i].zero();
       }
     }
     Turn turn;
-    load_turn<LPR>(a, lg, token, -1.f, turn);
+    load_turn<LPR>(a, lg, g.token, (int)g.t, -1.f, turn);
 #pragma unroll
     for (int i = 0; i < RPG; ++i) {
-      const int row = row0 + i, which = row >= a.H[0], h = which ? row - a.H[0] : row;
-      const bool on = live && row < heads;
-      if (a.rot) turn8(turn, a.inter, dn[i]);
+      const bool on = live && i < g.rows;
+      float dn[8];
+      rd[i].get(dn);
+      if (a.rot) turn8(turn, a.inter, dn);
       if (a.norm) {
-        float ss = 0.f, in = 0.f, z[8];
+        float ss = 0.f, in = 0.f, v[8];
+        rx[i].get(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          z[e] = dn[i][e] * (which ? w8[1][e] : w8[0][e]);
-          ss = fmaf(x[i][e], x[i][e], ss);
-          in = fmaf(z[e], x[i][e], in);
+          ss = fmaf(v[e], v[e], ss);
+          in = fmaf(dn[e] * w[e], v[e], in);
         }
         const float r = rsqrtf(fmaf(a.c, row_sum<LPR>(ss), a.eps));
         const float m = a.c * r * r * r * row_sum<LPR>(in);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float d = on ? dn[i][e] * x[i][e] * r : 0.f;
-          dw[0][e] += which ? 0.f : d;
-          dw[1][e] += which ? d : 0.f;
-          dn[i][e] = fmaf(r, z[e], -m * x[i][e]);
+          dw[e] += on ? dn[e] * (v[e] * r) : 0.f;
+          dn[e] = fmaf(r * w[e], dn[e], -m * v[e]);
         }
       }
-      if (on) store8((T*)a.y[which] + ((b * a.T + t) * a.H[which] + h) * D + lg * 8, dn[i]);
+      if (on) store8((T*)a.y[which] + at + i * D, dn);
     }
   }
   if (a.part == nullptr) return;
-#pragma unroll
-  for (int n = 0; n < 2; ++n) store8(&red[grp][n * D + lg * 8], dw[n]);
+  store8(&red[grp][lg * 8], dw);
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  if (threadIdx.x < D) {
     float s = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) s += red[g][i];
-    a.part[(long long)blockIdx.x * 2 * D + i] = s;
+    for (int g = 0; g < kGroups; ++g) s += red[g][threadIdx.x];
+    a.part[(long long)blockIdx.x * D + threadIdx.x] = s;
   }
 }
 
-// dw[i] = sum over the blocks' partials, 32 columns per CTA, in a fixed order
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, int blocks, int D,
-                                                          float* dwq, float* dwk) {
+// dw[i] = sum over the blocks' partials (rows [0, blocks_q) for the queries'
+// weight, the others for the keys'), 32 columns per CTA, in a fixed order
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* __restrict__ part, int blocks_q, int blocks,
+                                                          int D, float* dwq, float* dwk) {
   __shared__ float red[32][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  const int which = blockIdx.x >= D / 32, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int col = (which ? blockIdx.x - D / 32 : blockIdx.x) * 32 + lane;
   float s = 0.f;
-  for (int b = row; b < blocks; b += 32) s += part[(long long)b * 2 * D + col];
-  red[row][threadIdx.x & 31] = s;
+  for (int b = (which ? blocks_q : 0) + row; b < (which ? blocks : blocks_q); b += 32) s += part[(long long)b * D + col];
+  red[row][lane] = s;
   __syncthreads();
   if (row == 0) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-    float* out = col < D ? dwq : dwk;
-    if (out != nullptr) out[col < D ? col : col - D] = s;
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
+    float* out = which ? dwk : dwq;
+    if (out != nullptr) out[col] = s;
   }
 }
 
-constexpr int kRows = 4;                 // rows of one token per group of lanes
-constexpr int kBackwardBlocks = 148 * 6; // resident CTAs of the gradient kernel on 148 SMs
+// rows of one token per group of lanes: what 64 registers hold without spills
+template <typename T> constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+constexpr int kBackRows = 2;             // (gradients: two rows of x and dy in flight)
+constexpr int kBackBlocks = 148 * 3;     // resident CTAs of the gradient kernel on 148 SMs
 
 template <typename T, int D>
 cudaError_t forward(const Args& a, cudaStream_t stream) {
-  constexpr int kGroups = kThreads / (D / 8);
-  const int heads = a.H[0] + a.H[1];
+  constexpr int kGroups = kThreads / (D / 8), kRpg = kRows<T>;
   // few tokens (a decode step): one row per group, so that the rows spread over the SMs
-  const bool few = a.tokens * heads <= 148LL * kGroups * kRows;
-  const int parts = few ? heads : (heads + kRows - 1) / kRows;
-  const unsigned grid = (unsigned)((a.tokens * parts + kGroups - 1) / kGroups);
+  const bool few = a.tokens * (a.H[0] + a.H[1]) <= 148LL * kGroups * kRpg;
+  const int rpg = few ? 1 : kRpg;
+  const long long groups = a.tokens * ((a.H[0] + rpg - 1) / rpg + (a.H[1] + rpg - 1) / rpg);
+  const unsigned grid = (unsigned)((groups + kGroups - 1) / kGroups);
   if (few) qk_norm_kernel<T, D, 1><<<grid, kThreads, 0, stream>>>(a);
-  else qk_norm_kernel<T, D, kRows><<<grid, kThreads, 0, stream>>>(a);
+  else qk_norm_kernel<T, D, kRpg><<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-inline int backward_blocks(long long tokens, int heads, int D) {
-  const int groups = kThreads / (D / 8);
-  const long long need = (tokens * ((heads + kRows - 1) / kRows) + groups - 1) / groups;
-  return (int)(need < kBackwardBlocks ? need : kBackwardBlocks);
+// blocks for the queries and for the keys, in proportion to their groups
+inline void backward_blocks(long long tokens, int Hq, int Hkv, int D, int* bq, int* bk) {
+  const int per = kThreads / (D / 8);
+  const long long gq = tokens * ((Hq + kBackRows - 1) / kBackRows), gk = tokens * ((Hkv + kBackRows - 1) / kBackRows);
+  const long long nq = (gq + per - 1) / per, nk = (gk + per - 1) / per;
+  const long long q = nq * kBackBlocks / (nq + nk);
+  *bq = (int)(nq + nk <= kBackBlocks ? nq : (q < 1 ? 1 : q));
+  *bk = (int)(nq + nk <= kBackBlocks ? nk : (kBackBlocks - *bq < 1 ? 1 : kBackBlocks - *bq));
 }
 
 template <typename T, typename TG, int D>
 cudaError_t backward(const Args& a, float* dwq, float* dwk, cudaStream_t stream) {
-  const int blocks = backward_blocks(a.tokens, a.H[0] + a.H[1], D);
-  qk_norm_backward_kernel<T, TG, D, kRows><<<blocks, kThreads, 0, stream>>>(a);
-  if (a.part != nullptr) qk_norm_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(a.part, blocks, D, dwq, dwk);
+  int bq, bk;
+  backward_blocks(a.tokens, a.H[0], a.H[1], D, &bq, &bk);
+  qk_norm_backward_kernel<T, TG, D, kBackRows><<<bq + bk, kThreads, 0, stream>>>(a, bq);
+  if (a.part != nullptr) qk_norm_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(a.part, bq, bq + bk, D, dwq, dwk);
   return cudaGetLastError();
 }
 
@@ -302,7 +333,6 @@ Args args_of(const QkNormArgs& n) {
     a.dy[i] = n.dy[i];
     a.y[i] = n.y[i];
     a.xs[i] = n.xs[i];
-    a.ds[i] = n.ds[i];
     a.w[i] = n.w[i];
     a.H[i] = n.H[i];
   }
@@ -323,7 +353,9 @@ Args args_of(const QkNormArgs& n) {
 }  // namespace qkn
 
 size_t qk_norm_backward_bytes(int B, int T, int Hq, int Hkv, int D) {
-  return (size_t)qkn::backward_blocks((long long)B * T, Hq + Hkv, D) * 2 * D * sizeof(float);
+  int bq, bk;
+  qkn::backward_blocks((long long)B * T, Hq, Hkv, D, &bq, &bk);
+  return (size_t)(bq + bk) * D * sizeof(float);
 }
 
 cudaError_t qk_norm(const QkNormArgs& n, cudaStream_t stream) {

@@ -9,7 +9,8 @@ hybrid is delta_prefill, delta_step and delta_backward.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
+import inspect
 from dataclasses import dataclass
 
 import torch
@@ -287,7 +288,7 @@ class QKNorm:
 
     def struct(self, q, k) -> L.lte_qk_norm:
         B, T, Hq, D = q.shape
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != D or k.dtype != q.dtype:
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != D or k.dtype is not q.dtype:
             raise ValueError("q [B,T,Hq,D] and k [B,T,Hkv,D] of one dtype")
         if self.kind not in self.KINDS:
             raise ValueError(f"kind is one of {tuple(self.KINDS)}")
@@ -312,148 +313,151 @@ def rope_table(n_pos, rot_dim, base=10000.0, device="cuda") -> torch.Tensor:
 
 
 def _check(t, name, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-@contextlib.contextmanager
-def _on(t, stream):
-    """The device of t, and `stream` (default: that device's current stream) for the launches and
-    for the memory that they use."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    if stream is not None and stream.device != t.device:
-        raise ValueError("the stream and the tensors are on different devices")
-    with torch.cuda.device(t.device):
-        if stream is None:
-            yield torch.cuda.current_stream()
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+def _on_device(fn):
+    """Runs fn on the device of its first tensor and on `stream` (default: that device's current
+    stream), for the launches and for the memory that they use."""
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        dev = (args[0] if args else kw[first]).device
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError("the stream and the tensors are on different devices")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
-def qk_norm_rope(q, k, p: QKNorm, positions=None, q_out=None, k_out=None, stream=None):
+def _norm_struct(q, k, p, positions):
+    if k.device != q.device:
+        raise ValueError("q and k are on different devices")
+    if positions is not None:
+        _check(positions, "positions", q.shape[:2], torch.int32, q.device)
+    return p.struct(q, k)
+
+
+@_on_device
+def qk_norm_rope(q, k, p: QKNorm, positions=None, q_out=None, k_out=None):
     """Normed and rotated q [B,T,Hq,D] and k [B,T,Hkv,D] (bf16 or fp32; strided views with
-    contiguous channels are fine).  positions: int32 [B,T], default 0 .. T-1."""
-    with _on(q, stream) as st:
-        c = p.struct(q, k)
-        if k.device != q.device:
-            raise ValueError("q and k are on different devices")
-        if positions is not None:
-            _check(positions, "positions", q.shape[:2], torch.int32, q.device)
-        outs = []
-        for x, y in ((q, q_out), (k, k_out)):
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            else:
-                _check(y, "output", x.shape, x.dtype, x.device)
-            outs.append(y)
-        L.lte_qk_norm_rope(c, q, k, *outs, positions, st)
-    return tuple(outs)
+    contiguous channels are fine).  positions: int32 [B,T], default 0 .. T-1.  q_out and k_out may
+    be q and k if those are contiguous.  Also takes `stream`."""
+    c = _norm_struct(q, k, p, positions)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _check(q_out, "q_out", q.shape, q.dtype, q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+    else:
+        _check(k_out, "k_out", k.shape, k.dtype, q.device)
+    L.lte_qk_norm_rope(c, q, k, q_out, k_out, positions)
+    return q_out, k_out
 
 
-def qk_norm_rope_backward(q, k, dq_out, dk_out, p: QKNorm, positions=None, stream=None):
+@_on_device
+def qk_norm_rope_backward(q, k, dq_out, dk_out, p: QKNorm, positions=None):
     """Gradients through qk_norm_rope for those of its outputs (fp32, as the attention backward
-    gives them, or q's dtype): dq, dk in q's dtype and dwq, dwk fp32 [D] (None without a weight)."""
-    with _on(q, stream) as st:
-        c = p.struct(q, k)
-        if k.device != q.device:
-            raise ValueError("q and k are on different devices")
-        if positions is not None:
-            _check(positions, "positions", q.shape[:2], torch.int32, q.device)
-        if dq_out.dtype not in (torch.float32, q.dtype):
-            raise ValueError("gradients are fp32 or of q's dtype")
-        _check(dq_out, "dq_out", q.shape, dq_out.dtype, q.device)
-        _check(dk_out, "dk_out", k.shape, dq_out.dtype, q.device)
-        dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
-        normed = p.kind != "none"
-        dwq, dwk = (torch.empty_like(w) if normed and w is not None else None for w in (p.wq, p.wk))
-        ws = torch.empty(L.lte_qk_norm_backward_workspace_bytes(c), dtype=torch.uint8, device=q.device)
-        L.lte_qk_norm_rope_backward(c, q, k, dq_out, dk_out, dq, dk, dwq, dwk, ws, positions, st)
+    gives them, or q's dtype): dq, dk in q's dtype and dwq, dwk fp32 [D] (None without a weight).
+    Also takes `stream`."""
+    c = _norm_struct(q, k, p, positions)
+    if dq_out.dtype not in (torch.float32, q.dtype):
+        raise ValueError("gradients are fp32 or of q's dtype")
+    _check(dq_out, "dq_out", q.shape, dq_out.dtype, q.device)
+    _check(dk_out, "dk_out", k.shape, dq_out.dtype, q.device)
+    dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    dwq = dwk = None
+    if p.kind != "none":
+        dwq, dwk = (None if w is None else torch.empty_like(w) for w in (p.wq, p.wk))
+    ws = torch.empty(L.lte_qk_norm_backward_workspace_bytes(c), dtype=torch.uint8, device=q.device)
+    L.lte_qk_norm_rope_backward(c, q, k, dq_out, dk_out, dq, dk, dwq, dwk, ws, positions)
     return dq, dk, dwq, dwk
 
 
 # ---------------------------------------------------------------- gated delta rule
-def _delta_dims(q, k, v, scale):
+def _delta_dims(q, k, v, g, beta, lens, scale):
     B, T, Hk, dk = q.shape
     H, dv = v.shape[2:]
     if k.shape != q.shape or v.shape[:2] != q.shape[:2]:
         raise ValueError("q, k [B,T,Hk,dk] and v [B,T,H,dv]")
-    if not (q.dtype == k.dtype == v.dtype) or not (q.device == k.device == v.device):
+    if not (q.dtype is k.dtype is v.dtype) or not (q.device == k.device == v.device):
         raise ValueError("q, k and v share dtype and device")
+    _check(g, "g", (B, T, H), torch.float32, q.device)
+    _check(beta, "beta", (B, T, H), torch.float32, q.device)
+    if lens is not None:
+        _check(lens, "lens", (B,), torch.int32, q.device)
     return L.make_gdr_dims(B, T, H, Hk, dk, dv, dk ** -0.5 if scale is None else scale, q.dtype)
 
 
-def _delta_gates(v, g, beta, lens):
-    for t, name in ((g, "g"), (beta, "beta")):
-        _check(t, name, v.shape[:3], torch.float32, v.device)
-    if lens is not None:
-        _check(lens, "lens", v.shape[:1], torch.int32, v.device)
-
-
-def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out=None, stream=None):
+@_on_device
+def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out=None):
     """The gated delta rule over T tokens: q, k [B,T,Hk,dk], v [B,T,H,dv] (bf16 or fp32, strided
     views with contiguous channels are fine), g (log decay, <= 0) and beta fp32 [B,T,H], state
     fp32 [B,H,dv,dk] (default zeros), lens int32 [B]: sequence b has lens[b] tokens; the rows of o
     behind them are zero.  scale defaults to dk^-1/2.  Returns o and the state after the last
-    token (in state_out, which may be `state`; by default a new tensor)."""
-    with _on(q, stream) as st:
-        d = _delta_dims(q, k, v, scale)
-        _delta_gates(v, g, beta, lens)
-        B, T, H, dv = v.shape
-        shape = (B, H, dv, q.shape[3])
-        if state is not None:
-            _check(state, "state", shape, torch.float32, q.device)
-        if state_out is None:
-            state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
-        else:
-            _check(state_out, "state_out", shape, torch.float32, q.device)
-        make = torch.empty if lens is None else torch.zeros
-        o = make(v.shape, dtype=v.dtype, device=v.device)
-        ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL), dtype=torch.uint8, device=q.device)
-        L.lte_gdr_prefill(d, q, k, v, g, beta, o, state_out, ws, state, lens, st)
+    token (in state_out, which may be `state`; by default a new tensor).  Also takes `stream`."""
+    d = _delta_dims(q, k, v, g, beta, lens, scale)
+    shape = (v.shape[0], v.shape[2], v.shape[3], q.shape[3])
+    if state is not None:
+        _check(state, "state", shape, torch.float32, q.device)
+    if state_out is None:
+        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    else:
+        _check(state_out, "state_out", shape, torch.float32, q.device)
+    o = (torch.empty if lens is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
+    ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL), dtype=torch.uint8, device=q.device)
+    L.lte_gdr_prefill(d, q, k, v, g, beta, o, state_out, ws, state, lens)
     return o, state_out
 
 
-def delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lens=None, scale=None, stream=None):
+@_on_device
+def delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lens=None, scale=None):
     """Gradients of delta_prefill (bf16) for the gradients `do` of o and `dstate` of the final state
     (default zeros): dq, dk [B,T,Hk,dk], dv [B,T,H,dv] in bf16, dg, dbeta fp32 [B,T,H], and that of
-    the initial state, fp32 [B,H,dv,dk].  Rows behind `lens` are zero."""
-    with _on(q, stream) as st:
-        d = _delta_dims(q, k, v, scale)
-        _delta_gates(v, g, beta, lens)
-        B, T, H, dv = v.shape
-        shape = (B, H, dv, q.shape[3])
-        for t, name in ((state, "state"), (dstate, "dstate")):
-            if t is not None:
-                _check(t, name, shape, torch.float32, q.device)
-        if do.shape != v.shape or do.dtype != v.dtype or do.device != v.device:
-            raise ValueError("do has v's shape, dtype and device")
-        make = torch.empty if lens is None else torch.zeros
-        grads = [make(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v, g, beta)]
-        ds = torch.empty(shape, dtype=torch.float32, device=q.device)
-        ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD), dtype=torch.uint8, device=q.device)
-        L.lte_gdr_backward(d, q, k, v, g, beta, do, *grads, ws, state, lens, dstate, ds, st)
+    the initial state, fp32 [B,H,dv,dk].  Rows behind `lens` are zero.  Also takes `stream`."""
+    d = _delta_dims(q, k, v, g, beta, lens, scale)
+    shape = (v.shape[0], v.shape[2], v.shape[3], q.shape[3])
+    if state is not None:
+        _check(state, "state", shape, torch.float32, q.device)
+    if dstate is not None:
+        _check(dstate, "dstate", shape, torch.float32, q.device)
+    if do.shape != v.shape or do.dtype is not v.dtype or do.device != v.device:
+        raise ValueError("do has v's shape, dtype and device")
+    make = torch.empty if lens is None else torch.zeros
+    grads = [make(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v, g, beta)]
+    ds = torch.empty(shape, dtype=torch.float32, device=q.device)
+    ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD), dtype=torch.uint8, device=q.device)
+    L.lte_gdr_backward(d, q, k, v, g, beta, do, *grads, ws, state, lens, dstate, ds)
     return (*grads, ds)
 
 
-def delta_step(q_t, k_t, v_t, g_t, beta_t, state, scale=None, out=None, stream=None):
+@_on_device
+def delta_step(q_t, k_t, v_t, g_t, beta_t, state, scale=None, out=None):
     """One token per sequence: q_t, k_t [B,Hk,dk], v_t [B,H,dv], g_t, beta_t fp32 [B,H]; `state`
-    is updated in place.  Returns o_t [B,H,dv]."""
-    with _on(q_t, stream) as st:
-        d = _delta_dims(q_t[:, None], k_t[:, None], v_t[:, None], scale)
-        B, H, dv = v_t.shape
-        _check(state, "state", (B, H, dv, q_t.shape[2]), torch.float32, q_t.device)
-        for t, name, shape, dt in ((q_t, "q_t", q_t.shape, q_t.dtype), (k_t, "k_t", q_t.shape, q_t.dtype),
-                                   (v_t, "v_t", v_t.shape, q_t.dtype), (g_t, "g_t", (B, H), torch.float32),
-                                   (beta_t, "beta_t", (B, H), torch.float32)):
-            _check(t, name, shape, dt, q_t.device)
-        if out is None:
-            out = torch.empty_like(v_t)
-        else:
-            _check(out, "out", v_t.shape, v_t.dtype, v_t.device)
-        L.lte_gdr_decode_step(d, q_t, k_t, v_t, g_t, beta_t, out, state, st)
+    fp32 [B,H,dv,dk] is updated in place.  Returns o_t [B,H,dv].  Also takes `stream`."""
+    B, H, dv = v_t.shape
+    dt, dev = q_t.dtype, q_t.device
+    Hk, dk = q_t.shape[1:]
+    _check(q_t, "q_t", (B, Hk, dk), dt, dev)
+    _check(k_t, "k_t", (B, Hk, dk), dt, dev)
+    _check(v_t, "v_t", (B, H, dv), dt, dev)
+    _check(g_t, "g_t", (B, H), torch.float32, dev)
+    _check(beta_t, "beta_t", (B, H), torch.float32, dev)
+    _check(state, "state", (B, H, dv, dk), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(v_t)
+    else:
+        _check(out, "out", (B, H, dv), dt, dev)
+    L.lte_gdr_decode_step(L.make_gdr_dims(B, 1, H, Hk, dk, dv, dk ** -0.5 if scale is None else scale, dt),
+                          q_t, k_t, v_t, g_t, beta_t, out, state)
     return out
 
 

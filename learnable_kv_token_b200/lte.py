@@ -325,59 +325,86 @@ def lte_gla_decode_step(q_t, k_t, v_t, a_t, o_t, state, stream=None):
           _ptr(v_t), _ptr(a_t), _ptr(o_t), _ptr(state), _stream(stream))
 
 
+# The entry points below are called once per token and layer: their arguments go to ctypes as plain
+# integers and structs, and contiguous tensors need no strides.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw(stream):
+    # the raw handle: building a torch.cuda.Stream for it takes as long as the launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+
+
+def _ref_strides(t):
+    if t.is_contiguous():
+        return None
+    b, n, h, d = t.stride()
+    if d != 1:
+        raise ValueError("innermost stride must be 1")
+    return C.byref(lte_strides(b, n, h))
+
+
+def _check_status(name, st):
+    if st != 0:
+        raise LteError(name, st)
+
+
 def make_gdr_dims(B, T, H, Hk, dk, dv, scale, dtype) -> lte_gdr_dims:
-    return lte_gdr_dims(B, T, H, Hk, dk, dv, float(scale),
+    return lte_gdr_dims(B, T, H, Hk, dk, dv, scale,
                         dtype_code(dtype) if isinstance(dtype, torch.dtype) else int(dtype))
 
 
 def lte_gdr_workspace_bytes(dims: lte_gdr_dims, which: int) -> int:
-    return int(_lib.lte_gdr_workspace_bytes(C.byref(dims), which))
+    return _lib.lte_gdr_workspace_bytes(C.byref(dims), which)
 
 
 def lte_gdr_prefill(dims, q, k, v, g, beta, o, state_out, workspace, state_in=None, lens=None,
                     stream=None):
-    _call("lte_gdr_prefill", C.byref(dims), _ptr(q), _ptr(k), _ptr(v), C.byref(_strides(q)),
-          C.byref(_strides(k)), C.byref(_strides(v)), _ptr(g), _ptr(beta), _ptr(lens),
-          _ptr(state_in), _ptr(o), C.byref(_strides(o)), _ptr(state_out), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream(stream))
+    _check_status("lte_gdr_prefill", _lib.lte_gdr_prefill(
+        C.byref(dims), _addr(q), _addr(k), _addr(v), _ref_strides(q), _ref_strides(k),
+        _ref_strides(v), _addr(g), _addr(beta), _addr(lens), _addr(state_in), _addr(o),
+        _ref_strides(o), _addr(state_out), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _raw(stream)))
 
 
 def lte_gdr_backward(dims, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, workspace, state_in=None,
                      lens=None, dstate_out=None, dstate_in=None, stream=None):
-    _call("lte_gdr_backward", C.byref(dims), _ptr(q), _ptr(k), _ptr(v), C.byref(_strides(q)),
-          C.byref(_strides(k)), C.byref(_strides(v)), _ptr(g), _ptr(beta), _ptr(lens),
-          _ptr(state_in), _ptr(do), C.byref(_strides(do)), _ptr(dstate_out), _ptr(dq), _ptr(dk),
-          _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dstate_in), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream(stream))
+    _check_status("lte_gdr_backward", _lib.lte_gdr_backward(
+        C.byref(dims), _addr(q), _addr(k), _addr(v), _ref_strides(q), _ref_strides(k),
+        _ref_strides(v), _addr(g), _addr(beta), _addr(lens), _addr(state_in), _addr(do),
+        _ref_strides(do), _addr(dstate_out), _addr(dq), _addr(dk), _addr(dv), _addr(dg),
+        _addr(dbeta), _addr(dstate_in), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _raw(stream)))
 
 
 def lte_gdr_decode_step(dims, q_t, k_t, v_t, g_t, beta_t, o_t, state, stream=None):
-    _call("lte_gdr_decode_step", C.byref(dims), _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(g_t),
-          _ptr(beta_t), _ptr(o_t), _ptr(state), _stream(stream))
+    _check_status("lte_gdr_decode_step", _lib.lte_gdr_decode_step(
+        C.byref(dims), _addr(q_t), _addr(k_t), _addr(v_t), _addr(g_t), _addr(beta_t), _addr(o_t),
+        _addr(state), _raw(stream)))
 
 
 def make_qk_norm(B, T, Hq, Hkv, D, dtype, kind, eps, rot_dim=0, interleaved=False, wq=None,
                  wk=None, table=None) -> lte_qk_norm:
     """lte_qk_norm over device tensors wq, wk [D] and table [n_pos, rot_dim]
     (fp32, contiguous; the caller keeps them alive)."""
-    ptr = (lambda t: None if t is None else t.data_ptr())
-    return lte_qk_norm(B, T, Hq, Hkv, D, dtype_code(dtype), int(kind), float(eps), rot_dim,
-                       int(interleaved), 0 if table is None else table.shape[0], ptr(wq), ptr(wk),
-                       ptr(table))
+    return lte_qk_norm(B, T, Hq, Hkv, D, dtype_code(dtype), kind, eps, rot_dim, interleaved,
+                       0 if table is None else table.shape[0], _addr(wq), _addr(wk), _addr(table))
 
 
 def lte_qk_norm_rope(norm, q, k, q_out, k_out, positions=None, stream=None):
-    _call("lte_qk_norm_rope", C.byref(norm), _ptr(q), _ptr(k), C.byref(_strides(q)),
-          C.byref(_strides(k)), _ptr(positions), _ptr(q_out), _ptr(k_out), _stream(stream))
+    _check_status("lte_qk_norm_rope", _lib.lte_qk_norm_rope(
+        C.byref(norm), _addr(q), _addr(k), _ref_strides(q), _ref_strides(k), _addr(positions),
+        _addr(q_out), _addr(k_out), _raw(stream)))
 
 
 def lte_qk_norm_backward_workspace_bytes(norm) -> int:
-    return int(_lib.lte_qk_norm_backward_workspace_bytes(C.byref(norm)))
+    return _lib.lte_qk_norm_backward_workspace_bytes(C.byref(norm))
 
 
 def lte_qk_norm_rope_backward(norm, q, k, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                               positions=None, stream=None):
-    _call("lte_qk_norm_rope_backward", C.byref(norm), _ptr(q), _ptr(k), C.byref(_strides(q)),
-          C.byref(_strides(k)), _ptr(positions), _ptr(dq_out), _ptr(dk_out),
-          dtype_code(dq_out.dtype), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream(stream))
+    _check_status("lte_qk_norm_rope_backward", _lib.lte_qk_norm_rope_backward(
+        C.byref(norm), _addr(q), _addr(k), _ref_strides(q), _ref_strides(k), _addr(positions),
+        _addr(dq_out), _addr(dk_out), dtype_code(dq_out.dtype), _addr(dq), _addr(dk), _addr(dwq),
+        _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(), _raw(stream)))
