@@ -149,12 +149,14 @@ delta_back_chain_kernel(const GradArgs ga) {
         mma_bf16(P[2 * np + 1], dof[ks], x[2], x[3]);
       }
     }
-    // ---- F^T = dU^T T
+    // ---- F^T = dU^T T (the diagonal b in fp32)
     float F[8][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) F[n][e] = 0.f;
+    for (int n = 0; n < 8; ++n) {
+      const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * n + t2);
+      F[n][0] = bt.x * P[n][0]; F[n][1] = bt.y * P[n][1];
+      F[n][2] = bt.x * P[n][2]; F[n][3] = bt.y * P[n][3];
+    }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t hi[4], lo[4];
@@ -607,7 +609,7 @@ cudaError_t launch_back(const GradArgs& a, int B, cudaStream_t stream) {
 template <int DK>
 cudaError_t back_chain(const GradArgs& a, int B, cudaStream_t stream) {
   const long long strips = (long long)B * a.f.H * (a.f.dv / 16);   // as the forward chain
-  if (strips >= 8 * 148 && a.f.dv == 128) return launch_back<DK, 8>(a, B, stream);
+  if (strips >= 8 * 96 && a.f.dv == 128) return launch_back<DK, 8>(a, B, stream);
   if (strips >= 4 * 148) return launch_back<DK, 4>(a, B, stream);
   if (strips >= 2 * 148) return launch_back<DK, 2>(a, B, stream);
   return launch_back<DK, 1>(a, B, stream);

@@ -17,12 +17,51 @@ namespace delta {
 constexpr int kPrepThreads = 128;
 constexpr int kXs = 68;                                   // row stride of M and X in floats
 
+// x = hi + lo in TF32 (11 bits each); the tensor core drops the lower bits of lo
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// c (16 x 8 NT) = sign A (16 x 8 KS) B (8 KS x 8 NT), row stride kXs: three TF32
+// products per step keep about 21 bits
+template <int NT, int KS>
+__device__ __forceinline__ void mma_tf32x3(float (&c)[NT][4], const float* A, const float* B, float sign, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    uint32_t ah[4], al[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      split_tf32(sign * A[(g + 8 * (e & 1)) * kXs + 8 * k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) split_tf32(B[(8 * k + t + 4 * e) * kXs + 8 * n + g], bh[e], bl[e]);
+      mma_tf32(c[n], ah, bh);
+      mma_tf32(c[n], ah, bl);
+      mma_tf32(c[n], al, bh);
+    }
+  }
+}
+__device__ __forceinline__ void store_c(float* p, const float* c, int lane) {
+  float* q = p + (lane >> 2) * kXs + (lane & 3) * 2;
+  *reinterpret_cast<float2*>(q) = make_float2(c[0], c[1]);
+  *reinterpret_cast<float2*>(q + 8 * kXs) = make_float2(c[2], c[3]);
+}
+
 template <int DK, bool A_LO>
 __global__ void __launch_bounds__(kPrepThreads)
 delta_prepare_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ double G[L];
-  __shared__ float bs[L];
+  __shared__ __align__(16) float bs[L];
   const int u = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
@@ -122,85 +161,69 @@ delta_prepare_kernel(const ChunkArgs a) {
   for (int i = tid; i < (A_LO ? 2 : 1) * kImg / 16; i += kPrepThreads)
     reinterpret_cast<uint4*>(rec + 2 * kImg)[i] = reinterpret_cast<const uint4*>(img)[i];
   __syncthreads();
-  // the diagonal blocks: column j of block d
-  if (tid < 64) {
-    const int d = (tid >> 4) * 16, j = tid & 15;
+  // the diagonal blocks: warp d, a lane per column; rows of M by broadcast
+  if (lane < 16) {
+    const int d = 16 * warp;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == j ? 1.f : 0.f;
+      float s = i == lane ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < i; ++k) s = fmaf(-M[(d + i) * kXs + d + k], x[k], s);
+      for (int k = 0; k < i; k += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&M[(d + i) * kXs + d + k]);
+        s = fmaf(-m.x, x[k], s);
+        if (k + 1 < i) s = fmaf(-m.y, x[k + 1], s);
+        if (k + 2 < i) s = fmaf(-m.z, x[k + 2], s);
+        if (k + 3 < i) s = fmaf(-m.w, x[k + 3], s);
+      }
       x[i] = s;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) X[(d + i) * kXs + d + j] = x[i];
+    for (int i = 0; i < 16; ++i) X[(d + i) * kXs + d + lane] = x[i];
   }
   __syncthreads();
-  // pairs of 16: W = C A' (kept in the unused block above the diagonal of M), then -B' W
+  // pairs of 16 (warp: pair and half of its columns), then the pair of 32 (warp:
+  // half of its rows and of its columns): W = C A' goes to the block above M's
+  // diagonal, which is not used otherwise; then -B' W
   {
-    const int p = tid >> 6, i = (tid >> 2) & 15, j = (tid & 3) * 4, c0 = 32 * p, r0 = c0 + 16;
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float m = M[(r0 + i) * kXs + c0 + k];
-      const float4 x = *reinterpret_cast<const float4*>(&X[(c0 + k) * kXs + c0 + j]);
-      w[0] = fmaf(m, x.x, w[0]); w[1] = fmaf(m, x.y, w[1]); w[2] = fmaf(m, x.z, w[2]); w[3] = fmaf(m, x.w, w[3]);
-    }
-    *reinterpret_cast<float4*>(&M[(c0 + i) * kXs + r0 + j]) = make_float4(w[0], w[1], w[2], w[3]);
+    const int c0 = 32 * (warp >> 1), r0 = c0 + 16, n0 = 8 * (warp & 1);
+    float w[1][4] = {};
+    mma_tf32x3<1, 2>(w, &M[r0 * kXs + c0], &X[c0 * kXs + c0 + n0], 1.f, lane);
+    store_c(&M[c0 * kXs + r0 + n0], w[0], lane);
     __syncthreads();
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float m = -X[(r0 + i) * kXs + r0 + k];
-      const float4 x = *reinterpret_cast<const float4*>(&M[(c0 + k) * kXs + r0 + j]);
-      y[0] = fmaf(m, x.x, y[0]); y[1] = fmaf(m, x.y, y[1]); y[2] = fmaf(m, x.z, y[2]); y[3] = fmaf(m, x.w, y[3]);
-    }
-    *reinterpret_cast<float4*>(&X[(r0 + i) * kXs + c0 + j]) = make_float4(y[0], y[1], y[2], y[3]);
-    // the block above the diagonal of each pair is zero
-    *reinterpret_cast<float4*>(&X[(c0 + i) * kXs + r0 + j]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    float y[1][4] = {};
+    mma_tf32x3<1, 2>(y, &X[r0 * kXs + r0], &M[c0 * kXs + r0 + n0], -1.f, lane);
+    store_c(&X[r0 * kXs + c0 + n0], y[0], lane);
+    const float zero[4] = {};
+    store_c(&X[c0 * kXs + r0 + n0], zero, lane);           // above the diagonal of the pair
   }
   __syncthreads();
-  // the pair of 32
   {
-    const int i = tid >> 2, j = (tid & 3) * 8;
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      const float m = M[(32 + i) * kXs + k];
-      const float4 x = *reinterpret_cast<const float4*>(&X[k * kXs + j]);
-      const float4 y = *reinterpret_cast<const float4*>(&X[k * kXs + j + 4]);
-      w[0] = fmaf(m, x.x, w[0]); w[1] = fmaf(m, x.y, w[1]); w[2] = fmaf(m, x.z, w[2]); w[3] = fmaf(m, x.w, w[3]);
-      w[4] = fmaf(m, y.x, w[4]); w[5] = fmaf(m, y.y, w[5]); w[6] = fmaf(m, y.z, w[6]); w[7] = fmaf(m, y.w, w[7]);
-    }
-    *reinterpret_cast<float4*>(&M[i * kXs + 32 + j]) = make_float4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<float4*>(&M[i * kXs + 32 + j + 4]) = make_float4(w[4], w[5], w[6], w[7]);
+    const int m0 = 16 * (warp >> 1), n0 = 16 * (warp & 1);
+    float w[2][4] = {};
+    mma_tf32x3<2, 4>(w, &M[(32 + m0) * kXs], &X[n0], 1.f, lane);
+    store_c(&M[m0 * kXs + 32 + n0], w[0], lane);
+    store_c(&M[m0 * kXs + 40 + n0], w[1], lane);
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      const float m = -X[(32 + i) * kXs + 32 + k];
-      const float4 x = *reinterpret_cast<const float4*>(&M[k * kXs + 32 + j]);
-      const float4 y = *reinterpret_cast<const float4*>(&M[k * kXs + 32 + j + 4]);
-      w[0] = fmaf(m, x.x, w[0]); w[1] = fmaf(m, x.y, w[1]); w[2] = fmaf(m, x.z, w[2]); w[3] = fmaf(m, x.w, w[3]);
-      w[4] = fmaf(m, y.x, w[4]); w[5] = fmaf(m, y.y, w[5]); w[6] = fmaf(m, y.z, w[6]); w[7] = fmaf(m, y.w, w[7]);
-    }
-    *reinterpret_cast<float4*>(&X[(32 + i) * kXs + j]) = make_float4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<float4*>(&X[(32 + i) * kXs + j + 4]) = make_float4(w[4], w[5], w[6], w[7]);
+    float y[2][4] = {};
+    mma_tf32x3<2, 4>(y, &X[(32 + m0) * kXs + 32], &M[32 + n0], -1.f, lane);
+    store_c(&X[(32 + m0) * kXs + n0], y[0], lane);
+    store_c(&X[(32 + m0) * kXs + n0 + 8], y[1], lane);
   }
   __syncthreads();
-  // T = X diag(b) as hi and lo
+  // T = X diag(b) below the diagonal, as hi and lo (its diagonal is b itself)
   for (int i = tid; i < L * 8; i += kPrepThreads) {
     const int t = i >> 3, cc = i & 7;
-    uint32_t hi[4], lo[4];
+    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+    if (8 * cc < t) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int s = 8 * cc + 2 * e;
-      const float x0 = s <= t ? X[t * kXs + s] * bs[s] : 0.f, x1 = s + 1 <= t ? X[t * kXs + s + 1] * bs[s + 1] : 0.f;
-      split2(x0, x1, hi[e], lo[e]);
+      for (int e = 0; e < 2; ++e) {
+        const int s = 8 * cc + 4 * e;
+        const float4 x = *reinterpret_cast<const float4*>(&X[t * kXs + s]);
+        const float4 bb = *reinterpret_cast<const float4*>(&bs[s]);
+        split2(s < t ? x.x * bb.x : 0.f, s + 1 < t ? x.y * bb.y : 0.f, hi[2 * e], lo[2 * e]);
+        split2(s + 2 < t ? x.z * bb.z : 0.f, s + 3 < t ? x.w * bb.w : 0.f, hi[2 * e + 1], lo[2 * e + 1]);
+      }
     }
     const uint32_t off = t * 128 + ((cc ^ (t & 7)) << 4);
     *reinterpret_cast<uint4*>(rec + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -333,12 +356,14 @@ delta_chain_kernel(const ChunkArgs a) {
       }
       split_a(P[2 * np], P[2 * np + 1], rh[np], rl[np]);
     }
-    // ---- U^T = R^T T^T: hi hi + lo hi + hi lo over the triangle s <= t
+    // ---- U^T = R^T T^T: the diagonal b in fp32, hi hi + lo hi + hi lo below it
     float U[8][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[n][e] = 0.f;
+    for (int n = 0; n < 8; ++n) {
+      const float2 bt = *reinterpret_cast<const float2*>(scal + kBeta * L + 8 * n + t2);
+      U[n][0] = bt.x * P[n][0]; U[n][1] = bt.y * P[n][1];
+      U[n][2] = bt.x * P[n][2]; U[n][3] = bt.y * P[n][3];
+    }
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
 #pragma unroll
@@ -473,7 +498,7 @@ template <int DK, bool OUT>
 cudaError_t chain(const ChunkArgs& a, int B, cudaStream_t stream) {
   // few heads: fewer warps per CTA, so that the slices of a head's value channels spread over the SMs
   const long long strips = (long long)B * a.H * (a.dv / 16);
-  if (strips >= 8 * 148 && a.dv == 128) return launch_chain<DK, 8, OUT>(a, B, stream);
+  if (strips >= 8 * 96 && a.dv == 128) return launch_chain<DK, 8, OUT>(a, B, stream);
   if (strips >= 4 * 148) return launch_chain<DK, 4, OUT>(a, B, stream);
   if (strips >= 2 * 148) return launch_chain<DK, 2, OUT>(a, B, stream);
   return launch_chain<DK, 1, OUT>(a, B, stream);
