@@ -505,6 +505,9 @@ cudaError_t chain(const ChunkArgs& a, int B, cudaStream_t stream) {
 }
 
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream) {
+  bool done = false;
+  const cudaError_t e = forward_chain_tc(a, B, dk, stream, &done);
+  if (done) return e;
   const bool out = a.s0 == nullptr;
   if (dk == 128) return out ? chain<128, true>(a, B, stream) : chain<128, false>(a, B, stream);
   return out ? chain<64, true>(a, B, stream) : chain<64, false>(a, B, stream);

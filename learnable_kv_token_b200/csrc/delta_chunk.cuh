@@ -127,5 +127,8 @@ cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t s
 // the chain of states; with s0 and u, writes their images instead of o
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
 
+// delta_chain_tc.cu: the same on tcgen05; *done = false if a tensor's strides do not suit TMA
+cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done);
+
 }  // namespace delta
 }  // namespace lte
