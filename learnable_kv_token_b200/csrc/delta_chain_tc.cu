@@ -13,11 +13,15 @@
 // V^T comes to TMEM as fp32 by one product with an identity.  Columns: S (DK),
 // S hi, S lo (DK / 2 each), P or R (64), V or U (64), U hi, U lo (32 each), O (64).
 //
-// Warps: 0-3 turn S, R and U (a thread per value channel, chain warps); 4-7
-// finish O (or, for the gradients, write the images of S and U); 8 loads (TMA
-// for K, Q and V, bulk copies for the record; two stages); 9 issues the MMAs.
-// What bounds a chunk is the chain P -> R -> U -> S: about 1400 cycles of MMAs
-// and, between them, the chain warps' passes over 256 values per thread.
+// Warps: 0-7 turn S, R and U (two threads per value channel, each with half of
+// the columns: chain warps); 8-11 finish O (or, for the gradients, write the
+// images of S and U); 12 loads (TMA for K, Q and V, bulk copies for the record;
+// two stages); 13 issues the MMAs.
+// What bounds a chunk is the chain P -> R -> U -> S, so everything else is kept
+// off it: a pass publishes what the next product needs before it does the rest
+// (e^{G_L} S, U for O); S comes and goes in two halves of its columns, so a pass
+// over one half runs beside the product on the other; products with T and A
+// leave out the columns above the diagonal.
 //
 // Rows of the last chunk behind the sequence's length are set to zero in shared
 // memory before use, so what lies there (NaN, another sequence) does not enter.
@@ -33,19 +37,22 @@ namespace chaintc {
 
 using namespace tc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
 constexpr uint32_t kHalf = L * 128;                          // [64 tokens][64 channels] bf16, 128B-swizzled
 // a stage: K, Q, V (two halves each), then T hi, T lo, A, scalars as in the record
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kV = 4 * kHalf, kR = 6 * kHalf;
 constexpr uint32_t kScalOff = kR + 3 * kImg;
 constexpr uint32_t kStage = (kScalOff + kScal + 1023) / 1024 * 1024;
-constexpr uint32_t kIdent = 2 * kStage, kBars = kIdent + kImg, kSmem = kBars + 256;
+// then the identity and a chunk of O as token rows (two halves)
+constexpr uint32_t kIdent = 2 * kStage, kOut = kIdent + kImg, kBars = kOut + 2 * kHalf, kSmem = kBars + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // mbarriers; those without [] complete once per chunk
-enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bP = 6, bRr = 7, bU = 8, bUr = 9, bS = 10, bQS = 11, bOs = 12,
-             bO = 13, bOf = 14, bSread = 15, bUread = 16, bDrain = 17, kBarCount = 18 };
+enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bP = 7, bRr = 8, bU = 9, bUr = 10, bUh = 11, bS = 12, bQS = 14,
+             bOs = 15, bO = 16, bOf = 17, bSread = 18, bUread = 19, bDrain = 20, kBarCount = 21 };
+// columns; R and the scaled U lie as hi (16) and lo (16) over each 32 columns of P and U
 constexpr uint32_t kColS = 0, kColPR = 256, kColVU = 320, kColUH = 384, kColUL = 416, kColO = 448;
+__device__ __forceinline__ uint32_t pair_col(int ks, int lo) { return 32 * (ks >> 1) + 16 * lo + 8 * (ks & 1); }
 
 __device__ __forceinline__ uint32_t idesc2(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
@@ -56,20 +63,53 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// 16 pairs of values -> bf16 hi and lo words
-__device__ __forceinline__ void split32(const float (&x)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) split2(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+// two fp32 values in one register pair
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ void as_float(const uint32_t (&r)[32], float (&x)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+__device__ __forceinline__ void unf2(uint64_t r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a pair -> bf16 hi and lo words (as split2)
+__device__ __forceinline__ void split_pair(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float x0, x1;
+  unf2(x, x0, x1);
+  hi = pack_bf16(x0, x1);
+  unf2(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x), x0, x1);
+  lo = pack_bf16(x0, x1);
+}
+template <int N>
+__device__ __forceinline__ void split_pairs(const uint64_t (&x)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) split_pair(x[e], hi[e], lo[e]);
+}
+// columns of this warp's lanes <-> registers, by count
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[32]) { tmem_st32(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) { return f2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 
 template <int DK, int DV, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const ChunkArgs a) {
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                      const ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
   constexpr int kHK = DK / 64, kHV = DV / 64;                // 64-channel halves
@@ -84,8 +124,9 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
-      const bool warps4 = i == bSr || i == bRr || i == bUr || i == bOs || i == bOf || i == bSread || i == bUread;
-      mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 9 : warps4 ? 4 : 1);
+      const bool chain = i == bSr || i == bSr + 1 || i == bRr || i == bUr || i == bUh;      // 8 chain warps
+      const bool out = i == bOs || i == bOf || i == bSread || i == bUread;                  // 4 output warps
+      mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 13 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -98,7 +139,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     *reinterpret_cast<uint4*>(sm + kIdent + n * 128 + ((cc ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   fence_proxy_async();
-  if (warp == 9) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(tmem_slot)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -111,7 +152,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   int loaded = 0;                                            // chunks requested (producer)
   bool issued = false;                                       // MMAs issued (MMA warp)
 
-  if (warp == 8) {
+  if (warp == 12) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + (long long)u * a.chunks * kRecBytes;
     for (int c = 0; c < n_chunks; ++c) {
@@ -149,11 +190,11 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (lane == 0) mbar_arrive(bar(bFull + s));
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ================================================================= MMAs
     const uint32_t id_tok = idesc2(128, L, false, false);      // N = tokens, B [n][k]
     const uint32_t id_vt = idesc2(128, L, true, false);        // V^T from [token][channel]
-    const uint32_t id_s = idesc2(128, DK, false, true);        // N = key channels, B [k][n]
+    const uint32_t id_s = idesc2(128, 64, false, true);        // N = 64 key channels, B [k][n]
     const uint64_t ident = sdesc(s0 + kIdent, 16, 1024);
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
@@ -168,17 +209,22 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         for (int ks = 0; ks < L / 16; ++ks)
           mma_f16(tmem + kColVU, dv + ((ks * 2048) >> 4), ident + ((ks * 32) >> 4), id_vt, ks > 0);
       }
-      if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0))) break;
-      tc_fence_after();
-      if (elect_one()) {                                       // P^T = S K^T
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p) {                            // P^T = S K^T, by halves of S's columns
+        if (ok) ok = wwait(bar(bSr + p), ph, abort_flag, nullptr, 0);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            mma_f16_ts(tmem + kColPR, tmem + (p ? kColSl : kColSh) + 8 * ks, dk + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
-                       id_tok, p + ks > 0);
-        mma_commit(bar(bP));
+          for (int i = 0; i < DK / 16; ++i) {
+            const int ks = p * (DK / 32) + i / 2;
+            mma_f16_ts(tmem + kColPR, tmem + (i & 1 ? kColSl : kColSh) + 8 * ks, dk + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                       id_tok, p + i > 0);
+          }
+          if (p == 1) mma_commit(bar(bP));
+        }
       }
+      if (!ok) break;
       if (OUT) {                                               // S Q^T
         if (c > 0 && !(ok = wwait(bar(bOf), (c - 1) & 1, abort_flag, nullptr, 0))) break;
         tc_fence_after();
@@ -191,27 +237,34 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       if (!(ok = wwait(bar(bRr), ph, abort_flag, nullptr, 0))) break;
       tc_fence_after();
-      if (elect_one()) {                                       // U^T = R^T T^T
+      if (elect_one()) {                                       // U^T = R^T T^T: columns t >= 16 ks
 #pragma unroll
         for (int p = 0; p < 3; ++p)                            // hi hi, lo hi, hi lo
 #pragma unroll
           for (int ks = 0; ks < L / 16; ++ks)
-            mma_f16_ts(tmem + kColVU, tmem + kColPR + (p == 1 ? 32 : 0) + 8 * ks,
-                       dt + (((p == 2 ? kImg : 0) + ks * 32) >> 4), id_tok, p + ks > 0);
+            mma_f16_ts(tmem + kColVU + 16 * ks, tmem + kColPR + pair_col(ks, p == 1),
+                       dt + (((p == 2 ? kImg : 0) + ks * (16 * 128 + 32)) >> 4), idesc2(128, L - 16 * ks, false, false),
+                       p + ks > 0);
         mma_commit(bar(bU));
       }
       if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
       tc_fence_after();
-      if (elect_one()) {                                       // S += (U diag(e^{G_L - G}))^T K
-        const uint64_t dkn = sdesc(d + kK, kHalf, 1024);
+      if (elect_one()) {                                       // S += (U diag(e^{G_L - G}))^T K, by halves of its columns
+        constexpr int kN = DK == 128 ? 2 : 1;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int n = 0; n < kN; ++n) {
+          const uint64_t dkn = sdesc(d + kK + n * kHalf, kHalf, 1024);
 #pragma unroll
-          for (int ks = 0; ks < L / 16; ++ks)
-            mma_f16_ts(tmem + kColS, tmem + kColVU + 32 * p + 8 * ks, dkn + ((ks * 2048) >> 4), id_s, 1u);
-        mma_commit(bar(bS));
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < L / 16; ++ks)
+              mma_f16_ts(tmem + kColS + 64 * n, tmem + kColVU + pair_col(ks, p), dkn + ((ks * 2048) >> 4), id_s, 1u);
+          mma_commit(bar(bS + n));
+        }
+        if (kN == 1) mma_commit(bar(bS + 1));
       }
-      if (OUT) {                                               // O^T += U^T A^T
+      if (OUT) {                                               // O^T += U^T A^T, columns t >= 16 ks
+        if (!(ok = wwait(bar(bUh), ph, abort_flag, nullptr, 0))) break;
         if (!(ok = wwait(bar(bOs), ph, abort_flag, nullptr, 0))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -219,7 +272,8 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int ks = 0; ks < L / 16; ++ks)
-              mma_f16_ts(tmem + kColO, tmem + (p ? kColUL : kColUH) + 8 * ks, dt + ((2 * kImg + ks * 32) >> 4), id_tok, 1u);
+              mma_f16_ts(tmem + kColO + 16 * ks, tmem + (p ? kColUL : kColUH) + 8 * ks,
+                         dt + ((2 * kImg + ks * (16 * 128 + 32)) >> 4), idesc2(128, L - 16 * ks, false, false), 1u);
           mma_commit(bar(bO));
         }
       }
@@ -231,12 +285,12 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       __syncwarp();
       mbar_drain(bar(bDrain), 0);
     }
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ========================================================== chain warps
-    const int row = warp * 32 + lane;                          // value channel = TMEM lane
-    const uint32_t la = tmem + ((uint32_t)(warp * 32) << 16);
+    constexpr int QC = DK / 4;                                 // S columns per thread and half
+    const int row = (warp & 3) * 32 + lane, hc = warp >> 2;    // value channel = TMEM lane; which columns
+    const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const long long srow = ((long long)u * DV + (row < DV ? row : 0)) * DK;
-    auto scal_of = [&](int c) { return reinterpret_cast<const float*>(sm + (c & 1) * kStage + kScalOff); };
     auto arrive = [&](int i) {                                 // this warp's TMEM writes are done
       tmem_wait_st();
       tc_fence_before();
@@ -246,147 +300,142 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
       if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
-      const float* scal = scal_of(c);
-      // ---- the state: bf16 hi and lo, and e^{G_L} S for this chunk's update
-      if (c > 0) {
-        if (!(ok = wwait(bar(bS), (c - 1) & 1, abort_flag, nullptr, 0))) break;
-        if (!OUT && !(ok = wwait(bar(bSread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
-        tc_fence_after();
-      }
-      const float el = scal[kEG * L + L - 1];
+      const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
+      // ---- the state as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
+      if (!OUT && c > 0 && !(ok = wwait(bar(bSread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+      uint64_t S[2][QC / 2];
 #pragma unroll
-      for (int j = 0; j < DK / 32; ++j) {
-        float x[32];
-        uint32_t r[32], hi[16], lo[16];
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
         if (c > 0) {
-          tmem_ld32(la + kColS + 32 * j, r);
+          if (ok) ok = wwait(bar(bS + p), (c - 1) & 1, abort_flag, nullptr, 0);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t r[QC];
+          tm_ld(la + kColS + c0, r);
           tmem_wait_ld();
-          as_float(r, x);
+#pragma unroll
+          for (int e = 0; e < QC / 2; ++e) S[p][e] = pair_of(r + 2 * e);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < QC / 4; ++e) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.s_in != nullptr && row < DV) v = reinterpret_cast<const float4*>(a.s_in + srow + 32 * j)[e];
-            x[4 * e] = v.x; x[4 * e + 1] = v.y; x[4 * e + 2] = v.z; x[4 * e + 3] = v.w;
+            if (a.s_in != nullptr && row < DV) v = reinterpret_cast<const float4*>(a.s_in + srow + c0)[e];
+            S[p][2 * e] = f2(v.x, v.y);
+            S[p][2 * e + 1] = f2(v.z, v.w);
           }
         }
-        split32(x, hi, lo);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(x[e] * el);
-        tmem_st16(la + kColSh + 16 * j, hi);
-        tmem_st16(la + kColSl + 16 * j, lo);
-        tmem_st32(la + kColS + 32 * j, r);
+        uint32_t hi[QC / 2], lo[QC / 2];
+        split_pairs(S[p], hi, lo);
+        tm_st(la + kColSh + c0 / 2, hi);
+        tm_st(la + kColSl + c0 / 2, lo);
+        arrive(bSr + p);
       }
-      arrive(bSr);
-      // ---- R^T = V^T - P^T diag(e^G)
+      if (!ok) break;
+      // ---- e^{G_L} S for this chunk's update (published with R)
+      {
+        const float el = scal[kEG * L + L - 1];
+        const uint64_t el2 = f2(el, el);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t r[QC];
+#pragma unroll
+          for (int e = 0; e < QC / 2; ++e) {
+            float x, y;
+            unf2(mul2(S[p][e], el2), x, y);
+            r[2 * e] = __float_as_uint(x);
+            r[2 * e + 1] = __float_as_uint(y);
+          }
+          tm_st(la + kColS + QC * (2 * p + hc), r);
+        }
+      }
+      // ---- R^T = V^T - P^T diag(e^G), tokens 32 hc .. + 31
+      uint64_t gm[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * hc + 4 * e);
+        gm[2 * e] = f2(-g.x, -g.y);
+        gm[2 * e + 1] = f2(-g.z, -g.w);
+      }
       if (!(ok = wwait(bar(bP), ph, abort_flag, nullptr, 0))) break;
       tc_fence_after();
-      float R[2][32];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t p[32], v[32], hi[16], lo[16];
-        tmem_ld32(la + kColPR + 32 * j, p);
-        tmem_ld32(la + kColVU + 32 * j, v);
+      uint64_t R[16];
+      {
+        uint32_t x[32], v[32], hi[16], lo[16];
+        tmem_ld32(la + kColPR + 32 * hc, x);
+        tmem_ld32(la + kColVU + 32 * hc, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * j + e);
-          R[j][e] = fmaf(-g.x, __uint_as_float(p[e]), __uint_as_float(v[e]));
-          R[j][e + 1] = fmaf(-g.y, __uint_as_float(p[e + 1]), __uint_as_float(v[e + 1]));
-          R[j][e + 2] = fmaf(-g.z, __uint_as_float(p[e + 2]), __uint_as_float(v[e + 2]));
-          R[j][e + 3] = fmaf(-g.w, __uint_as_float(p[e + 3]), __uint_as_float(v[e + 3]));
-        }
-        split32(R[j], hi, lo);
-        // hi over columns 0-31 of P's region, lo over 32-63: both halves of P are read first
-        if (j == 0) {
-          uint32_t p1[32], v1[32];
-          tmem_ld32(la + kColPR + 32, p1);
-          tmem_ld32(la + kColVU + 32, v1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 + e);
-            R[1][e] = fmaf(-g.x, __uint_as_float(p1[e]), __uint_as_float(v1[e]));
-            R[1][e + 1] = fmaf(-g.y, __uint_as_float(p1[e + 1]), __uint_as_float(v1[e + 1]));
-            R[1][e + 2] = fmaf(-g.z, __uint_as_float(p1[e + 2]), __uint_as_float(v1[e + 2]));
-            R[1][e + 3] = fmaf(-g.w, __uint_as_float(p1[e + 3]), __uint_as_float(v1[e + 3]));
-          }
-          tmem_st16(la + kColPR, hi);
-          tmem_st16(la + kColPR + 32, lo);
-          split32(R[1], hi, lo);
-          tmem_st16(la + kColPR + 16, hi);
-          tmem_st16(la + kColPR + 48, lo);
-          break;
-        }
+        for (int e = 0; e < 16; ++e) R[e] = fma2(gm[e], pair_of(x + 2 * e), pair_of(v + 2 * e));
+        split_pairs(R, hi, lo);
+        tmem_st16(la + kColPR + 32 * hc, hi);
+        tmem_st16(la + kColPR + 32 * hc + 16, lo);
       }
       arrive(bRr);
-      // ---- U = T R + b R; U and U diag(e^{G_L - G}) as hi and lo
+      // ---- U = T R + b R; first U diag(e^{G_L - G}) as hi and lo, then U
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 g = *reinterpret_cast<const float4*>(scal + kBeta * L + 32 * hc + 4 * e);
+        R[2 * e] = mul2(R[2 * e], f2(g.x, g.y));
+        R[2 * e + 1] = mul2(R[2 * e + 1], f2(g.z, g.w));
+        const float4 l = *reinterpret_cast<const float4*>(scal + kLam * L + 32 * hc + 4 * e);
+        gm[2 * e] = f2(l.x, l.y);
+        gm[2 * e + 1] = f2(l.z, l.w);
+      }
+      if (lane == 0) mbar_arrive(bar(bEmpty + s));             // the scalars have been read
       if (!(ok = wwait(bar(bU), ph, abort_flag, nullptr, 0))) break;
-      if (!OUT && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
       tc_fence_after();
       {
-        uint32_t r0[32], r1[32];
-        tmem_ld32(la + kColVU, r0);
-        tmem_ld32(la + kColVU + 32, r1);
+        uint32_t x[32], hi[16], lo[16];
+        tmem_ld32(la + kColVU + 32 * hc, x);
         tmem_wait_ld();
+        const uint64_t one = f2(1.f, 1.f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x[32];
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(scal + kBeta * L + 32 * j + e);
-            const uint32_t* r = j ? r1 : r0;
-            x[e] = fmaf(g.x, R[j][e], __uint_as_float(r[e]));
-            x[e + 1] = fmaf(g.y, R[j][e + 1], __uint_as_float(r[e + 1]));
-            x[e + 2] = fmaf(g.z, R[j][e + 2], __uint_as_float(r[e + 2]));
-            x[e + 3] = fmaf(g.w, R[j][e + 3], __uint_as_float(r[e + 3]));
-          }
-          split32(x, hi, lo);
-          tmem_st16(la + kColUH + 16 * j, hi);
-          tmem_st16(la + kColUL + 16 * j, lo);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(scal + kLam * L + 32 * j + e);
-            x[e] *= g.x; x[e + 1] *= g.y; x[e + 2] *= g.z; x[e + 3] *= g.w;
-          }
-          split32(x, hi, lo);
-          tmem_st16(la + kColVU + 16 * j, hi);
-          tmem_st16(la + kColVU + 32 + 16 * j, lo);
+        for (int e = 0; e < 16; ++e) {
+          R[e] = fma2(pair_of(x + 2 * e), one, R[e]);
+          gm[e] = mul2(R[e], gm[e]);
         }
+        split_pairs(gm, hi, lo);
+        tmem_st16(la + kColVU + 32 * hc, hi);
+        tmem_st16(la + kColVU + 32 * hc + 16, lo);
+        arrive(bUr);
+        split_pairs(R, hi, lo);
+        if (!OUT && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+        tmem_st16(la + kColUH + 16 * hc, hi);
+        tmem_st16(la + kColUL + 16 * hc, lo);
+        arrive(bUh);
       }
-      arrive(bUr);
-      if (lane == 0) mbar_arrive(bar(bEmpty + s));
     }
     if (ok && n_chunks > 0) {
-      ok = wwait(bar(bS), (n_chunks - 1) & 1, abort_flag, nullptr, 0);
+      ok = wwait(bar(bS), (n_chunks - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n_chunks - 1) & 1, abort_flag, nullptr, 0);
       tc_fence_after();
     }
     if (a.s_out != nullptr) {
 #pragma unroll
-      for (int j = 0; j < DK / 32; ++j) {
-        uint32_t r[32];
-        tmem_ld32(la + kColS + 32 * j, r);
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
+        uint32_t r[QC];
+        tm_ld(la + kColS + c0, r);
         tmem_wait_ld();
         if (row < DV) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < QC / 4; ++e) {
             float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
             if (n_chunks == 0)
               v = a.s_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                    : reinterpret_cast<const float4*>(a.s_in + srow + 32 * j)[e];
+                                    : reinterpret_cast<const float4*>(a.s_in + srow + c0)[e];
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
-            reinterpret_cast<float4*>(a.s_out + srow + 32 * j)[e] = v;
+            reinterpret_cast<float4*>(a.s_out + srow + c0)[e] = v;
           }
         }
       }
     }
   } else {
     // ==================================================== O, or the images
-    const int quad = warp - 4, row = quad * 32 + lane;
+    const int quad = warp - 8, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    __nv_bfloat16* op = a.o + b * a.os.b + h * a.os.h + row;
+    __nv_bfloat16* op = a.o + b * a.os.b + h * a.os.h;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
       if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
@@ -426,16 +475,37 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bOf));
-        if (row < DV) {                                        // a warp writes 64 bytes of each token's row
-          const int n = min(L, len - c * L);
-          __nv_bfloat16* o = op + (long long)c * L * a.os.t;
+        // token rows in shared memory, then one TMA store per half; the last
+        // chunk's rows behind the sequence are not written
+        if (tid == 256) bulk_wait_read();                      // the chunk before has left the buffer
+        bar_sync(1, 128);
+        if (row < DV) {
+          const uint32_t col = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
+          const int cc = (row & 63) >> 3;
 #pragma unroll
           for (int t = 0; t < L; ++t)
-            if (t < n) o[(long long)t * a.os.t] = __float2bfloat16_rn(__uint_as_float(r[t >> 5][t & 31]));
+            *reinterpret_cast<__nv_bfloat16*>(sm + kOut + col + t * 128 + ((cc ^ (t & 7)) << 4)) =
+                __float2bfloat16_rn(__uint_as_float(r[t >> 5][t & 31]));
+        }
+        const int n = len - c * L;
+        if (n >= L) {
+          fence_proxy_async();
+          bar_sync(1, 128);
+          if (tid == 256) {
+            for (int i = 0; i < kHV; ++i) tma_store_4d(&tm_o, s0 + kOut + i * kHalf, 64 * i, h, c * L, b);
+            bulk_commit();
+          }
+        } else {
+          bar_sync(1, 128);
+          for (int i = tid - 256; i < n * (DV / 8); i += 128) {
+            const int t = i / (DV / 8), cc = i % (DV / 8);
+            *reinterpret_cast<uint4*>(op + (long long)(c * L + t) * a.os.t + cc * 8) =
+                *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
+          }
         }
       } else {
         if (lane == 0) mbar_arrive(bar(bEmpty + s));
-        if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0))) break;
         tc_fence_after();
         // images in 8 x 8 blocks: a row's 16 bytes of each column block
         const int rb = row >> 3, r7 = row & 7;
@@ -457,7 +527,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bSread));
-        if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bUh), ph, abort_flag, nullptr, 0))) break;
         tc_fence_after();
         uint32_t r[2][32];
         tmem_ld32(la + kColUH, r[0]);
@@ -478,15 +548,16 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
     }
   }
+  if (OUT && tid == 256) bulk_wait_all();                      // output stores complete before exit
   // copies in flight land before exit (only after a wait gave up)
-  if (warp == 8 && *abort_flag) {
+  if (warp == 12 && *abort_flag) {
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
       if (i * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
       else mbar_drain(bar(bTail), 0);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9)
+  if (warp == 13)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -504,7 +575,7 @@ template <int DK, int DV, bool OUT>
 cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  delta_chain_tc_kernel<DK, DV, OUT><<<(unsigned)(B * a.H), kThreads, kSmem, stream>>>(m[0], m[1], m[2], a);
+  delta_chain_tc_kernel<DK, DV, OUT><<<(unsigned)(B * a.H), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
 template <bool OUT>
@@ -516,9 +587,10 @@ cudaError_t dispatch(const CUtensorMap* m, const ChunkArgs& a, int B, int dk, cu
 }  // namespace chaintc
 
 cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done) {
-  CUtensorMap m[3];
+  CUtensorMap m[4];
   *done = chaintc::map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) && chaintc::map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) &&
-          chaintc::map_of(&m[2], a.v, a.dv, a.H, a.T, B, a.vs);
+          chaintc::map_of(&m[2], a.v, a.dv, a.H, a.T, B, a.vs) &&
+          (a.s0 != nullptr || chaintc::map_of(&m[3], a.o, a.dv, a.H, a.T, B, a.os));
   if (!*done) return cudaSuccess;
   return a.s0 == nullptr ? chaintc::dispatch<true>(m, a, B, dk, stream) : chaintc::dispatch<false>(m, a, B, dk, stream);
 }
