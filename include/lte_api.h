@@ -517,7 +517,8 @@ typedef struct {
 
 enum { LTE_GDR_WS_PREFILL = 0, LTE_GDR_WS_BACKWARD = 1 };
 
-/* Bytes of workspace that a call needs (0 on invalid dims). */
+/* Bytes of workspace that a call needs (0 on invalid dims, and for the
+ * token-by-token forms, which take workspace = NULL). */
 size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which);
 
 /* lte_gdr_prefill -- T tokens per sequence.  state_in (nullable: zeros) and

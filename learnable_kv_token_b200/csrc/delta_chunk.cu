@@ -17,6 +17,11 @@ namespace delta {
 constexpr int kPrepThreads = 128;
 constexpr int kXs = 68;                                   // row stride of M and X in floats
 
+__device__ __forceinline__ float ex2_approx(float x) {     // relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // x = hi + lo in TF32 (11 bits each); the tensor core drops the lower bits of lo
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
@@ -57,10 +62,10 @@ __device__ __forceinline__ void store_c(float* p, const float* c, int lane) {
 }
 
 template <int DK, bool A_LO>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 5)
 delta_prepare_kernel(const ChunkArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ double G[L];
+  __shared__ __align__(16) float2 G2[L];                  // log2(e) G as a float pair
   __shared__ __align__(16) float bs[L];
   const int u = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
@@ -97,8 +102,10 @@ delta_prepare_kernel(const ChunkArgs a) {
     }
     const double last = __shfl_sync(0xffffffffu, sum, 31);
     const double G0 = sum - x1, G1 = sum;
-    G[2 * lane] = G0;
-    G[2 * lane + 1] = G1;
+    constexpr double kLog2e = 1.4426950408889634;
+    const float h0 = (float)(G0 * kLog2e), h1 = (float)(G1 * kLog2e);
+    G2[2 * lane] = make_float2(h0, (float)(G0 * kLog2e - h0));
+    G2[2 * lane + 1] = make_float2(h1, (float)(G1 * kLog2e - h1));
     bs[2 * lane] = b0;
     bs[2 * lane + 1] = b1;
     float2* out = reinterpret_cast<float2*>(scal) + lane;
@@ -137,22 +144,28 @@ delta_prepare_kernel(const ChunkArgs a) {
   float* M = reinterpret_cast<float*>(sm);
   float* X = M + L * kXs;
   uint8_t* img = reinterpret_cast<uint8_t*>(X);           // A's image, before X is formed
+  const int ta = 16 * warp + g;
+  const float2 Ga = G2[ta], Gb = G2[ta + 8];
+  const float ba = bs[ta], bb = bs[ta + 8];
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
+    const int s = 8 * n + t2;
+    const bool below = n <= 2 * warp + 1;                   // else nothing of this tile is at or below the diagonal
+    const float4 Gs = *reinterpret_cast<const float4*>(&G2[s]);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int t = 16 * warp + g + 8 * r, s = 8 * n + t2;
-      float m[2], av[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float d = s + e <= t ? expf((float)(G[t] - G[s + e])) : 0.f;
-        m[e] = s + e < t ? bs[t] * (d * kk[n][2 * r + e]) : 0.f;
-        av[e] = s + e <= t ? a.scale * (d * qk[n][2 * r + e]) : 0.f;
-      }
-      *reinterpret_cast<float2*>(&M[t * kXs + s]) = make_float2(m[0], m[1]);
-      uint32_t hi, lo;
-      split2(av[0], av[1], hi, lo);
+      const int t = ta + 8 * r;
       const uint32_t off = t * 128 + ((n ^ (t & 7)) << 4) + t2 * 2;
+      uint32_t hi = 0, lo = 0;
+      if (below) {
+        const float2 Gt = r ? Gb : Ga;
+        const float bt = r ? bb : ba;
+        const float d0 = s <= t ? ex2_approx((Gt.x - Gs.x) + (Gt.y - Gs.y)) : 0.f;
+        const float d1 = s + 1 <= t ? ex2_approx((Gt.x - Gs.z) + (Gt.y - Gs.w)) : 0.f;
+        *reinterpret_cast<float2*>(&M[t * kXs + s]) =
+            make_float2(s < t ? bt * (d0 * kk[n][2 * r]) : 0.f, s + 1 < t ? bt * (d1 * kk[n][2 * r + 1]) : 0.f);
+        split2(a.scale * (d0 * qk[n][2 * r]), a.scale * (d1 * qk[n][2 * r + 1]), hi, lo);
+      }
       *reinterpret_cast<uint32_t*>(img + off) = hi;
       if (A_LO) *reinterpret_cast<uint32_t*>(img + kImg + off) = lo;
     }
@@ -518,7 +531,7 @@ cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream
 bool delta_chunked(const lte_gdr_dims* d) { return d->dtype == LTE_BF16 && d->T > delta::kFewTokens; }
 
 size_t delta_prefill_bytes(const lte_gdr_dims* d) {
-  if (!delta_chunked(d)) return 16;
+  if (!delta_chunked(d)) return 0;
   return (size_t)d->B * d->H * ((d->T + delta::L - 1) / delta::L) * delta::rec_bytes(false);
 }
 

@@ -577,8 +577,8 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
       (st = strides_of(v_strides, d->T, d->H, d->dv, d->dtype, &a.vs)) != LTE_OK ||
       (st = strides_of(o_strides, d->T, d->H, d->dv, d->dtype, &a.os)) != LTE_OK)
     return st;
-  if (workspace == nullptr || ws_bytes < lte_gdr_workspace_bytes(d, LTE_GDR_WS_PREFILL))
-    return LTE_ERR_WORKSPACE;
+  const size_t need = lte::delta_prefill_bytes(d);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return LTE_ERR_WORKSPACE;
   a.d = d; a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lens = lens;
   a.s_in = state_in; a.o = o; a.s_out = state_out; a.scratch = workspace;
   return from_cuda(lte::delta_prefill(a, as_stream(stream)));

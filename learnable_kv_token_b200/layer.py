@@ -337,6 +337,15 @@ def _on_device(fn):
     return call
 
 
+def _new(x, lens=None):
+    """A contiguous tensor like x, zeros if some of its rows lie behind a sequence's length."""
+    return (torch.empty_like if lens is None else torch.zeros_like)(x, memory_format=torch.contiguous_format)
+
+
+def _workspace(x, n):
+    return x.new_empty(n, dtype=torch.uint8) if n else None
+
+
 def _norm_struct(q, k, p, positions):
     if k.device != q.device:
         raise ValueError("q and k are on different devices")
@@ -352,11 +361,11 @@ def qk_norm_rope(q, k, p: QKNorm, positions=None, q_out=None, k_out=None):
     be q and k if those are contiguous.  Also takes `stream`."""
     c = _norm_struct(q, k, p, positions)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new(q)
     else:
         _check(q_out, "q_out", q.shape, q.dtype, q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+        k_out = _new(k)
     else:
         _check(k_out, "k_out", k.shape, k.dtype, q.device)
     L.lte_qk_norm_rope(c, q, k, q_out, k_out, positions)
@@ -373,11 +382,11 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, p: QKNorm, positions=None):
         raise ValueError("gradients are fp32 or of q's dtype")
     _check(dq_out, "dq_out", q.shape, dq_out.dtype, q.device)
     _check(dk_out, "dk_out", k.shape, dq_out.dtype, q.device)
-    dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    dq, dk = _new(q), _new(k)
     dwq = dwk = None
     if p.kind != "none":
         dwq, dwk = (None if w is None else torch.empty_like(w) for w in (p.wq, p.wk))
-    ws = torch.empty(L.lte_qk_norm_backward_workspace_bytes(c), dtype=torch.uint8, device=q.device)
+    ws = _workspace(q, L.lte_qk_norm_backward_workspace_bytes(c))
     L.lte_qk_norm_rope_backward(c, q, k, dq_out, dk_out, dq, dk, dwq, dwk, ws, positions)
     return dq, dk, dwq, dwk
 
@@ -409,11 +418,11 @@ def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out
     if state is not None:
         _check(state, "state", shape, torch.float32, q.device)
     if state_out is None:
-        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        state_out = g.new_empty(shape)
     else:
         _check(state_out, "state_out", shape, torch.float32, q.device)
-    o = (torch.empty if lens is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
-    ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL), dtype=torch.uint8, device=q.device)
+    o = _new(v, lens)
+    ws = _workspace(q, L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL))
     L.lte_gdr_prefill(d, q, k, v, g, beta, o, state_out, ws, state, lens)
     return o, state_out
 
@@ -431,10 +440,9 @@ def delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lens=None, sca
         _check(dstate, "dstate", shape, torch.float32, q.device)
     if do.shape != v.shape or do.dtype is not v.dtype or do.device != v.device:
         raise ValueError("do has v's shape, dtype and device")
-    make = torch.empty if lens is None else torch.zeros
-    grads = [make(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v, g, beta)]
-    ds = torch.empty(shape, dtype=torch.float32, device=q.device)
-    ws = torch.empty(L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD), dtype=torch.uint8, device=q.device)
+    grads = [_new(x, lens) for x in (q, k, v, g, beta)]
+    ds = g.new_empty(shape)
+    ws = _workspace(q, L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD))
     L.lte_gdr_backward(d, q, k, v, g, beta, do, *grads, ws, state, lens, dstate, ds)
     return (*grads, ds)
 

@@ -345,6 +345,10 @@ def _ref_strides(t):
     return C.byref(lte_strides(b, n, h))
 
 
+def _ws_bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
 def _check_status(name, st):
     if st != 0:
         raise LteError(name, st)
@@ -365,7 +369,7 @@ def lte_gdr_prefill(dims, q, k, v, g, beta, o, state_out, workspace, state_in=No
         C.byref(dims), _addr(q), _addr(k), _addr(v), _ref_strides(q), _ref_strides(k),
         _ref_strides(v), _addr(g), _addr(beta), _addr(lens), _addr(state_in), _addr(o),
         _ref_strides(o), _addr(state_out), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _raw(stream)))
+        _ws_bytes(workspace), _raw(stream)))
 
 
 def lte_gdr_backward(dims, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, workspace, state_in=None,
@@ -375,7 +379,7 @@ def lte_gdr_backward(dims, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, workspac
         _ref_strides(v), _addr(g), _addr(beta), _addr(lens), _addr(state_in), _addr(do),
         _ref_strides(do), _addr(dstate_out), _addr(dq), _addr(dk), _addr(dv), _addr(dg),
         _addr(dbeta), _addr(dstate_in), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _raw(stream)))
+        _ws_bytes(workspace), _raw(stream)))
 
 
 def lte_gdr_decode_step(dims, q_t, k_t, v_t, g_t, beta_t, o_t, state, stream=None):
@@ -407,4 +411,4 @@ def lte_qk_norm_rope_backward(norm, q, k, dq_out, dk_out, dq, dk, dwq, dwk, work
     _check_status("lte_qk_norm_rope_backward", _lib.lte_qk_norm_rope_backward(
         C.byref(norm), _addr(q), _addr(k), _ref_strides(q), _ref_strides(k), _addr(positions),
         _addr(dq_out), _addr(dk_out), dtype_code(dq_out.dtype), _addr(dq), _addr(dk), _addr(dwq),
-        _addr(dwk), _addr(workspace), workspace.numel() * workspace.element_size(), _raw(stream)))
+        _addr(dwk), _addr(workspace), _ws_bytes(workspace), _raw(stream)))
