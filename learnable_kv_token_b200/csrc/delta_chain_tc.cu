@@ -23,6 +23,13 @@
 // over one half runs beside the product on the other; products with T and A
 // leave out the columns above the diagonal.
 //
+// Long sequences of few heads are cut into segments of chunks, one CTA each.  A
+// row of S goes through a segment by an affine map s -> s X + n that is the same
+// X for every row, so a first pass finds, for all segments at once, n (the chain
+// from a zero state) and X (the chain from the identity with no values); a small
+// kernel carries the states from segment to segment, and a second pass runs every
+// segment from its state for O.  Twice the work on many times the SMs.
+//
 // Rows of the last chunk behind the sequence's length are set to zero in shared
 // memory before use, so what lies there (NaN, another sequence) does not enter.
 // Every mbarrier wait is bounded; a CTA that gives up writes NaN to its state.
@@ -105,7 +112,10 @@ __device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[8]) {
 }
 __device__ __forceinline__ uint64_t pair_of(const uint32_t* r) { return f2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 
-template <int DK, int DV, bool OUT>
+// what a chain leaves besides the state
+enum : int { kImages = 0, kO = 1, kStateOnly = 2 };
+
+template <int DK, int DV, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -113,14 +123,23 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   extern __shared__ __align__(1024) uint8_t sm[];
   constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
   constexpr int kHK = DK / 64, kHV = DV / 64;                // 64-channel halves
-  const int u = blockIdx.x, b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
+  constexpr bool OUT = KIND == kO;
+  // the unit's segment: for kStateOnly first n of segments 0 .. G - 2, then X of 1 .. G - 2
+  const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs, u = blockIdx.x / per, j0 = blockIdx.x % per;
+  const bool hom = KIND == kStateOnly && j0 >= a.segs - 1;
+  const int seg = hom ? j0 - a.segs + 2 : j0;
+  const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t s0 = sa(sm), bars = s0 + kBars;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
   auto bar = [&](int i) { return bars + 8 * i; };
-  const int len = seq_len(a.lens, b, a.T), n_chunks = (len + L - 1) / L;
-  constexpr int kRecBytes = rec_bytes(!OUT);
+  // chunks cb .. cb + n_chunks - 1 of the sequence; `len` tokens from chunk cb on
+  const int cb = seg * a.seg_chunks;
+  const int len = max(seq_len(a.lens, b, a.T) - cb * L, 0);
+  const int n_chunks = a.segs == 1 ? (len + L - 1) / L : min((len + L - 1) / L, a.seg_chunks);
+  constexpr int kRecBytes = rec_bytes(KIND == kImages);
+  constexpr bool kRecHasALo = KIND == kImages;
 
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
@@ -154,7 +173,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
   if (warp == 12) {
     // ================================================================ loads
-    const uint8_t* recs = a.rec + (long long)u * a.chunks * kRecBytes;
+    const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * kRecBytes;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1;
       if (c >= 2 && !(ok = wwait(bar(bEmpty + s), ((c >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
@@ -165,15 +184,15 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint8_t* r = recs + (long long)c * kRecBytes;
         mbar_expect_tx(fb, (OUT ? 2 * kHK + kHV : kHK + kHV) * kHalf + (OUT ? 3 : 2) * kImg + kScal);
         for (int i = 0; i < kHK; ++i) {
-          tma_load_4d(d + kK + i * kHalf, &tm_k, fb, 64 * i, hk, c * L, b);
-          if (OUT) tma_load_4d(d + kQ + i * kHalf, &tm_q, fb, 64 * i, hk, c * L, b);
+          tma_load_4d(d + kK + i * kHalf, &tm_k, fb, 64 * i, hk, (cb + c) * L, b);
+          if (OUT) tma_load_4d(d + kQ + i * kHalf, &tm_q, fb, 64 * i, hk, (cb + c) * L, b);
         }
-        for (int i = 0; i < kHV; ++i) tma_load_4d(d + kV + i * kHalf, &tm_v, fb, 64 * i, h, c * L, b);
+        for (int i = 0; i < kHV; ++i) tma_load_4d(d + kV + i * kHalf, &tm_v, fb, 64 * i, h, (cb + c) * L, b);
         if (OUT) {
           bulk_load(d + kR, r, 3 * kImg + kScal, fb);
         } else {
           bulk_load(d + kR, r, 2 * kImg, fb);
-          bulk_load(d + kScalOff, r + 4 * kImg, kScal, fb);
+          bulk_load(d + kScalOff, r + (kRecHasALo ? 4 : 3) * kImg, kScal, fb);
         }
       }
       ++loaded;
@@ -290,7 +309,21 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     constexpr int QC = DK / 4;                                 // S columns per thread and half
     const int row = (warp & 3) * 32 + lane, hc = warp >> 2;    // value channel = TMEM lane; which columns
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const long long srow = ((long long)u * DV + (row < DV ? row : 0)) * DK;
+    // where this row of the state comes from and goes to (NULL: zeros; nowhere)
+    const int rows = hom ? DK : DV, r_in = row < rows ? row : 0;
+    const bool joined = KIND == kO && a.segs > 1;              // (s_out may be s_in: that was read by the join)
+    const float* src = joined ? a.seg_s + seg * DV * DK : seg == 0 ? a.s_in : nullptr;
+    float* dst = KIND == kStateOnly ? (hom ? a.seg_x + ((long long)u * (a.segs - 2) + seg - 1) * DK * DK
+                                           : a.seg_n + ((long long)u * (a.segs - 1) + seg) * DV * DK)
+                 : seg == a.segs - 1 && a.s_out != nullptr ? a.s_out + (long long)u * DV * DK : nullptr;
+    if (src != nullptr) src += (long long)u * (joined ? a.segs : 1) * DV * DK + r_in * DK;
+    if (dst != nullptr) dst += r_in * DK;
+    auto first = [&](int col) {                                // four columns of the initial state
+      if (hom)
+        return make_float4(col == row ? 1.f : 0.f, col + 1 == row ? 1.f : 0.f, col + 2 == row ? 1.f : 0.f,
+                           col + 3 == row ? 1.f : 0.f);
+      return src != nullptr && row < rows ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
     auto arrive = [&](int i) {                                 // this warp's TMEM writes are done
       tmem_wait_st();
       tc_fence_before();
@@ -302,7 +335,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       // ---- the state as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
-      if (!OUT && c > 0 && !(ok = wwait(bar(bSread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (KIND == kImages && c > 0 && !(ok = wwait(bar(bSread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
       uint64_t S[2][QC / 2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -319,8 +352,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         } else {
 #pragma unroll
           for (int e = 0; e < QC / 4; ++e) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.s_in != nullptr && row < DV) v = reinterpret_cast<const float4*>(a.s_in + srow + c0)[e];
+            const float4 v = first(c0 + 4 * e);
             S[p][2 * e] = f2(v.x, v.y);
             S[p][2 * e + 1] = f2(v.z, v.w);
           }
@@ -366,7 +398,8 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tmem_ld32(la + kColVU + 32 * hc, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) R[e] = fma2(gm[e], pair_of(x + 2 * e), pair_of(v + 2 * e));
+        for (int e = 0; e < 16; ++e)
+          R[e] = KIND == kStateOnly && hom ? mul2(gm[e], pair_of(x + 2 * e)) : fma2(gm[e], pair_of(x + 2 * e), pair_of(v + 2 * e));
         split_pairs(R, hi, lo);
         tmem_st16(la + kColPR + 32 * hc, hi);
         tmem_st16(la + kColPR + 32 * hc + 16, lo);
@@ -399,8 +432,9 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tmem_st16(la + kColVU + 32 * hc, hi);
         tmem_st16(la + kColVU + 32 * hc + 16, lo);
         arrive(bUr);
+        if (KIND == kStateOnly) continue;
         split_pairs(R, hi, lo);
-        if (!OUT && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+        if (KIND == kImages && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
         tmem_st16(la + kColUH + 16 * hc, hi);
         tmem_st16(la + kColUL + 16 * hc, lo);
         arrive(bUh);
@@ -410,23 +444,21 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       ok = wwait(bar(bS), (n_chunks - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n_chunks - 1) & 1, abort_flag, nullptr, 0);
       tc_fence_after();
     }
-    if (a.s_out != nullptr) {
+    if (dst != nullptr) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
         uint32_t r[QC];
         tm_ld(la + kColS + c0, r);
         tmem_wait_ld();
-        if (row < DV) {
+        if (row < rows) {
 #pragma unroll
           for (int e = 0; e < QC / 4; ++e) {
             float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-            if (n_chunks == 0)
-              v = a.s_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                    : reinterpret_cast<const float4*>(a.s_in + srow + c0)[e];
+            if (n_chunks == 0) v = first(c0 + 4 * e);
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
-            reinterpret_cast<float4*>(a.s_out + srow + c0)[e] = v;
+            *reinterpret_cast<float4*>(dst + c0 + 4 * e) = v;
           }
         }
       }
@@ -440,8 +472,10 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       const int s = c & 1, ph = c & 1;
       if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
-      const long long img = (long long)u * a.chunks + c;
-      if (OUT) {
+      const long long img = (long long)u * a.chunks + cb + c;
+      if (KIND == kStateOnly) {
+        if (lane == 0) mbar_arrive(bar(bEmpty + s));
+      } else if (OUT) {
         if (!(ok = wwait(bar(bQS), ph, abort_flag, nullptr, 0))) break;
         tc_fence_after();
 #pragma unroll
@@ -492,14 +526,14 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           fence_proxy_async();
           bar_sync(1, 128);
           if (tid == 256) {
-            for (int i = 0; i < kHV; ++i) tma_store_4d(&tm_o, s0 + kOut + i * kHalf, 64 * i, h, c * L, b);
+            for (int i = 0; i < kHV; ++i) tma_store_4d(&tm_o, s0 + kOut + i * kHalf, 64 * i, h, (cb + c) * L, b);
             bulk_commit();
           }
         } else {
           bar_sync(1, 128);
           for (int i = tid - 256; i < n * (DV / 8); i += 128) {
             const int t = i / (DV / 8), cc = i % (DV / 8);
-            *reinterpret_cast<uint4*>(op + (long long)(c * L + t) * a.os.t + cc * 8) =
+            *reinterpret_cast<uint4*>(op + (long long)((cb + c) * L + t) * a.os.t + cc * 8) =
                 *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
           }
         }
@@ -571,17 +605,88 @@ inline bool map_of(CUtensorMap* m, const void* p, int D, int heads, int T, int B
   return tc::encode(m, p, 4, dims, sb, box);
 }
 
-template <int DK, int DV, bool OUT>
+// The states that the segments start from: S_0 as given, S_1 = n_0, S_{g+1} = S_g
+// X_g + n_g, in fp32.  One CTA per 16 rows of a unit's state: rows do not mix.
+// The next segment's X comes in by cp.async while this one's is in use.
+template <int DK>
+__global__ void __launch_bounds__(256)
+delta_join_kernel(const ChunkArgs a) {
+  constexpr int CT = DK / 16;                                  // columns per thread
+  extern __shared__ __align__(128) float jsm[];                // two X, then 16 rows of S
+  float* S = jsm + 2 * DK * DK;
+  const int slices = a.dv / 16, u = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 16;
+  const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 4; // columns c0 + 64 j .. + 3
+  auto fetch = [&](int g) {                                    // X of segment g
+    if (g >= 1 && g + 1 < a.segs) {
+      const float* x = a.seg_x + ((long long)u * (a.segs - 2) + g - 1) * DK * DK;
+      const uint32_t d = smem_u32(jsm + (g & 1) * DK * DK);
+#pragma unroll
+      for (int i = 0; i < DK * DK / 4 / 256; ++i)
+        cp_async16(d + (i * 256 + threadIdx.x) * 16, x + (i * 256 + threadIdx.x) * 4, true);
+    }
+    cp_async_commit();
+  };
+  fetch(1);
+#pragma unroll
+  for (int j = 0; j < CT; j += 4)
+    *reinterpret_cast<float4*>(a.seg_s + ((long long)u * a.segs * a.dv + r0 + r) * DK + c0 + 16 * j) =
+        a.s_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f)
+                          : *reinterpret_cast<const float4*>(a.s_in + ((long long)u * a.dv + r0 + r) * DK + c0 + 16 * j);
+  for (int g = 0; g + 1 < a.segs; ++g) {
+    float y[CT];
+    const float* n = a.seg_n + (((long long)u * (a.segs - 1) + g) * a.dv + r0 + r) * DK + c0;
+#pragma unroll
+    for (int j = 0; j < CT; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(n + 16 * j);
+      y[j] = v.x; y[j + 1] = v.y; y[j + 2] = v.z; y[j + 3] = v.w;
+    }
+    if (g > 0) {
+      fetch(g + 1);
+      cp_async_wait<1>();
+      __syncthreads();                                         // X of g has landed; S is complete
+      const float* x = jsm + (g & 1) * DK * DK + c0;
+#pragma unroll 8
+      for (int k = 0; k < DK; ++k) {
+        const float s = S[r * DK + k];
+#pragma unroll
+        for (int j = 0; j < CT; j += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(x + k * DK + 16 * j);
+          y[j] = fmaf(s, v.x, y[j]); y[j + 1] = fmaf(s, v.y, y[j + 1]);
+          y[j + 2] = fmaf(s, v.z, y[j + 2]); y[j + 3] = fmaf(s, v.w, y[j + 3]);
+        }
+      }
+      __syncthreads();                                         // S and X of g have been read
+    }
+    float* out = a.seg_s + (((long long)u * a.segs + g + 1) * a.dv + r0 + r) * DK + c0;
+#pragma unroll
+    for (int j = 0; j < CT; j += 4) {
+      const float4 v = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+      *reinterpret_cast<float4*>(out + 16 * j) = v;
+      *reinterpret_cast<float4*>(&S[r * DK + c0 + 16 * j]) = v;
+    }
+  }
+}
+
+template <int DK, int DV, int KIND>
 cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  delta_chain_tc_kernel<DK, DV, OUT><<<(unsigned)(B * a.H), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
+  const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
+  delta_chain_tc_kernel<DK, DV, KIND><<<(unsigned)(B * a.H * per), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
-template <bool OUT>
-cudaError_t dispatch(const CUtensorMap* m, const ChunkArgs& a, int B, int dk, cudaStream_t stream) {
-  if (dk == 128) return a.dv == 128 ? launch<128, 128, OUT>(m, a, B, stream) : launch<128, 64, OUT>(m, a, B, stream);
-  return a.dv == 128 ? launch<64, 128, OUT>(m, a, B, stream) : launch<64, 64, OUT>(m, a, B, stream);
+template <int DK, int DV>
+cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
+  if (a.s0 != nullptr) return launch<DK, DV, kImages>(m, a, B, stream);
+  if (a.segs > 1) {
+    const cudaError_t e = launch<DK, DV, kStateOnly>(m, a, B, stream);
+    if (e != cudaSuccess) return e;
+    constexpr int smem = (2 * DK * DK + 16 * DK) * 4;
+    const cudaError_t f = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (f != cudaSuccess) return f;
+    delta_join_kernel<DK><<<(unsigned)(B * a.H * (DV / 16)), 256, smem, stream>>>(a);
+  }
+  return launch<DK, DV, kO>(m, a, B, stream);
 }
 
 }  // namespace chaintc
@@ -592,7 +697,27 @@ cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t str
           chaintc::map_of(&m[2], a.v, a.dv, a.H, a.T, B, a.vs) &&
           (a.s0 != nullptr || chaintc::map_of(&m[3], a.o, a.dv, a.H, a.T, B, a.os));
   if (!*done) return cudaSuccess;
-  return a.s0 == nullptr ? chaintc::dispatch<true>(m, a, B, dk, stream) : chaintc::dispatch<false>(m, a, B, dk, stream);
+  if (dk == 128) return a.dv == 128 ? chaintc::run<128, 128>(m, a, B, stream) : chaintc::run<128, 64>(m, a, B, stream);
+  return a.dv == 128 ? chaintc::run<64, 128>(m, a, B, stream) : chaintc::run<64, 64>(m, a, B, stream);
+}
+
+// Segments of a sequence, by the time of both passes in chunk steps (2.3 us
+// each): a wave of CTAs per 148 units and segments, about one step per segment
+// for the join, six for two more launches.  One sequence of 16384 tokens and 16
+// heads: 637 us in one piece, XXX us in six.
+int chain_segments(long long units, int chunks) {
+  int best = 1;
+  double least = 0.9 * chunks;
+  for (int g = 3; g <= 64 && g * 2 <= chunks; ++g) {
+    const int per = (chunks + g - 1) / g;
+    const long long w1 = (units * (2 * g - 3) + 147) / 148, w2 = (units * g + 147) / 148;
+    const double t = per * (0.9 * w1 + w2) + g + 6;
+    if (t < least) {
+      least = t;
+      best = g;
+    }
+  }
+  return best;
 }
 
 }  // namespace delta

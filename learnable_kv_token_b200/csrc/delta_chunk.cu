@@ -530,21 +530,41 @@ cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream
 
 bool delta_chunked(const lte_gdr_dims* d) { return d->dtype == LTE_BF16 && d->T > delta::kFewTokens; }
 
-size_t delta_prefill_bytes(const lte_gdr_dims* d) {
-  if (!delta_chunked(d)) return 0;
-  return (size_t)d->B * d->H * ((d->T + delta::L - 1) / delta::L) * delta::rec_bytes(false);
-}
+namespace {
+// workspace: records, then the segments' maps and states
+struct PrefillLayout {
+  int chunks, segs;
+  size_t n, x, s, total;
+  explicit PrefillLayout(const lte_gdr_dims* d) {
+    const size_t units = (size_t)d->B * d->H, state = (size_t)d->dv * d->dk * 4;
+    chunks = (d->T + delta::L - 1) / delta::L;
+    segs = delta::chain_segments((long long)units, chunks);
+    size_t at = units * chunks * delta::rec_bytes(false);
+    auto take = [&](size_t bytes) { const size_t r = (at + 255) & ~(size_t)255; at = r + bytes; return r; };
+    n = take(segs > 1 ? units * (segs - 1) * state : 0);
+    x = take(segs > 1 ? units * (segs - 2) * d->dk * d->dk * 4 : 0);
+    s = take(segs > 1 ? units * segs * state : 0);
+    total = at;
+  }
+};
+}  // namespace
+
+size_t delta_prefill_bytes(const lte_gdr_dims* d) { return delta_chunked(d) ? PrefillLayout(d).total : 0; }
 
 cudaError_t delta_prefill(const DeltaArgs& a, cudaStream_t stream) {
   const lte_gdr_dims* d = a.d;
   if (!delta_chunked(d)) return delta_recurrent(a, stream);
+  const PrefillLayout w(d);
+  uint8_t* ws = (uint8_t*)a.scratch;
   delta::ChunkArgs c{};
   c.q = (const __nv_bfloat16*)a.q; c.k = (const __nv_bfloat16*)a.k; c.v = (const __nv_bfloat16*)a.v;
   c.qs = a.qs; c.ks = a.ks; c.vs = a.vs; c.os = a.os;
   c.g = a.g; c.beta = a.beta; c.lens = a.lens; c.s_in = a.s_in; c.s_out = a.s_out;
-  c.o = (__nv_bfloat16*)a.o; c.rec = (uint8_t*)a.scratch;
-  c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = (d->T + delta::L - 1) / delta::L;
+  c.o = (__nv_bfloat16*)a.o; c.rec = ws;
+  c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = w.chunks;
   c.scale = d->scale;
+  c.segs = w.segs; c.seg_chunks = (w.chunks + w.segs - 1) / w.segs;
+  c.seg_n = (float*)(ws + w.n); c.seg_x = (float*)(ws + w.x); c.seg_s = (float*)(ws + w.s);
   cudaError_t e = delta::prepare(c, d->B, d->dk, false, stream);
   return e != cudaSuccess ? e : delta::forward_chain(c, d->B, d->dk, stream);
 }

@@ -120,6 +120,10 @@ struct ChunkArgs {
   uint32_t *s0, *u;      // images of S_0 (hi, lo) and U (hi, lo) per chunk, for the gradients
   int T, H, Hk, dv, chunks;
   float scale;
+  // segments (forward only; segs = 1: the sequence in one piece): chunks of each,
+  // n [units][segs - 1][dv][dk], X [units][segs - 2][dk][dk], states [units][segs][dv][dk]
+  int segs, seg_chunks;
+  float *seg_n, *seg_x, *seg_s;
 };
 
 // delta_chunk.cu
@@ -128,6 +132,7 @@ cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t s
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
 
 // delta_chain_tc.cu: the same on tcgen05; *done = false if a tensor's strides do not suit TMA
+int chain_segments(long long units, int chunks);
 cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done);
 
 }  // namespace delta

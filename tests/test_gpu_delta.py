@@ -136,6 +136,20 @@ def test_prefill_extreme_gates(layer, dtype, kind):
     check_prefill(layer, x, scale)
 
 
+@pytest.mark.parametrize("shape,lens", [((1, 2600, 2, 1, 128, 128), None), ((2, 3000, 1, 1, 64, 128), [2999, 700]),
+                                        ((1, 1500, 1, 1, 128, 64), None), ((3, 1100, 1, 1, 64, 64), [0, 1100, 64])],
+                         ids=str)
+def test_prefill_long_few_heads(layer, shape, lens):
+    """Few heads over many chunks: the sequence runs in segments.  The result in place equals the one
+    in a new tensor, and slow decay carries the first tokens to the end."""
+    x = inputs(40, *shape, lens=lens)
+    x["g"].mul_(0.05)
+    o, S = check_prefill(layer, x)
+    st = x["state"].clone()
+    o2, S2 = layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=st, lens=x["lens"], state_out=st)
+    assert S2 is st and torch.equal(o, o2) and torch.equal(S, st)
+
+
 def test_prefill_continues(layer):
     """A prompt in three calls, in place on one state, equals the prompt in one call."""
     x = inputs(4, 2, 300, 4, 4, 128, 128)
