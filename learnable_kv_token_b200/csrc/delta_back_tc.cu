@@ -1,0 +1,658 @@
+// The backward chain of the gated delta rule on 5th-generation tensor cores
+// (formulas: delta_backward.cu; layout and pipeline as in delta_chain_tc.cu).
+//
+// One CTA per (batch, value head) walks the chunks from the last to the first
+// with dS in TMEM, lane = value channel:
+//   X   = dO^T A                                   SS, A as hi + lo (columns s <= t)
+//   P   = dS K^T                                   TS, dS as hi + lo
+//   dU  = P diag(e^{G_L - G}) + X                  by threads; hi + lo over P
+//   F   = dU T                                     TS; + b dU by threads; -e^G F as hi + lo over F
+//   dS  = e^{G_L} dS + (scale e^G dO)^T Q - (e^G F)^T K     TS
+// (all transposed: rows are value channels, columns tokens or key channels).
+// Columns: dS (DK), dS hi, lo (DK / 2 each), P or dU (64), F (64), X, then F as
+// fp32 (64), dO^T, then scale e^G dO^T as hi + lo (64).
+//
+// Warps 0-7 keep the chain; 8-15 scale dO, write the images of dS and F and dV,
+// and take the sums over value channels that the gates' gradients need: u.F / b
+// and v.F per token, <dS, S> per chunk (two threads per value channel, half of the
+// columns each, here too); 16 loads; 17 issues the MMAs.  Registers: 112 for the
+// chain, 104 for the sums, 48 for the rest; one spilled costs a trip to L2.
+// The products of dO with Q run while the chain warps turn F, so the chain of a
+// chunk is P -> dU -> F -> dS as in the forward pass.
+#include <math.h>
+
+#include "delta_chain_tc.cuh"
+
+namespace lte {
+namespace delta {
+namespace backtc {
+
+using namespace chaintc;
+
+constexpr int kThreads = 640;
+// a stage: K, Q, dO, V (two halves each), the record's T hi, T lo, A hi, A lo, scalars
+constexpr uint32_t kK = 0, kQ = 2 * kHalf, kD = 4 * kHalf, kV = 6 * kHalf, kR = 8 * kHalf;
+constexpr uint32_t kScalOff = kR + 4 * kImg;
+constexpr uint32_t kStage = (kScalOff + kScal + 1023) / 1024 * 1024;
+// then the identity and a chunk of dV as token rows
+constexpr uint32_t kIdent = 2 * kStage, kOut = kIdent + kImg, kBars = kOut + 2 * kHalf, kSmem = kBars + 256;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bX = 7, bP = 8, bUr = 9, bF = 10, bFr = 11, bFx = 12, bXf = 13,
+             bDr = 14, bS = 15, bSread = 17, bDrain = 18, kBarCount = 19 };
+constexpr uint32_t kColS = 0, kColP = 256, kColF = 320, kColX = 384, kColD = 448;
+
+// z[j] summed over the warp's lanes; lane j gets the sum of z[j].  At each step
+// a lane keeps half of its values and adds its partner's copy of them.
+template <int N>
+__device__ __forceinline__ void fold(float (&z)[32], int lane) {
+  const bool upper = (lane & N) != 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float send = upper ? z[j] : z[j + N], keep = upper ? z[j + N] : z[j];
+    z[j] = keep + __shfl_xor_sync(0xffffffffu, send, N);
+  }
+}
+__device__ __forceinline__ float lane_sums(float (&z)[32], int lane) {
+  fold<16>(z, lane);
+  fold<8>(z, lane);
+  fold<4>(z, lane);
+  fold<2>(z, lane);
+  fold<1>(z, lane);
+  return z[0];
+}
+__device__ __forceinline__ float dot8(const uint4& h, const uint4& l, const float* x, float s) {
+  const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    s = fmaf(x[2 * e], bf_lo(a[e]) + bf_lo(b[e]), s);
+    s = fmaf(x[2 * e + 1], bf_hi(a[e]) + bf_hi(b[e]), s);
+  }
+  return s;
+}
+
+// read once: not kept in what is left of the L1 cache
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_dv, const GradArgs ga) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const ChunkArgs& a = ga.f;
+  constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
+  constexpr int kHK = DK / 64, kHV = DV / 64, kStrips = DV / 16;
+  const int u = blockIdx.x, b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t s0 = sa(sm), bars = s0 + kBars;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
+  auto bar = [&](int i) { return bars + 8 * i; };
+  const int len = seq_len(a.lens, b, a.T), n = (len + L - 1) / L;
+
+  if (tid == 0) {
+    for (int i = 0; i < kBarCount; ++i) {
+      const bool chain = i == bSr || i == bSr + 1 || i == bUr || i == bFr || i == bFx;     // 8 chain warps
+      const bool out = i == bDr || i == bXf || i == bSread;                                // 8 output warps
+      mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain || out ? 8 : 1);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  write_identity(sm + kIdent, kThreads);
+  fence_proxy_async();
+  if (warp == 17) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true, issued = false;
+  int loaded = 0;
+
+  if (warp >= 16) regs_dec<48>();
+  if (warp == 16) {
+    // ================================================================ loads
+    const uint8_t* recs = a.rec + (long long)u * a.chunks * rec_bytes(true);
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1, c = n - 1 - i;
+      if (i >= 2 && !(ok = wwait(bar(bEmpty + s), ((i >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
+      const uint32_t d = s0 + s * kStage;
+      const bool tail = c * L + L > len;                       // the first one to come
+      const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
+      if (elect_one()) {
+        mbar_expect_tx(fb, 2 * (kHK + kHV) * kHalf + 4 * kImg + kScal);
+        for (int j = 0; j < kHK; ++j) {
+          tma_load_4d(d + kK + j * kHalf, &tm_k, fb, 64 * j, hk, c * L, b);
+          tma_load_4d(d + kQ + j * kHalf, &tm_q, fb, 64 * j, hk, c * L, b);
+        }
+        for (int j = 0; j < kHV; ++j) {
+          tma_load_4d(d + kD + j * kHalf, &tm_d, fb, 64 * j, h, c * L, b);
+          tma_load_4d(d + kV + j * kHalf, &tm_v, fb, 64 * j, h, c * L, b);
+        }
+        bulk_load(d + kR, recs + (long long)c * rec_bytes(true), 4 * kImg + kScal, fb);
+      }
+      {                                                        // the images that the output warps read: to L2, a piece per lane
+        const long long img = (long long)u * a.chunks + c;
+        prefetch_l2(reinterpret_cast<const uint8_t*>(a.u + img * DV * L) + lane * (DV * L / 8), DV * L / 8);
+        prefetch_l2(reinterpret_cast<const uint8_t*>(a.s0 + img * DV * DK) + lane * (DV * DK / 8), DV * DK / 8);
+      }
+      ++loaded;
+      if (tail) {
+        if (!(ok = wwait(fb, 0, abort_flag, nullptr, 0))) break;
+        const int r0 = len - c * L;
+        uint8_t* st = sm + s * kStage;
+        for (int j = 0; j < kHK; ++j) {
+          zero_rows(st + kK + j * kHalf, r0, lane);
+          zero_rows(st + kQ + j * kHalf, r0, lane);
+        }
+        for (int j = 0; j < kHV; ++j) {
+          zero_rows(st + kD + j * kHalf, r0, lane);
+          zero_rows(st + kV + j * kHalf, r0, lane);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bFull + s));
+      }
+    }
+  } else if (warp == 17) {
+    // ================================================================= MMAs
+    const uint32_t id_tok = idesc2(128, L, false, false), id_dt = idesc2(128, L, true, false);
+    const uint32_t id_s = idesc2(128, 64, false, true);
+    const uint64_t ident = sdesc(s0 + kIdent, 16, 1024);
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1, ph = i & 1;
+      const uint32_t d = s0 + s * kStage;
+      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+      if (i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      issued = true;
+      const uint64_t dk = sdesc(d + kK, 16, 1024), dd = sdesc(d + kD, kHalf, 1024), dt = sdesc(d + kR, kHalf, 1024);
+      if (elect_one()) {                                       // dO^T, and X = dO^T A
+#pragma unroll
+        for (int ks = 0; ks < L / 16; ++ks)
+          mma_f16(tmem + kColD, dd + ((ks * 2048) >> 4), ident + ((ks * 32) >> 4), id_dt, ks > 0);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = L / 16 - 1; ks >= 0; --ks)
+            mma_f16(tmem + kColX, dd + ((ks * 2048) >> 4), dt + (((2 + p) * kImg + ks * 2048) >> 4),
+                    idesc2(128, 16 * (ks + 1), true, true), !(p == 0 && ks == L / 16 - 1));
+        mma_commit(bar(bX));
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {                            // P = dS K^T, by halves of dS's columns
+        if (ok) ok = wwait(bar(bSr + p), ph, abort_flag, nullptr, 0);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < DK / 16; ++j) {
+            const int ks = p * (DK / 32) + j / 2;
+            mma_f16_ts(tmem + kColP, tmem + (j & 1 ? kColSl : kColSh) + 8 * ks, dk + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                       id_tok, p + j > 0);
+          }
+          if (p == 1) mma_commit(bar(bP));
+        }
+      }
+      if (!ok) break;
+      if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      if (elect_one()) {                                       // F = dU T, columns s < 16 (ks + 1)
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int ks = L / 16 - 1; ks >= 0; --ks)
+            mma_f16_ts(tmem + kColF, tmem + kColP + pair_col(ks, p == 1), dt + (((p == 2 ? kImg : 0) + ks * 2048) >> 4),
+                       idesc2(128, 16 * (ks + 1), false, true), !(p == 0 && ks == L / 16 - 1));
+        mma_commit(bar(bF));
+      }
+      if (!(ok = wwait(bar(bDr), ph, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      if (elect_one()) {                                       // dS += (scale e^G dO)^T Q
+#pragma unroll
+        for (int m = 0; m < kHK; ++m)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < L / 16; ++ks)
+              mma_f16_ts(tmem + kColS + 64 * m, tmem + kColD + pair_col(ks, p),
+                         sdesc(d + kQ + m * kHalf, kHalf, 1024) + ((ks * 2048) >> 4), id_s, 1u);
+      }
+      if (!(ok = wwait(bar(bFr), ph, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      if (elect_one()) {                                       // dS -= (e^G F)^T K, by halves of its columns
+#pragma unroll
+        for (int m = 0; m < kHK; ++m) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < L / 16; ++ks)
+              mma_f16_ts(tmem + kColS + 64 * m, tmem + kColF + pair_col(ks, p),
+                         sdesc(d + kK + m * kHalf, kHalf, 1024) + ((ks * 2048) >> 4), id_s, 1u);
+          mma_commit(bar(bS + m));
+        }
+        if (kHK == 1) mma_commit(bar(bS + 1));
+        if (i + 2 < n) mma_commit(bar(bEmpty + s));            // the stage is loaded once more
+      }
+    }
+    if (!ok && issued) {                                       // MMAs in flight end before exit
+      __syncwarp();
+      if (elect_one()) mma_commit(bar(bDrain));
+      __syncwarp();
+      mbar_drain(bar(bDrain), 0);
+    }
+  } else if (warp < 8) {
+    // ========================================================== chain warps
+    regs_inc<112>();
+    constexpr int QC = DK / 4;
+    const int row = (warp & 3) * 32 + lane, hc = warp >> 2;
+    const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const long long srow = ((long long)u * DV + (row < DV ? row : 0)) * DK;
+    auto arrive = [&](int j) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(j));
+    };
+    auto first = [&](int col) {
+      return ga.ds_out != nullptr && row < DV ? *reinterpret_cast<const float4*>(ga.ds_out + srow + col)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1, ph = i & 1;
+      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+      const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
+      // ---- dS as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
+      if (i > 0 && !(ok = wwait(bar(bSread), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      const float el = scal[kEG * L + L - 1];
+      const uint64_t el2 = f2(el, el);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
+        uint64_t S[QC / 2];
+        if (i > 0) {
+          if (ok) ok = wwait(bar(bS + p), (i - 1) & 1, abort_flag, nullptr, 0);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t r[QC];
+          tm_ld(la + kColS + c0, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < QC / 2; ++e) S[e] = pair_of(r + 2 * e);
+        } else {
+#pragma unroll
+          for (int e = 0; e < QC / 4; ++e) {
+            const float4 v = first(c0 + 4 * e);
+            S[2 * e] = f2(v.x, v.y);
+            S[2 * e + 1] = f2(v.z, v.w);
+          }
+        }
+        {
+          uint32_t hi[QC / 2], lo[QC / 2];
+          split_pairs(S, hi, lo);
+          tm_st(la + kColSh + c0 / 2, hi);
+          tm_st(la + kColSl + c0 / 2, lo);
+        }
+        arrive(bSr + p);
+        // e^{G_L} dS for this chunk's update (published with dU)
+        uint32_t r[QC];
+#pragma unroll
+        for (int e = 0; e < QC / 2; ++e) {
+          float x, y;
+          unf2(mul2(S[e], el2), x, y);
+          r[2 * e] = __float_as_uint(x);
+          r[2 * e + 1] = __float_as_uint(y);
+        }
+        tm_st(la + kColS + c0, r);
+      }
+      if (!ok) break;
+      // ---- dU = P diag(e^{G_L - G}) + X, tokens 32 hc .. + 31
+      uint64_t U[16];
+      if (!(ok = wwait(bar(bX), ph, abort_flag, nullptr, 0) && wwait(bar(bP), ph, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {                          // 16 columns at a time
+          uint32_t x[16], v[16];
+          tmem_ld16(la + kColP + 32 * hc + 16 * q, x);
+          tmem_ld16(la + kColX + 32 * hc + 16 * q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 g = *reinterpret_cast<const float4*>(scal + kLam * L + 32 * hc + 16 * q + 4 * e);
+            U[8 * q + 2 * e] = fma2(f2(g.x, g.y), pair_of(x + 4 * e), pair_of(v + 4 * e));
+            U[8 * q + 2 * e + 1] = fma2(f2(g.z, g.w), pair_of(x + 4 * e + 2), pair_of(v + 4 * e + 2));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split_pair(U[8 * q + e], hi[8 * q + e], lo[8 * q + e]);
+        }
+        tmem_st16(la + kColP + 32 * hc, hi);
+        tmem_st16(la + kColP + 32 * hc + 16, lo);
+      }
+      arrive(bUr);
+      // ---- F = dU T + b dU; first -e^G F as hi and lo, then F itself
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 g = *reinterpret_cast<const float4*>(scal + kBeta * L + 32 * hc + 4 * e);
+        U[2 * e] = mul2(U[2 * e], f2(g.x, g.y));
+        U[2 * e + 1] = mul2(U[2 * e + 1], f2(g.z, g.w));
+      }
+      if (!(ok = wwait(bar(bF), ph, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      {
+        uint32_t hi[16], lo[16];
+        const uint64_t one = f2(1.f, 1.f);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t x[16];
+          tmem_ld16(la + kColF + 32 * hc + 16 * q, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * hc + 16 * q + 4 * e);
+            const int f = 8 * q + 2 * e;
+            U[f] = fma2(pair_of(x + 4 * e), one, U[f]);
+            U[f + 1] = fma2(pair_of(x + 4 * e + 2), one, U[f + 1]);
+            split_pair(mul2(U[f], f2(-g.x, -g.y)), hi[f], lo[f]);
+            split_pair(mul2(U[f + 1], f2(-g.z, -g.w)), hi[f + 1], lo[f + 1]);
+          }
+        }
+        tmem_st16(la + kColF + 32 * hc, hi);
+        tmem_st16(la + kColF + 32 * hc + 16, lo);
+        arrive(bFr);
+        if (lane == 0) mbar_arrive(bar(bEmpty + s));           // the scalars have been read
+        uint32_t x[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float y, z;
+          unf2(U[e], y, z);
+          x[2 * e] = __float_as_uint(y);
+          x[2 * e + 1] = __float_as_uint(z);
+        }
+        tmem_st32(la + kColX + 32 * hc, x);
+        arrive(bFx);
+      }
+    }
+    if (ok && n > 0) {
+      ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
+      tc_fence_after();
+    }
+    if (ga.ds_in != nullptr) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
+        uint32_t r[QC];
+        tm_ld(la + kColS + c0, r);
+        tmem_wait_ld();
+        if (row < DV) {
+#pragma unroll
+          for (int e = 0; e < QC / 4; ++e) {
+            float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                   __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+            if (n == 0) v = first(c0 + 4 * e);
+            if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
+            *reinterpret_cast<float4*>(ga.ds_in + srow + c0 + 4 * e) = v;
+          }
+        }
+      }
+    }
+  } else if (warp < 16) {
+    // =============================================== dO, images, dV, sums
+    regs_inc<104>();
+    const int quad = warp & 3, oh = (warp >> 2) & 1, row = quad * 32 + lane;   // oh: which half of the columns
+    const bool mine = quad * 32 < DV;                          // a warp of value channels that exist
+    const int rb = row >> 3, r7 = row & 7;
+    const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
+    __nv_bfloat16* dvp = ga.dv + ((long long)b * a.T * a.H + h) * DV;
+    // this row's 16 bytes in column block 0 of the images of S_0, dS, U and F of a chunk
+    const int at_s = rb * (DK / 8) * 128 + r7 * 16, at_t = rb * (L / 8) * 128 + r7 * 16;
+    const uint8_t* s_img = reinterpret_cast<const uint8_t*>(a.s0) + (long long)u * a.chunks * (DV * DK * 4) + at_s;
+    const uint8_t* u_img = reinterpret_cast<const uint8_t*>(a.u) + (long long)u * a.chunks * (DV * L * 4) + at_t;
+    uint8_t* d_img = reinterpret_cast<uint8_t*>(ga.ds) + (long long)u * a.chunks * (DV * DK * 2) + at_s;
+    uint8_t* f_img = reinterpret_cast<uint8_t*>(ga.fimg) + (long long)u * a.chunks * (DV * L * 2) + at_t;
+    auto put_inner = [&](int c, float s) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0 && mine) ga.inner[((long long)u * a.chunks + c) * kStrips + 2 * quad + oh] = s;
+    };
+    for (int i = 0; i < n; ++i) {
+      const int s = i & 1, ph = i & 1, c = n - 1 - i;
+      // (a warp whose wait gave up still meets the others at the vote below)
+      ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
+      const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
+      const long long img = (long long)u * a.chunks + c;
+      // ---- the state of the chunk behind, hi and lo: on its way long before its use
+      uint4 st[2][8];
+      const bool inner = mine && i > 0;
+      auto fetch_state = [&](int j) {
+        const uint8_t* p = s_img + (long long)(c + 1) * (DV * DK * 4) + (oh * (DK / 64) + j) * 512;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          st[j][e] = load_once(p + e * 128);
+          st[j][4 + e] = load_once(p + DV * DK * 2 + e * 128);
+        }
+      };
+      if (inner) fetch_state(0);
+      // ---- scale e^G dO^T as hi and lo
+      ok = ok && wwait(bar(bX), ph, abort_flag, nullptr, 0);
+      tc_fence_after();
+      {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {                          // 16 columns at a time
+          uint32_t r[16];
+          tmem_ld16(la + kColD + 32 * oh + 16 * q, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * oh + 16 * q + 4 * e);
+            split_pair(mul2(pair_of(r + 4 * e), f2(a.scale * g.x, a.scale * g.y)), hi[8 * q + 2 * e], lo[8 * q + 2 * e]);
+            split_pair(mul2(pair_of(r + 4 * e + 2), f2(a.scale * g.z, a.scale * g.w)), hi[8 * q + 2 * e + 1], lo[8 * q + 2 * e + 1]);
+          }
+        }
+        tmem_st16(la + kColD + 32 * oh, hi);
+        tmem_st16(la + kColD + 32 * oh + 16, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bDr));
+      // ---- dS: its image (hi), and <dS, S_0> with the state of the chunk behind
+      if (inner && DK > 64) fetch_state(1);
+      ok = ok && wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0);
+      tc_fence_after();
+      {
+        float in = 0.f;
+        uint8_t* im = d_img + (long long)c * (DV * DK * 2);
+#pragma unroll
+        for (int j = 0; j < DK / 64; ++j) {                    // 32 key channels: 16 words each of hi and lo
+          const int jc = oh * (DK / 64) + j;
+          uint32_t hi[16], lo[16];
+          tmem_ld16(la + kColSh + 16 * jc, hi);
+          tmem_ld16(la + kColSl + 16 * jc, lo);
+          tmem_wait_ld();
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(im + (4 * jc + e) * 128) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+          }
+          if (inner) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x[8];
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                x[2 * f] = bf_lo(hi[4 * e + f]) + bf_lo(lo[4 * e + f]);
+                x[2 * f + 1] = bf_hi(hi[4 * e + f]) + bf_hi(lo[4 * e + f]);
+              }
+              in = dot8(st[j][e], st[j][4 + e], x, in);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bSread));
+        if (i > 0) put_inner(c + 1, in);
+      }
+      // ---- F: image, dV, u.F / b and v.F per token (32 tokens)
+      uint4 uw[8];
+      const int j = oh;
+      auto fetch_u = [&]() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint8_t* p = u_img + (long long)c * (DV * L * 4) + (4 * j + e) * 128;
+          uw[e] = load_once(p);
+          uw[4 + e] = load_once(p + DV * L * 2);
+        }
+      };
+      if (mine) fetch_u();
+      ok = ok && wwait(bar(bFx), ph, abort_flag, nullptr, 0);
+      tc_fence_after();
+      if (tid == 256) bulk_wait_read();                        // the chunk before has left the buffer
+      if (!(ok = bar_and(1, 256, ok))) break;
+      const uint32_t colv = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
+      const int cv = (row & 63) >> 3;
+      uint8_t* im = f_img + (long long)c * (DV * L * 2);
+      float* xp = ga.x + (img * kStrips + 2 * quad) * (2 * L);
+      {
+        uint32_t F[32];
+        tmem_ld32(la + kColX + 32 * j, F);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bXf));
+        if (mine) {
+          float z[32];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t wh[4] = {uw[e].x, uw[e].y, uw[e].z, uw[e].w};
+            const uint32_t wl[4] = {uw[4 + e].x, uw[4 + e].y, uw[4 + e].z, uw[4 + e].w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              z[8 * e + 2 * f] = __uint_as_float(F[8 * e + 2 * f]) * (bf_lo(wh[f]) + bf_lo(wl[f]));
+              z[8 * e + 2 * f + 1] = __uint_as_float(F[8 * e + 2 * f + 1]) * (bf_hi(wh[f]) + bf_hi(wl[f]));
+            }
+          }
+          const float x = lane_sums(z, lane) / scal[kBeta * L + 32 * j + lane];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int t = 32 * j + e;
+            z[e] = __uint_as_float(F[e]) *
+                   __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + s * kStage + kV + colv + t * 128 + ((cv ^ (t & 7)) << 4)));
+          }
+          const float v = lane_sums(z, lane);
+          xp[32 * j + lane] = x;
+          xp[L + 32 * j + lane] = v;
+          xp[2 * L + 32 * j + lane] = 0.f;                     // the warp's second strip of 16
+          xp[3 * L + 32 * j + lane] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              w[f] = pack_bf16(__uint_as_float(F[8 * e + 2 * f]), __uint_as_float(F[8 * e + 2 * f + 1]));
+              const int t = 32 * j + 8 * e + 2 * f;
+              *reinterpret_cast<uint16_t*>(sm + kOut + colv + t * 128 + ((cv ^ (t & 7)) << 4)) = (uint16_t)(w[f] & 0xffff);
+              *reinterpret_cast<uint16_t*>(sm + kOut + colv + (t + 1) * 128 + ((cv ^ ((t + 1) & 7)) << 4)) = (uint16_t)(w[f] >> 16);
+            }
+            *reinterpret_cast<uint4*>(im + (4 * j + e) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bEmpty + s));
+      const int nt = len - c * L;
+      if (nt >= L) {
+        fence_proxy_async();
+        bar_sync(1, 256);
+        if (tid == 256) {
+          for (int j = 0; j < kHV; ++j) tma_store_4d(&tm_dv, s0 + kOut + j * kHalf, 64 * j, h, c * L, b);
+          bulk_commit();
+        }
+      } else {
+        bar_sync(1, 256);
+        for (int j = tid - 256; j < nt * (DV / 8); j += 256) {
+          const int t = j / (DV / 8), cc = j % (DV / 8);
+          *reinterpret_cast<uint4*>(dvp + (long long)(c * L + t) * a.H * DV + cc * 8) =
+              *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
+        }
+      }
+    }
+    // ---- the gradient of the initial state with that state
+    if (ok && n > 0) {
+      ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
+      tc_fence_after();
+      if (ok) {
+        float in = 0.f;
+#pragma unroll
+        for (int k = 0; k < DK / 32; ++k) {
+          const int j = oh * (DK / 32) + k;
+          uint32_t r[16];
+          tmem_ld16(la + kColS + 16 * j, r);
+          tmem_wait_ld();
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 sh = load_once(s_img + (2 * j + e) * 128);
+              const uint4 sl = load_once(s_img + DV * DK * 2 + (2 * j + e) * 128);
+              float x[8];
+#pragma unroll
+              for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(r[8 * e + f]);
+              in = dot8(sh, sl, x, in);
+            }
+          }
+        }
+        put_inner(0, in);
+      }
+    }
+  }
+  if (tid == 256) bulk_wait_all();                             // output stores complete before exit
+  // copies in flight land before exit (only after a wait gave up)
+  if (warp == 16 && *abort_flag) {
+    for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
+      if ((n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
+      else mbar_drain(bar(bTail), 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <int DK, int DV>
+cudaError_t launch(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  delta_back_tc_kernel<DK, DV><<<(unsigned)(B * a.f.H), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
+  return cudaGetLastError();
+}
+
+}  // namespace backtc
+
+cudaError_t back_chain_tc(const GradArgs& g, int B, int dk, cudaStream_t stream, bool* done) {
+  using namespace backtc;
+  const ChunkArgs& a = g.f;
+  CUtensorMap m[5];
+  const Strides4 out{(long long)a.T * a.H * a.dv, (long long)a.H * a.dv, a.dv};
+  *done = map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) && map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) &&
+          map_of(&m[2], g.dO, a.dv, a.H, a.T, B, g.dos) && map_of(&m[3], a.v, a.dv, a.H, a.T, B, a.vs) &&
+          map_of(&m[4], g.dv, a.dv, a.H, a.T, B, out);
+  if (!*done) return cudaSuccess;
+  if (dk == 128) return a.dv == 128 ? launch<128, 128>(m, g, B, stream) : launch<128, 64>(m, g, B, stream);
+  return a.dv == 128 ? launch<64, 128>(m, g, B, stream) : launch<64, 64>(m, g, B, stream);
+}
+
+}  // namespace delta
+}  // namespace lte

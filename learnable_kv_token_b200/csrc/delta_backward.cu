@@ -23,18 +23,6 @@
 namespace lte {
 namespace delta {
 
-struct GradArgs {
-  ChunkArgs f;
-  const __nv_bfloat16* dO;
-  Strides4 dos;
-  const float* ds_out;       // gradient of the final state (NULL = zeros)
-  float* ds_in;              // gradient of the initial state (nullable)
-  __nv_bfloat16 *dq, *dk, *dv;
-  float *dg, *db;
-  uint32_t *ds, *fimg;       // images of dS (hi) and F (hi) per chunk
-  float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
-};
-
 // ------------------------------------------------------------- backward chain
 // As the forward chain: a warp per 16 value channels, products transposed, each
 // result the next one's A operand in place.
@@ -608,6 +596,9 @@ cudaError_t launch_back(const GradArgs& a, int B, cudaStream_t stream) {
 }
 template <int DK>
 cudaError_t back_chain(const GradArgs& a, int B, cudaStream_t stream) {
+  bool done = false;
+  const cudaError_t e = back_chain_tc(a, B, DK, stream, &done);
+  if (done) return e;
   const long long strips = (long long)B * a.f.H * (a.f.dv / 16);   // as the forward chain
   if (strips >= 8 * 96 && a.f.dv == 128) return launch_back<DK, 8>(a, B, stream);
   if (strips >= 4 * 148) return launch_back<DK, 4>(a, B, stream);

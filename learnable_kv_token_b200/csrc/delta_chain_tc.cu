@@ -35,17 +35,13 @@
 // Every mbarrier wait is bounded; a CTA that gives up writes NaN to its state.
 #include <math.h>
 
-#include "delta_chunk.cuh"
-#include "tc_ptx.cuh"
+#include "delta_chain_tc.cuh"
 
 namespace lte {
 namespace delta {
 namespace chaintc {
 
-using namespace tc;
-
-constexpr int kThreads = 448;
-constexpr uint32_t kHalf = L * 128;                          // [64 tokens][64 channels] bf16, 128B-swizzled
+constexpr int kThreads = 512;
 // a stage: K, Q, V (two halves each), then T hi, T lo, A, scalars as in the record
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kV = 4 * kHalf, kR = 6 * kHalf;
 constexpr uint32_t kScalOff = kR + 3 * kImg;
@@ -57,60 +53,8 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 // mbarriers; those without [] complete once per chunk
 enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bP = 7, bRr = 8, bU = 9, bUr = 10, bUh = 11, bS = 12, bQS = 14,
              bOs = 15, bO = 16, bOf = 17, bSread = 18, bUread = 19, bDrain = 20, kBarCount = 21 };
-// columns; R and the scaled U lie as hi (16) and lo (16) over each 32 columns of P and U
+// columns; R and the scaled U lie over P and U (pair_col)
 constexpr uint32_t kColS = 0, kColPR = 256, kColVU = 320, kColUH = 384, kColUL = 416, kColO = 448;
-__device__ __forceinline__ uint32_t pair_col(int ks, int lo) { return 32 * (ks >> 1) + 16 * lo + 8 * (ks & 1); }
-
-__device__ __forceinline__ uint32_t idesc2(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-// two fp32 values in one register pair
-__device__ __forceinline__ uint64_t f2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unf2(uint64_t r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// a pair -> bf16 hi and lo words (as split2)
-__device__ __forceinline__ void split_pair(uint64_t x, uint32_t& hi, uint32_t& lo) {
-  float x0, x1;
-  unf2(x, x0, x1);
-  hi = pack_bf16(x0, x1);
-  unf2(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x), x0, x1);
-  lo = pack_bf16(x0, x1);
-}
-template <int N>
-__device__ __forceinline__ void split_pairs(const uint64_t (&x)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) split_pair(x[e], hi[e], lo[e]);
-}
-// columns of this warp's lanes <-> registers, by count
-__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
-__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
-__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[32]) { tmem_st32(t, r); }
-__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
-__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) { return f2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 
 // what a chain leaves besides the state
 enum : int { kImages = 0, kO = 1, kStateOnly = 2 };
@@ -150,13 +94,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // the identity, [n][k] bf16
-  for (int i = tid; i < L * 8; i += kThreads) {
-    const int n = i >> 3, cc = i & 7;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (cc == n >> 3) w[(n & 7) >> 1] = (n & 1) ? 0x3f800000u : 0x00003f80u;
-    *reinterpret_cast<uint4*>(sm + kIdent + n * 128 + ((cc ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  write_identity(sm + kIdent, kThreads);
   fence_proxy_async();
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(tmem_slot)), "r"(512u)
@@ -171,6 +109,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   int loaded = 0;                                            // chunks requested (producer)
   bool issued = false;                                       // MMAs issued (MMA warp)
 
+  if (warp >= 12) regs_dec<80>();
   if (warp == 12) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * kRecBytes;
@@ -199,11 +138,8 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       if (tail) {                                            // the last chunk: zeros behind the sequence
         if (!(ok = wwait(fb, 0, abort_flag, nullptr, 0))) break;
         const int r0 = len - c * L;
-        for (int i = lane; i < (L - r0) * 8; i += 32) {
-          const uint32_t off = (uint32_t)(r0 * 128 + i * 16);
-          for (int j = 0; j < kHK; ++j) *reinterpret_cast<uint4*>(sm + s * kStage + kK + j * kHalf + off) = make_uint4(0, 0, 0, 0);
-          for (int j = 0; j < kHV; ++j) *reinterpret_cast<uint4*>(sm + s * kStage + kV + j * kHalf + off) = make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < kHK; ++j) zero_rows(sm + s * kStage + kK + j * kHalf, r0, lane);
+        for (int j = 0; j < kHV; ++j) zero_rows(sm + s * kStage + kV + j * kHalf, r0, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bFull + s));
@@ -306,6 +242,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
   } else if (warp < 8) {
     // ========================================================== chain warps
+    regs_inc<144>();
     constexpr int QC = DK / 4;                                 // S columns per thread and half
     const int row = (warp & 3) * 32 + lane, hc = warp >> 2;    // value channel = TMEM lane; which columns
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -463,20 +400,22 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
       }
     }
-  } else {
+  } else if (warp < 12) {
     // ==================================================== O, or the images
+    regs_inc<144>();
     const int quad = warp - 8, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
     __nv_bfloat16* op = a.o + b * a.os.b + h * a.os.h;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
-      if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
+      ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0);
+      if (!OUT && !ok) break;                                  // (O: the warps meet at the vote below)
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       const long long img = (long long)u * a.chunks + cb + c;
       if (KIND == kStateOnly) {
         if (lane == 0) mbar_arrive(bar(bEmpty + s));
       } else if (OUT) {
-        if (!(ok = wwait(bar(bQS), ph, abort_flag, nullptr, 0))) break;
+        ok = ok && wwait(bar(bQS), ph, abort_flag, nullptr, 0);
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -500,7 +439,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mbar_arrive(bar(bEmpty + s));
           mbar_arrive(bar(bOs));
         }
-        if (!(ok = wwait(bar(bO), ph, abort_flag, nullptr, 0))) break;
+        ok = ok && wwait(bar(bO), ph, abort_flag, nullptr, 0);
         tc_fence_after();
         uint32_t r[2][32];
         tmem_ld32(la + kColO, r[0]);
@@ -512,7 +451,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // token rows in shared memory, then one TMA store per half; the last
         // chunk's rows behind the sequence are not written
         if (tid == 256) bulk_wait_read();                      // the chunk before has left the buffer
-        bar_sync(1, 128);
+        if (!(ok = bar_and(1, 128, ok))) break;
         if (row < DV) {
           const uint32_t col = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
           const int cc = (row & 63) >> 3;
@@ -593,16 +532,6 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   __syncthreads();
   if (warp == 13)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-}
-
-// [channels, heads, T, B] with the tensor's strides; boxes of 64 tokens x 64 channels
-inline bool map_of(CUtensorMap* m, const void* p, int D, int heads, int T, int B, Strides4 s) {
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
-  // the stride of an extent of 1 is never used, and need not be valid
-  const cuuint64_t sb[3] = {(cuuint64_t)(heads > 1 ? s.h : D) * 2, (cuuint64_t)(T > 1 ? s.t : D) * 2,
-                            (cuuint64_t)(B > 1 ? s.b : D) * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)L, 1};
-  return tc::encode(m, p, 4, dims, sb, box);
 }
 
 // The states that the segments start from: S_0 as given, S_1 = n_0, S_{g+1} = S_g

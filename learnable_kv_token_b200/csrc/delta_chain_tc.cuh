@@ -1,0 +1,101 @@
+// What the tcgen05 chains of the gated delta rule share.
+#pragma once
+
+#include "delta_chunk.cuh"
+#include "tc_ptx.cuh"
+
+namespace lte {
+namespace delta {
+namespace chaintc {
+
+using namespace tc;
+
+constexpr uint32_t kHalf = L * 128;                          // [64 tokens][64 channels] bf16, 128B-swizzled
+// columns of a bf16 operand that lies as hi (16) and lo (16) over each 32 fp32 columns it was made from
+__device__ __forceinline__ uint32_t pair_col(int ks, int lo) { return 32 * (ks >> 1) + 16 * lo + 8 * (ks & 1); }
+__device__ __forceinline__ uint32_t idesc2(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Registers go from the warps that load and issue to those that compute: 4 warp
+// groups of 128 registers a thread at launch, 144 + 144 + 144 + 80 after.  (With
+// nearly all of the L1 cache as shared memory, a spilled register costs a trip to
+// L2.)  All four warps of a group call these.
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// two fp32 values in one register pair
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a pair -> bf16 hi and lo words (as split2)
+__device__ __forceinline__ void split_pair(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float x0, x1;
+  unf2(x, x0, x1);
+  hi = pack_bf16(x0, x1);
+  unf2(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x), x0, x1);
+  lo = pack_bf16(x0, x1);
+}
+template <int N>
+__device__ __forceinline__ void split_pairs(const uint64_t (&x)[N], uint32_t (&hi)[N], uint32_t (&lo)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) split_pair(x[e], hi[e], lo[e]);
+}
+// columns of this warp's lanes <-> registers, by count
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[32]) { tmem_st32(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* r) { return f2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+
+// the identity [n][k] bf16 in shared memory (all threads of the CTA)
+__device__ __forceinline__ void write_identity(uint8_t* p, int threads) {
+  for (int i = threadIdx.x; i < L * 8; i += threads) {
+    const int n = i >> 3, cc = i & 7;
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (cc == n >> 3) w[(n & 7) >> 1] = (n & 1) ? 0x3f800000u : 0x00003f80u;
+    *reinterpret_cast<uint4*>(p + n * 128 + ((cc ^ (n & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// zeros in rows [r0, 64) of a half (the lanes of one warp)
+__device__ __forceinline__ void zero_rows(uint8_t* half, int r0, int lane) {
+  for (int i = lane; i < (L - r0) * 8; i += 32) *reinterpret_cast<uint4*>(half + r0 * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// [channels, heads, T, B] with the tensor's strides; boxes of 64 tokens x 64 channels
+inline bool map_of(CUtensorMap* m, const void* p, int D, int heads, int T, int B, Strides4 s) {
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
+  // the stride of an extent of 1 is never used, and need not be valid
+  const cuuint64_t sb[3] = {(cuuint64_t)(heads > 1 ? s.h : D) * 2, (cuuint64_t)(T > 1 ? s.t : D) * 2,
+                            (cuuint64_t)(B > 1 ? s.b : D) * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)L, 1};
+  return tc::encode(m, p, 4, dims, sb, box);
+}
+
+}  // namespace chaintc
+}  // namespace delta
+}  // namespace lte

@@ -97,6 +97,11 @@ __device__ __forceinline__ void load_linear(uint32_t dst, const uint8_t* src) {
   for (int i = threadIdx.x; i < BYTES / 16; i += THREADS) cp_async16(dst + i * 16, src + i * 16, true);
 }
 
+// 16-byte multiples of contiguous memory on their way to L2
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
   return lens == nullptr ? T : min(max(lens[b], 0), T);
 }
@@ -126,6 +131,18 @@ struct ChunkArgs {
   float *seg_n, *seg_x, *seg_s;
 };
 
+struct GradArgs {
+  ChunkArgs f;
+  const __nv_bfloat16* dO;
+  Strides4 dos;
+  const float* ds_out;       // gradient of the final state (NULL = zeros)
+  float* ds_in;              // gradient of the initial state (nullable)
+  __nv_bfloat16 *dq, *dk, *dv;
+  float *dg, *db;
+  uint32_t *ds, *fimg;       // images of dS (hi) and F (hi) per chunk
+  float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
+};
+
 // delta_chunk.cu
 cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t stream);
 // the chain of states; with s0 and u, writes their images instead of o
@@ -134,6 +151,8 @@ cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream
 // delta_chain_tc.cu: the same on tcgen05; *done = false if a tensor's strides do not suit TMA
 int chain_segments(long long units, int chunks);
 cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done);
+// delta_back_tc.cu: the backward chain, likewise
+cudaError_t back_chain_tc(const GradArgs& a, int B, int dk, cudaStream_t stream, bool* done);
 
 }  // namespace delta
 }  // namespace lte
