@@ -641,15 +641,15 @@ cudaError_t launch(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t 
 
 }  // namespace backtc
 
-cudaError_t back_chain_tc(const GradArgs& g, int B, int dk, cudaStream_t stream, bool* done) {
+cudaError_t back_chain(const GradArgs& g, int B, int dk, cudaStream_t stream) {
   using namespace backtc;
   const ChunkArgs& a = g.f;
   CUtensorMap m[5];
   const Strides4 out{(long long)a.T * a.H * a.dv, (long long)a.H * a.dv, a.dv};
-  *done = map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) && map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) &&
-          map_of(&m[2], g.dO, a.dv, a.H, a.T, B, g.dos) && map_of(&m[3], a.v, a.dv, a.H, a.T, B, a.vs) &&
-          map_of(&m[4], g.dv, a.dv, a.H, a.T, B, out);
-  if (!*done) return cudaSuccess;
+  if (!map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) || !map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) ||
+      !map_of(&m[2], g.dO, a.dv, a.H, a.T, B, g.dos) || !map_of(&m[3], a.v, a.dv, a.H, a.T, B, a.vs) ||
+      !map_of(&m[4], g.dv, a.dv, a.H, a.T, B, out))
+    return cudaErrorNotSupported;
   if (dk == 128) return a.dv == 128 ? launch<128, 128>(m, g, B, stream) : launch<128, 64>(m, g, B, stream);
   return a.dv == 128 ? launch<64, 128>(m, g, B, stream) : launch<64, 64>(m, g, B, stream);
 }

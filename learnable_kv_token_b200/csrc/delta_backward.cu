@@ -14,271 +14,15 @@
 //          is read from t on is linear in S_{t-1} and the v together, and
 //          linear in q), which within a chunk runs from dg_first = <dS_0, S_0>:
 //          no difference of long sums.
-// Launches: the per-chunk systems, the forward chain (S_0 and U of every chunk
-// to the workspace), the backward chain (dS, F, dV), then all chunks at once
-// for dQ, dK, dg, db.  The sums over value channels and over the heads that
+// Launches: the per-chunk systems (delta_prepare.cu), the forward chain with S_0
+// and U of every chunk to the workspace (delta_chain_tc.cu), the backward chain
+// with dS, F and dV (delta_back_tc.cu), then all chunks at once for dQ, dK, dg and
+// db (here).  The sums over value channels and over the heads that
 // share a key run in a fixed order: no atomics.
 #include "delta_chunk.cuh"
 
 namespace lte {
 namespace delta {
-
-// ------------------------------------------------------------- backward chain
-// As the forward chain: a warp per 16 value channels, products transposed, each
-// result the next one's A operand in place.
-template <int DK, int W>
-struct BackSmem {
-  static constexpr int kK = 0, kQ = L * DK * 2, kD = 2 * L * DK * 2, kV = kD + L * 32 * W;
-  static constexpr int kR = kV + L * 32 * W, kS = kR + 4 * kImg, kStage = kS + kScal;
-  static constexpr int kO = 2 * kStage, kTotal = kO + W * L * 32;
-};
-
-template <int DK, int W>
-__global__ void __launch_bounds__(W * 32)
-delta_back_chain_kernel(const GradArgs ga) {
-  using SM = BackSmem<DK, W>;
-  const ChunkArgs& a = ga.f;
-  extern __shared__ __align__(128) uint8_t sm[];
-  constexpr int kThr = W * 32;
-  const int slices = a.dv / (16 * W);
-  const int u = blockIdx.x / slices, slice = blockIdx.x % slices;
-  const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int len = seq_len(a.lens, b, a.T), n_chunks = (len + L - 1) / L;
-  const int strip = slice * W + warp, strips = a.dv / 16;
-  const uint32_t s0 = smem_u32(sm);
-  const __nv_bfloat16* kp = a.k + b * a.ks.b + hk * a.ks.h;
-  const __nv_bfloat16* qp = a.q + b * a.qs.b + hk * a.qs.h;
-  const __nv_bfloat16* dop = ga.dO + b * ga.dos.b + h * ga.dos.h + slice * W * 16;
-  const __nv_bfloat16* vp = a.v + b * a.vs.b + h * a.vs.h + slice * W * 16;
-  __nv_bfloat16* dvp = ga.dv + ((long long)b * a.T * a.H + h) * a.dv + strip * 16;
-  const uint8_t* recs = a.rec + (long long)u * a.chunks * rec_bytes(true);
-  auto load = [&](int c) {
-    const uint32_t d = s0 + (c & 1) * SM::kStage;
-    const int t0 = c * L;
-    load_rows<DK, kThr>(d + SM::kK, kp, a.ks.t, t0, len);
-    load_rows<DK, kThr>(d + SM::kQ, qp, a.qs.t, t0, len);
-    for (int i = tid; i < L * 2 * W; i += kThr) {
-      const int t = i / (2 * W), cc = i % (2 * W);
-      const bool ok = t0 + t < len;
-      cp_async16(d + SM::kD + swz_cols<W>(t, cc), dop + (long long)(ok ? t0 + t : t0) * ga.dos.t + cc * 8, ok);
-      cp_async16(d + SM::kV + swz_cols<W>(t, cc), vp + (long long)(ok ? t0 + t : t0) * a.vs.t + cc * 8, ok);
-    }
-    load_linear<4 * kImg + kScal, kThr>(d + SM::kR, recs + (long long)c * rec_bytes(true));
-    cp_async_commit();
-  };
-  if (n_chunks > 0) load(n_chunks - 1);
-  float S[DK / 8][4];                                      // dS, rows = value channels
-  const long long srow = ((long long)u * a.dv + strip * 16 + g) * DK + t2;
-#pragma unroll
-  for (int j = 0; j < DK / 8; ++j) {
-    float2 x = make_float2(0.f, 0.f), y = x;
-    if (ga.ds_out != nullptr) {
-      x = *reinterpret_cast<const float2*>(ga.ds_out + srow + 8 * j);
-      y = *reinterpret_cast<const float2*>(ga.ds_out + srow + 8 * DK + 8 * j);
-    }
-    S[j][0] = x.x; S[j][1] = x.y; S[j][2] = y.x; S[j][3] = y.y;
-  }
-  for (int c = n_chunks - 1; c >= 0; --c) {
-    cp_async_wait<0>();
-    __syncthreads();
-    if (c > 0) load(c - 1);
-    const uint32_t d = s0 + (c & 1) * SM::kStage;
-    const float* scal = reinterpret_cast<const float*>(sm + (c & 1) * SM::kStage + SM::kS);
-    const float* eG = scal + kEG * L;
-    const float* lam = scal + kLam * L;
-    const float* beta = scal + kBeta * L;
-    const long long img = (long long)u * a.chunks + c;
-    // ---- P^T = dS K^T
-    float P[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) P[n][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t hi[4], lo[4];
-      split_a(S[2 * ks], S[2 * ks + 1], hi, lo);
-      uint32_t* im = ga.ds + img * (a.dv * DK / 2);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) im[block_word(strip * 2 + (e & 1), 2 * ks + (e >> 1), DK / 8, lane)] = hi[e];
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t x[4];
-        ldsm_x4(d + SM::kK + swz<DK>(16 * np + ldn_row(lane), 2 * ks + ldn_col(lane)), x[0], x[1], x[2], x[3]);
-        mma_bf16(P[2 * np], hi, x[0], x[1]);
-        mma_bf16(P[2 * np + 1], hi, x[2], x[3]);
-        mma_bf16(P[2 * np], lo, x[0], x[1]);
-        mma_bf16(P[2 * np + 1], lo, x[2], x[3]);
-      }
-    }
-    // ---- dU^T = P^T diag(e^{G_L - G}) + dO^T A
-    uint32_t dof[4][4];                                    // dO^T as the A operand of each token step
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      ldsm_x4_t(d + SM::kD + swz_cols<W>(16 * ks + ldn_row(lane), 2 * warp + ldn_col(lane)), dof[ks][0], dof[ks][1],
-                dof[ks][2], dof[ks][3]);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 f = *reinterpret_cast<const float2*>(lam + 8 * n + t2);
-      P[n][0] *= f.x; P[n][1] *= f.y; P[n][2] *= f.x; P[n][3] *= f.y;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-#pragma unroll
-      for (int np = 0; np <= ks; ++np) {
-        uint32_t x[4];
-        const uint32_t off = swz<64>(16 * ks + ldt_row(lane), 2 * np + ldt_col(lane));
-        ldsm_x4_t(d + SM::kR + 2 * kImg + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(P[2 * np], dof[ks], x[0], x[1]);
-        mma_bf16(P[2 * np + 1], dof[ks], x[2], x[3]);
-        ldsm_x4_t(d + SM::kR + 3 * kImg + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(P[2 * np], dof[ks], x[0], x[1]);
-        mma_bf16(P[2 * np + 1], dof[ks], x[2], x[3]);
-      }
-    }
-    // ---- F^T = dU^T T (the diagonal b in fp32)
-    float F[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * n + t2);
-      F[n][0] = bt.x * P[n][0]; F[n][1] = bt.y * P[n][1];
-      F[n][2] = bt.x * P[n][2]; F[n][3] = bt.y * P[n][3];
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t hi[4], lo[4];
-      split_a(P[2 * ks], P[2 * ks + 1], hi, lo);
-#pragma unroll
-      for (int np = 0; np <= ks; ++np) {
-        uint32_t x[4];
-        const uint32_t off = swz<64>(16 * ks + ldt_row(lane), 2 * np + ldt_col(lane));
-        ldsm_x4_t(d + SM::kR + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(F[2 * np], hi, x[0], x[1]);
-        mma_bf16(F[2 * np + 1], hi, x[2], x[3]);
-        mma_bf16(F[2 * np], lo, x[0], x[1]);
-        mma_bf16(F[2 * np + 1], lo, x[2], x[3]);
-        ldsm_x4_t(d + SM::kR + kImg + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(F[2 * np], hi, x[0], x[1]);
-        mma_bf16(F[2 * np + 1], hi, x[2], x[3]);
-      }
-    }
-    // ---- F out: its image, dV = F (one rounding), u.y and v.F per token over this strip
-    {
-      uint32_t* im = ga.fimg + img * (a.dv * L / 2);
-      const uint32_t* uh = a.u + img * a.dv * L;
-      const uint32_t* ul = uh + (long long)a.dv * L / 2;
-      const uint32_t so = s0 + SM::kO + warp * (L * 32);
-      __syncwarp();
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t w[4], vv[4];
-        float xs[4], vs[4];
-        ldsm_x4_t(d + SM::kV + swz_cols<W>(16 * np + ldn_row(lane), 2 * warp + ldn_col(lane)), vv[0], vv[1], vv[2],
-                  vv[3]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = 2 * np + i;
-          vs[2 * i] = F[n][0] * bf_lo(vv[2 * i]) + F[n][2] * bf_lo(vv[2 * i + 1]);
-          vs[2 * i + 1] = F[n][1] * bf_hi(vv[2 * i]) + F[n][3] * bf_hi(vv[2 * i + 1]);
-          w[2 * i] = pack_bf16(F[n][0], F[n][1]);
-          w[2 * i + 1] = pack_bf16(F[n][2], F[n][3]);
-          const long long w0 = block_word(strip * 2, n, L / 8, lane), w1 = block_word(strip * 2 + 1, n, L / 8, lane);
-          im[w0] = w[2 * i];
-          im[w1] = w[2 * i + 1];
-          const uint32_t a0 = __ldg(uh + w0), a1 = __ldg(uh + w1), l0 = __ldg(ul + w0), l1 = __ldg(ul + w1);
-          const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * n + t2);
-          const float r0 = 1.f / bt.x, r1 = 1.f / bt.y;
-          xs[2 * i] = (F[n][0] * r0) * (bf_lo(a0) + bf_lo(l0)) + (F[n][2] * r0) * (bf_lo(a1) + bf_lo(l1));
-          xs[2 * i + 1] = (F[n][1] * r1) * (bf_hi(a0) + bf_hi(l0)) + (F[n][3] * r1) * (bf_hi(a1) + bf_hi(l1));
-        }
-        stsm_x4_t(so + swz_cols<1>(16 * np + ldn_row(lane), ldn_col(lane)), w[0], w[1], w[2], w[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) {
-            xs[e] += __shfl_xor_sync(0xffffffffu, xs[e], o);
-            vs[e] += __shfl_xor_sync(0xffffffffu, vs[e], o);
-          }
-        if (g == 0) {
-          float* out = ga.x + (img * strips + strip) * (2 * L) + 16 * np + t2;
-          *reinterpret_cast<float2*>(out) = make_float2(xs[0], xs[1]);
-          *reinterpret_cast<float2*>(out + 8) = make_float2(xs[2], xs[3]);
-          *reinterpret_cast<float2*>(out + L) = make_float2(vs[0], vs[1]);
-          *reinterpret_cast<float2*>(out + L + 8) = make_float2(vs[2], vs[3]);
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * i + (lane >> 1), cc = lane & 1;
-        if (c * L + t < len)
-          *reinterpret_cast<uint4*>(dvp + (long long)(c * L + t) * a.H * a.dv + cc * 8) =
-              *reinterpret_cast<const uint4*>(sm + SM::kO + warp * (L * 32) + swz_cols<1>(t, cc));
-      }
-    }
-    // ---- dS_0 = e^{G_L} dS + (scale e^G dO)^T Q - (e^G F)^T K
-    const float el = eG[L - 1];
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[j][e] *= el;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t dh[4], dl[4], fh[4], fl[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 f = *reinterpret_cast<const float2*>(eG + 16 * ks + 8 * i + t2);
-        const float f0 = a.scale * f.x, f1 = a.scale * f.y;
-        split2(f0 * bf_lo(dof[ks][2 * i]), f1 * bf_hi(dof[ks][2 * i]), dh[2 * i], dl[2 * i]);
-        split2(f0 * bf_lo(dof[ks][2 * i + 1]), f1 * bf_hi(dof[ks][2 * i + 1]), dh[2 * i + 1], dl[2 * i + 1]);
-        float* x = F[2 * ks + i];
-        split2(-f.x * x[0], -f.y * x[1], fh[2 * i], fl[2 * i]);
-        split2(-f.x * x[2], -f.y * x[3], fh[2 * i + 1], fl[2 * i + 1]);
-      }
-#pragma unroll
-      for (int j = 0; j < DK / 16; ++j) {
-        uint32_t x[4];
-        const uint32_t off = swz<DK>(16 * ks + ldt_row(lane), 2 * j + ldt_col(lane));
-        ldsm_x4_t(d + SM::kQ + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(S[2 * j], dh, x[0], x[1]);
-        mma_bf16(S[2 * j + 1], dh, x[2], x[3]);
-        mma_bf16(S[2 * j], dl, x[0], x[1]);
-        mma_bf16(S[2 * j + 1], dl, x[2], x[3]);
-        ldsm_x4_t(d + SM::kK + off, x[0], x[1], x[2], x[3]);
-        mma_bf16(S[2 * j], fh, x[0], x[1]);
-        mma_bf16(S[2 * j + 1], fh, x[2], x[3]);
-        mma_bf16(S[2 * j], fl, x[0], x[1]);
-        mma_bf16(S[2 * j + 1], fl, x[2], x[3]);
-      }
-    }
-    // ---- <dS_0, S_0> over this strip
-    {
-      const uint32_t* sh = a.s0 + img * a.dv * DK;
-      const uint32_t* sl = sh + (long long)a.dv * DK / 2;
-      float in = 0.f;
-#pragma unroll
-      for (int j = 0; j < DK / 8; ++j) {
-        const long long w0 = block_word(strip * 2, j, DK / 8, lane), w1 = block_word(strip * 2 + 1, j, DK / 8, lane);
-        const uint32_t a0 = __ldg(sh + w0), a1 = __ldg(sh + w1), l0 = __ldg(sl + w0), l1 = __ldg(sl + w1);
-        in = fmaf(S[j][0], bf_lo(a0) + bf_lo(l0), in);
-        in = fmaf(S[j][1], bf_hi(a0) + bf_hi(l0), in);
-        in = fmaf(S[j][2], bf_lo(a1) + bf_lo(l1), in);
-        in = fmaf(S[j][3], bf_hi(a1) + bf_hi(l1), in);
-      }
-#pragma unroll
-      for (int o = 1; o <= 16; o <<= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
-      if (lane == 0) ga.inner[img * strips + strip] = in;
-    }
-  }
-  if (ga.ds_in != nullptr) {
-#pragma unroll
-    for (int j = 0; j < DK / 8; ++j) {
-      *reinterpret_cast<float2*>(ga.ds_in + srow + 8 * j) = make_float2(S[j][0], S[j][1]);
-      *reinterpret_cast<float2*>(ga.ds_in + srow + 8 * DK + 8 * j) = make_float2(S[j][2], S[j][3]);
-    }
-  }
-}
 
 // -------------------------------------------------------------- all chunks
 // One CTA of eight warps per (batch, key head, chunk): warp (m, half) has token
@@ -586,25 +330,6 @@ delta_grad_kernel(const GradArgs ga) {
   }
 }
 
-template <int DK, int W>
-cudaError_t launch_back(const GradArgs& a, int B, cudaStream_t stream) {
-  constexpr int smem = BackSmem<DK, W>::kTotal;
-  cudaError_t e = cudaFuncSetAttribute(delta_back_chain_kernel<DK, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  delta_back_chain_kernel<DK, W><<<(unsigned)(B * a.f.H) * (a.f.dv / (16 * W)), W * 32, smem, stream>>>(a);
-  return cudaGetLastError();
-}
-template <int DK>
-cudaError_t back_chain(const GradArgs& a, int B, cudaStream_t stream) {
-  bool done = false;
-  const cudaError_t e = back_chain_tc(a, B, DK, stream, &done);
-  if (done) return e;
-  const long long strips = (long long)B * a.f.H * (a.f.dv / 16);   // as the forward chain
-  if (strips >= 8 * 96 && a.f.dv == 128) return launch_back<DK, 8>(a, B, stream);
-  if (strips >= 4 * 148) return launch_back<DK, 4>(a, B, stream);
-  if (strips >= 2 * 148) return launch_back<DK, 2>(a, B, stream);
-  return launch_back<DK, 1>(a, B, stream);
-}
 template <int DK, int DV>
 cudaError_t grad(const GradArgs& a, int B, cudaStream_t stream) {
   constexpr int smem = GradSmem<DK, DV>::kTotal;
@@ -653,8 +378,7 @@ cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStre
   n.x = (float*)(ws + w.x); n.inner = (float*)(ws + w.inner);
   cudaError_t e = delta::prepare(c, d->B, d->dk, true, stream);
   if (e == cudaSuccess) e = delta::forward_chain(c, d->B, d->dk, stream);
-  if (e == cudaSuccess)
-    e = d->dk == 128 ? delta::back_chain<128>(n, d->B, stream) : delta::back_chain<64>(n, d->B, stream);
+  if (e == cudaSuccess) e = delta::back_chain(n, d->B, d->dk, stream);
   if (e != cudaSuccess) return e;
   if (d->dk == 128)
     return d->dv == 128 ? delta::grad<128, 128>(n, d->B, stream) : delta::grad<128, 64>(n, d->B, stream);

@@ -620,12 +620,12 @@ cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t st
 
 }  // namespace chaintc
 
-cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done) {
+cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream) {
   CUtensorMap m[4];
-  *done = chaintc::map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) && chaintc::map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) &&
-          chaintc::map_of(&m[2], a.v, a.dv, a.H, a.T, B, a.vs) &&
-          (a.s0 != nullptr || chaintc::map_of(&m[3], a.o, a.dv, a.H, a.T, B, a.os));
-  if (!*done) return cudaSuccess;
+  if (!chaintc::map_of(&m[0], a.q, dk, a.Hk, a.T, B, a.qs) || !chaintc::map_of(&m[1], a.k, dk, a.Hk, a.T, B, a.ks) ||
+      !chaintc::map_of(&m[2], a.v, a.dv, a.H, a.T, B, a.vs) ||
+      (a.s0 == nullptr && !chaintc::map_of(&m[3], a.o, a.dv, a.H, a.T, B, a.os)))
+    return cudaErrorNotSupported;
   if (dk == 128) return a.dv == 128 ? chaintc::run<128, 128>(m, a, B, stream) : chaintc::run<128, 64>(m, a, B, stream);
   return a.dv == 128 ? chaintc::run<64, 128>(m, a, B, stream) : chaintc::run<64, 64>(m, a, B, stream);
 }

@@ -22,6 +22,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
 // Registers go from the warps that load and issue to those that compute: 4 warp
 // groups of 128 registers a thread at launch, 144 + 144 + 144 + 80 after.  (With
 // nearly all of the L1 cache as shared memory, a spilled register costs a trip to

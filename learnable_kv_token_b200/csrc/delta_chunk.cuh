@@ -10,7 +10,7 @@
 //   O   = scale diag(e^G) Q S_0^T + A U,  A_ts = scale e^{G_t - G_s} q_t.k_s  (s <= t)
 //   S_L = e^{G_L} S_0 + U^T diag(e^{G_L - G}) K.
 // T and A depend on no state: one launch computes them for every chunk at
-// once (delta_prepare_kernel).  Every exponent is a difference taken forwards
+// once (delta_prepare.cu).  Every exponent is a difference taken forwards
 // in time, so with g <= 0 no factor exceeds 1, whatever the decay.
 //
 // Precision.  q, k, v and their gradients are bf16, exact as operands.  Where a
@@ -44,28 +44,12 @@ __host__ __device__ constexpr int rec_bytes(bool a_lo) { return (a_lo ? 4 : 3) *
 // (the gradient of b is y.e).
 __device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-60f ? 0x1p-60f : b; }
 
-// Order of 16-byte pieces in a tile of `16 * W` columns of 2 bytes: the eight
-// rows that one ldmatrix reads lie in eight different bank groups.
-template <int W>
-__device__ __forceinline__ uint32_t swz_cols(int r, int c) {
-  if (W >= 4) return (uint32_t)(r * 32 * W + ((c ^ (r & 7)) << 4));
-  if (W == 2) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-  return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
-}
-
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 // (x0, x1) as bf16 pairs: hi rounded to nearest, lo the rounded remainder
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(x0, x1);
   lo = pack_bf16(x0 - bf_lo(hi), x1 - bf_hi(hi));
-}
-// accumulator tiles c0, c1 (columns 16 kk .. + 7, + 8 .. + 15) as the A operand of k-step kk
-__device__ __forceinline__ void split_a(const float* c0, const float* c1, uint32_t* hi, uint32_t* lo) {
-  split2(c0[0], c0[1], hi[0], lo[0]);
-  split2(c0[2], c0[3], hi[1], lo[1]);
-  split2(c1[0], c1[1], hi[2], lo[2]);
-  split2(c1[2], c1[3], hi[3], lo[3]);
 }
 
 // B operand pair from [n][k] rows: n-tiles n0, n0 + 8 of k-step at 16-byte piece c
@@ -74,12 +58,6 @@ __device__ __forceinline__ int ldn_col(int lane) { return (lane >> 3) & 1; }
 // B operand pair from [k][n] rows (transposed load): k-step rows, n-tiles at pieces c, c + 1
 __device__ __forceinline__ int ldt_row(int lane) { return (lane & 7) + ((lane >> 3) & 1) * 8; }
 __device__ __forceinline__ int ldt_col(int lane) { return (lane >> 4) & 1; }
-
-__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r0),
-               "r"(r1), "r"(r2), "r"(r3)
-               : "memory");
-}
 
 // rows [t0, t0 + 64) of a [T][D] tensor (row stride `ts`) -> a swizzled tile,
 // zeros from row `len` on
@@ -106,13 +84,9 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
   return lens == nullptr ? T : min(max(lens[b], 0), T);
 }
 
-// Images of [rows][cols] bf16 in blocks of 8 x 8 (128 bytes: row g at 16 g): an
-// accumulator register of a warp is one block, so a warp stores and loads it as
-// 32 consecutive words, and ldmatrix reads blocks without bank conflicts.
-__device__ __forceinline__ long long block_word(int rb, int cb, int cbs, int lane) {
-  return ((long long)rb * cbs + cb) * 32 + lane;
-}
-
+// Images of S_0, U, dS and F: [rows][cols] bf16 in blocks of 8 x 8 (128 bytes: row g
+// at 16 g), rows = value channels.  A thread that has a row stores 16 bytes per
+// block, eight threads a block; ldmatrix reads blocks without bank conflicts.
 struct ChunkArgs {
   const __nv_bfloat16 *q, *k, *v;
   Strides4 qs, ks, vs, os;
@@ -143,16 +117,15 @@ struct GradArgs {
   float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
 };
 
-// delta_chunk.cu
+// Each returns cudaErrorNotSupported, without a launch, for tensors whose strides
+// TMA does not take.
+// delta_prepare.cu: the records of all chunks (with A's lo for the gradients)
 cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t stream);
-// the chain of states; with s0 and u, writes their images instead of o
+// delta_chain_tc.cu: the chain of states with O; with s0 and u, writes their images instead of O
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
-
-// delta_chain_tc.cu: the same on tcgen05; *done = false if a tensor's strides do not suit TMA
 int chain_segments(long long units, int chunks);
-cudaError_t forward_chain_tc(const ChunkArgs& a, int B, int dk, cudaStream_t stream, bool* done);
-// delta_back_tc.cu: the backward chain, likewise
-cudaError_t back_chain_tc(const GradArgs& a, int B, int dk, cudaStream_t stream, bool* done);
+// delta_back_tc.cu: the backward chain
+cudaError_t back_chain(const GradArgs& a, int B, int dk, cudaStream_t stream);
 
 }  // namespace delta
 }  // namespace lte

@@ -613,7 +613,8 @@ lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k,
   a.s_in = state_in; a.scratch = workspace;
   n.dO = dO; n.ds_out = dstate_out; n.dq = dq; n.dk = dk; n.dv = dv;
   n.dg = dg; n.db = dbeta; n.ds_in = dstate_in;
-  return from_cuda(lte::delta_backward(a, n, as_stream(stream)));
+  const cudaError_t e = lte::delta_backward(a, n, as_stream(stream));
+  return e == cudaErrorNotSupported ? LTE_ERR_UNSUPPORTED : from_cuda(e);
 }
 
 lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,

@@ -150,6 +150,16 @@ def test_prefill_long_few_heads(layer, shape, lens):
     assert S2 is st and torch.equal(o, o2) and torch.equal(S, st)
 
 
+def test_broadcast_and_padded_views(layer):
+    """Keys shared by the batch as an expanded view, values in rows wider than they need."""
+    x = inputs(41, 3, 100, 2, 2, 64, 128)
+    wide = torch.zeros(3, 100, 2, 192, dtype=torch.bfloat16, device="cuda")
+    wide[..., 64:] = x["v"]
+    y = {**x, "q": x["q"][:1].expand(3, -1, -1, -1), "k": x["k"][:1].expand(3, -1, -1, -1), "v": wide[..., 64:]}
+    check_prefill(layer, y)
+    check_backward(layer, y)
+
+
 def test_prefill_continues(layer):
     """A prompt in three calls, in place on one state, equals the prompt in one call."""
     x = inputs(4, 2, 300, 4, 4, 128, 128)
