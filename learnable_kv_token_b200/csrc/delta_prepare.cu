@@ -40,17 +40,17 @@ __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// c (16 x 8 NT) = sign A (16 x 8 KS) B (8 KS x 8 NT), row stride kXs: three TF32
+// c (16 x 8 NT) = A (16 x 8 KS) B (8 KS x 8 NT), row stride kXs: three TF32
 // products per step keep about 21 bits
 template <int NT, int KS>
-__device__ __forceinline__ void mma_tf32x3(float (&c)[NT][4], const float* A, const float* B, float sign, int lane) {
+__device__ __forceinline__ void mma_tf32x3(float (&c)[NT][4], const float* A, const float* B, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int k = 0; k < KS; ++k) {
     uint32_t ah[4], al[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      split_tf32(sign * A[(g + 8 * (e & 1)) * kXs + 8 * k + t + 4 * (e >> 1)], ah[e], al[e]);
+      split_tf32(A[(g + 8 * (e & 1)) * kXs + 8 * k + t + 4 * (e >> 1)], ah[e], al[e]);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       uint32_t bh[2], bl[2];
@@ -62,10 +62,10 @@ __device__ __forceinline__ void mma_tf32x3(float (&c)[NT][4], const float* A, co
     }
   }
 }
-__device__ __forceinline__ void store_c(float* p, const float* c, int lane) {
+__device__ __forceinline__ void store_c(float* p, const float* c, int lane, float sign = 1.f) {
   float* q = p + (lane >> 2) * kXs + (lane & 3) * 2;
-  *reinterpret_cast<float2*>(q) = make_float2(c[0], c[1]);
-  *reinterpret_cast<float2*>(q + 8 * kXs) = make_float2(c[2], c[3]);
+  *reinterpret_cast<float2*>(q) = make_float2(sign * c[0], sign * c[1]);
+  *reinterpret_cast<float2*>(q + 8 * kXs) = make_float2(sign * c[2], sign * c[3]);
 }
 
 
@@ -179,6 +179,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const bool keys = warp < 2;
       const float f = keys ? bs[t] : a.scale;
       const int last = keys ? t - 1 : t;                  // M is strictly below the diagonal
+      const uint64_t gh = f2(Gt.x, Gt.x), gl = f2(Gt.y, Gt.y), ff = f2(f, f), minus = f2(-1.f, -1.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {                       // 16 columns
         float y[16];
@@ -188,10 +189,16 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
+            // G2 holds two columns as (hi, lo, hi, lo): gathered as pairs of hi and of lo
             const float4 Gs = *reinterpret_cast<const float4*>(&G2[16 * j + e]);
-            const float d0 = ex2((Gt.x - Gs.x) + (Gt.y - Gs.y)), d1 = ex2((Gt.x - Gs.z) + (Gt.y - Gs.w));
-            y[e] = 16 * j + e <= last ? f * (d0 * __uint_as_float(r[e])) : 0.f;
-            y[e + 1] = 16 * j + e + 1 <= last ? f * (d1 * __uint_as_float(r[e + 1])) : 0.f;
+            const uint64_t d = fma2(f2(Gs.x, Gs.z), minus, gh), dl = fma2(f2(Gs.y, Gs.w), minus, gl);
+            float d0, d1;
+            unf2(fma2(dl, f2(1.f, 1.f), d), d0, d1);
+            unf2(mul2(mul2(pair_of(r + e), ff), f2(ex2(d0), ex2(d1))), y[e], y[e + 1]);
+          }
+          if (j >= 2 * far) {                             // a block on the diagonal of this warp's rows
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = 16 * j + e <= last ? y[e] : 0.f;
           }
         } else {
 #pragma unroll
@@ -250,13 +257,13 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     {
       const int c0 = 32 * (warp >> 1), r0 = c0 + 16, n0 = 8 * (warp & 1);
       float w[1][4] = {};
-      mma_tf32x3<1, 2>(w, &M[r0 * kXs + c0], &M[c0 * kXs + c0 + n0], 1.f, lane);
+      mma_tf32x3<1, 2>(w, &M[r0 * kXs + c0], &M[c0 * kXs + c0 + n0], lane);
       store_c(&M[c0 * kXs + r0 + n0], w[0], lane);
       __syncthreads();
       float y[1][4] = {};
-      mma_tf32x3<1, 2>(y, &M[r0 * kXs + r0], &M[c0 * kXs + r0 + n0], -1.f, lane);
+      mma_tf32x3<1, 2>(y, &M[r0 * kXs + r0], &M[c0 * kXs + r0 + n0], lane);
       __syncthreads();                                    // W has been read
-      store_c(&M[r0 * kXs + c0 + n0], y[0], lane);
+      store_c(&M[r0 * kXs + c0 + n0], y[0], lane, -1.f);
       const float zero[4] = {};
       store_c(&M[c0 * kXs + r0 + n0], zero, lane);        // above the diagonal of the pair
     }
@@ -264,14 +271,14 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     {
       const int m0 = 16 * (warp >> 1), n0 = 16 * (warp & 1);
       float w[2][4] = {};
-      mma_tf32x3<2, 4>(w, &M[(32 + m0) * kXs], &M[n0], 1.f, lane);
+      mma_tf32x3<2, 4>(w, &M[(32 + m0) * kXs], &M[n0], lane);
       store_c(&M[m0 * kXs + 32 + n0], w[0], lane);
       store_c(&M[m0 * kXs + 40 + n0], w[1], lane);
       __syncthreads();
       float y[2][4] = {};
-      mma_tf32x3<2, 4>(y, &M[(32 + m0) * kXs + 32], &M[32 + n0], -1.f, lane);
-      store_c(&M[(32 + m0) * kXs + n0], y[0], lane);      // C was read before W was complete
-      store_c(&M[(32 + m0) * kXs + n0 + 8], y[1], lane);
+      mma_tf32x3<2, 4>(y, &M[(32 + m0) * kXs + 32], &M[32 + n0], lane);
+      store_c(&M[(32 + m0) * kXs + n0], y[0], lane, -1.f); // C was read before W was complete
+      store_c(&M[(32 + m0) * kXs + n0 + 8], y[1], lane, -1.f);
     }
     if (tid == 127) bulk_wait_read();                     // A's image has left
     __syncthreads();
