@@ -25,318 +25,318 @@ namespace lte {
 namespace delta {
 
 // -------------------------------------------------------------- all chunks
-// One CTA of eight warps per (batch, key head, chunk): warp (m, half) has token
-// rows 16 m .. + 15 and one half of the columns of every product.  The value
-// heads that share the key head follow one another; dQ and dK stay in
-// registers over them and are rounded once.
-template <int DK, int DV>
+// Persistent CTAs of sixteen warps, one per SM, over (batch, key head, chunk): warp
+// (m, q) has token rows 16 m .. + 15 and a quarter of the columns of every product
+// (warp MMAs: the operands are small, all in shared memory, and each result's rows
+// are scaled, summed or masked before its next use).  The value channels come in
+// halves, two buffers deep: the next half, of the next head or chunk too, loads by
+// cp.async while this one is in use.  The value heads that share a key head follow
+// one another; dQ and dK stay in registers over them and are rounded once.
+// Bound by what it reads: 224 KB per chunk and head, 176 of them images.
+constexpr int kGradThreads = 512;
+constexpr int kHV = 64;                                    // value channels of a half
+
+template <int DK>
 struct GradSmem {
-  static constexpr int kK = 0, kQ = kK + L * DK * 2, kD = kQ + L * DK * 2, kU = kD + L * DV * 2;
-  static constexpr int kF = kU + 2 * DV * L * 2, kS = kF + DV * L * 2, kG = kS + 2 * DV * DK * 2;
-  static constexpr int kW = kG + DV * DK * 2, kZ = kW + 2 * kImg, kC = kZ + kImg;
-  static constexpr int kR = kC + kScal, kTotal = kR + 2 * L * 4;
+  static constexpr int kD = 0, kU = kD + L * kHV * 2, kF = kU + 2 * kHV * L * 2, kS = kF + kHV * L * 2;
+  static constexpr int kG = kS + 2 * kHV * DK * 2, kStage = kG + kHV * DK * 2;
+  static constexpr int kK = 2 * kStage, kQ = kK + L * DK * 2, kW = kQ + L * DK * 2, kZ = kW + 2 * kImg;
+  static constexpr int kR = kZ + kImg, kC = kR + 4 * L * 4;
+  // a head's scalars and its partial sums of u.y, v.dv and <dS_0, S_0> (up to 8 strips)
+  static constexpr int kX = kC + kScal, kI = kX + 8 * 2 * L * 4, kTotal = kI + 32;
 };
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(256, 1)
-delta_grad_kernel(const GradArgs ga) {
-  using SM = GradSmem<DK, DV>;
+// SHARED: several value heads to a key head, whose dQ and dK are kept in registers
+// beside the products of the next one
+template <int DK, int DV, bool SHARED>
+__global__ void __launch_bounds__(kGradThreads, 1)
+delta_grad_kernel(const GradArgs ga, int items) {
+  using SM = GradSmem<DK>;
   static_assert(SM::kTotal <= 227 * 1024, "shared memory");
   const ChunkArgs& a = ga.f;
   extern __shared__ __align__(128) uint8_t sm[];
-  constexpr int NP = DK / 32;                              // column pairs of 16 per warp in dQ, dK
-  const int c = blockIdx.x % a.chunks, bh = blockIdx.x / a.chunks, b = bh / a.Hk, hk = bh % a.Hk;
+  constexpr int NP = DK / 64, NH = DV / kHV;               // column pairs of 16 per warp in dQ, dK; halves
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int m = warp & 3, half = warp >> 2, rep = a.H / a.Hk;
-  const int len = seq_len(a.lens, b, a.T), t0 = c * L;
-  if (t0 >= len) return;
+  const int m = warp & 3, q = warp >> 2, rep = SHARED ? a.H / a.Hk : 1;
   const uint32_t s0 = smem_u32(sm);
   const int l7 = lane & 7, i0 = (lane >> 3) & 1, i1 = lane >> 4;
   // operands from 8 x 8 blocks: [k][n] as B (both 8-row halves of k, two n-tiles); [k][m] as A
   auto blk = [](uint32_t base, int rb, int cb, int cbs, int r) { return base + (uint32_t)((rb * cbs + cb) * 128 + r * 16); };
-  load_rows<DK, 256>(s0 + SM::kK, a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, t0, len);
-  load_rows<DK, 256>(s0 + SM::kQ, a.q + b * a.qs.b + hk * a.qs.h, a.qs.t, t0, len);
-  float dQ[2 * NP][4], dK[2 * NP][4];
-#pragma unroll
-  for (int n = 0; n < 2 * NP; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dQ[n][e] = dK[n][e] = 0.f;
-  const float* scal = reinterpret_cast<const float*>(sm + SM::kC);
+  auto len_of = [&](int it) { return seq_len(a.lens, it / a.chunks / a.Hk, a.T); };
+  auto next = [&](int it) {                                // the next chunk that has tokens
+    for (it += gridDim.x; it < items && (it % a.chunks) * L >= len_of(it); it += gridDim.x) {
+    }
+    return it;
+  };
+  auto load_half = [&](int it, int r, int hv, int buf) {
+    const int c = it % a.chunks, bh = it / a.chunks, b = bh / a.Hk, h = (bh % a.Hk) * rep + r;
+    const long long img = ((long long)b * a.H + h) * a.chunks + c;
+    const uint32_t d = s0 + buf * SM::kStage;
+    const uint8_t* us = reinterpret_cast<const uint8_t*>(a.u) + img * (2 * DV * L * 2) + hv * (kHV * L * 2);
+    const uint8_t* ss = reinterpret_cast<const uint8_t*>(a.s0) + img * (2 * DV * DK * 2) + hv * (kHV * DK * 2);
+    load_rows<kHV, kGradThreads>(d + SM::kD, ga.dO + b * ga.dos.b + h * ga.dos.h + hv * kHV, ga.dos.t, c * L, len_of(it));
+    load_linear<kHV * L * 2, kGradThreads>(d + SM::kU, us);
+    load_linear<kHV * L * 2, kGradThreads>(d + SM::kU + kHV * L * 2, us + DV * L * 2);
+    load_linear<kHV * L * 2, kGradThreads>(d + SM::kF, reinterpret_cast<const uint8_t*>(ga.fimg) + img * (DV * L * 2) + hv * (kHV * L * 2));
+    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kS, ss);
+    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kS + kHV * DK * 2, ss + DV * DK * 2);
+    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kG, reinterpret_cast<const uint8_t*>(ga.ds) + img * (DV * DK * 2) + hv * (kHV * DK * 2));
+  };
   float* qdq = reinterpret_cast<float*>(sm + SM::kR);
   const int ta = 16 * m + g, tb = ta + 8;                  // this thread's token rows
-  for (int r = 0; r < rep; ++r) {
-    const int h = hk * rep + r;
-    const long long img = ((long long)b * a.H + h) * a.chunks + c;
-    if (r > 0) __syncthreads();                            // the head before has been read
-    load_rows<DV, 256>(s0 + SM::kD, ga.dO + b * ga.dos.b + h * ga.dos.h, ga.dos.t, t0, len);
-    load_linear<2 * DV * L * 2, 256>(s0 + SM::kU, reinterpret_cast<const uint8_t*>(a.u) + img * (2 * DV * L * 2));
-    load_linear<DV * L * 2, 256>(s0 + SM::kF, reinterpret_cast<const uint8_t*>(ga.fimg) + img * (DV * L * 2));
-    load_linear<kScal, 256>(s0 + SM::kC, a.rec + img * rec_bytes(true) + 4 * kImg);
-    cp_async_commit();
-    load_linear<2 * DV * DK * 2, 256>(s0 + SM::kS, reinterpret_cast<const uint8_t*>(a.s0) + img * (2 * DV * DK * 2));
-    load_linear<DV * DK * 2, 256>(s0 + SM::kG, reinterpret_cast<const uint8_t*>(ga.ds) + img * (DV * DK * 2));
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    // ---- dO U^T (U as hi + lo) and F U^T, columns 32 half .. + 31, on and below the diagonal
-    {
-      float X[4][4], Y[4][4];
+  int it = next((int)blockIdx.x - (int)gridDim.x), buf = 0;
+  if (it < items) load_half(it, 0, 0, 0);
+  cp_async_commit();
+  while (it < items) {
+    const int c = it % a.chunks, bh = it / a.chunks, b = bh / a.Hk, hk = bh % a.Hk, t0 = c * L;
+    const int len = len_of(it), it1 = next(it);
+    float dQ[2 * NP][4], dK[2 * NP][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) X[n][e] = Y[n][e] = 0.f;
-      if (2 * half <= m) {
+      for (int e = 0; e < 4; ++e) dQ[n][e] = dK[n][e] = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < rep; ++r) {
+      const int h = hk * rep + r;
+      const long long img = ((long long)b * a.H + h) * a.chunks + c;
+      float X[2][4], Y[2][4], QI[2 * NP][4], US[2 * NP][4], FS[2 * NP][4];
 #pragma unroll
-        for (int ks = 0; ks < DV / 16; ++ks) {
-          uint32_t ad[4], af[4];
-          ldsm_x4(s0 + SM::kD + swz<DV>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane)), ad[0], ad[1], ad[2], ad[3]);
-          ldsm_x4_t(blk(s0 + SM::kF, 2 * ks + i1, 2 * m + i0, L / 8, l7), af[0], af[1], af[2], af[3]);
+      for (int e = 0; e < 4; ++e) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int np = 2 * half + p;
-            if (np <= m) {
-              uint32_t x[4];
-              ldsm_x4_t(blk(s0 + SM::kU, 2 * ks + i0, 2 * np + i1, L / 8, l7), x[0], x[1], x[2], x[3]);
-              mma_bf16(X[2 * p], ad, x[0], x[1]);
-              mma_bf16(X[2 * p + 1], ad, x[2], x[3]);
-              mma_bf16(Y[2 * p], af, x[0], x[1]);
-              mma_bf16(Y[2 * p + 1], af, x[2], x[3]);
-              ldsm_x4_t(blk(s0 + SM::kU + DV * L * 2, 2 * ks + i0, 2 * np + i1, L / 8, l7), x[0], x[1], x[2], x[3]);
-              mma_bf16(X[2 * p], ad, x[0], x[1]);
-              mma_bf16(X[2 * p + 1], ad, x[2], x[3]);
-            }
+        for (int n = 0; n < 2; ++n) X[n][e] = Y[n][e] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2 * NP; ++n) QI[n][e] = US[n][e] = FS[n][e] = 0.f;
+      }
+#pragma unroll 1
+      for (int hv = 0; hv < NH; ++hv) {
+        cp_async_wait<0>();
+        __syncthreads();                                   // this half has landed; the one before has been read
+        if (r == 0 && hv == 0) {                           // (and so have the chunk before's K and Q)
+          load_rows<DK, kGradThreads>(s0 + SM::kK, a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, t0, len);
+          load_rows<DK, kGradThreads>(s0 + SM::kQ, a.q + b * a.qs.b + hk * a.qs.h, a.qs.t, t0, len);
+        }
+        if (hv == 0) {                                     // the head's small things, used behind its last half
+          load_linear<kScal, kGradThreads>(s0 + SM::kC, a.rec + img * rec_bytes(true) + 4 * kImg);
+          load_linear<(DV / 16) * 2 * L * 4, kGradThreads>(s0 + SM::kX, reinterpret_cast<const uint8_t*>(ga.x) + img * ((DV / 16) * 2 * L * 4));
+          load_linear<(DV / 16) * 4, kGradThreads>(s0 + SM::kI, reinterpret_cast<const uint8_t*>(ga.inner) + img * ((DV / 16) * 4));
+          if (NH == 1) cp_async_commit();
+        }
+        if (hv + 1 < NH) load_half(it, r, hv + 1, buf ^ 1);
+        else if (r + 1 < rep) load_half(it, r + 1, 0, buf ^ 1);
+        else if (it1 < items) load_half(it1, 0, 0, buf ^ 1);
+        cp_async_commit();
+        const uint32_t d = s0 + buf * SM::kStage;
+#pragma unroll
+        for (int ks = 0; ks < kHV / 16; ++ks) {
+          uint32_t ad[4], af[4], au[4];
+          ldsm_x4(d + SM::kD + swz<kHV>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane)), ad[0], ad[1], ad[2], ad[3]);
+          ldsm_x4_t(blk(d + SM::kF, 2 * ks + i1, 2 * m + i0, L / 8, l7), af[0], af[1], af[2], af[3]);
+          ldsm_x4_t(blk(d + SM::kU, 2 * ks + i1, 2 * m + i0, L / 8, l7), au[0], au[1], au[2], au[3]);
+          if (q <= m) {                                    // dO U^T (U as hi + lo), F U^T: columns 16 q .. + 15
+            uint32_t x[4];
+            ldsm_x4_t(blk(d + SM::kU, 2 * ks + i0, 2 * q + i1, L / 8, l7), x[0], x[1], x[2], x[3]);
+            mma_bf16(X[0], ad, x[0], x[1]);
+            mma_bf16(X[1], ad, x[2], x[3]);
+            mma_bf16(Y[0], af, x[0], x[1]);
+            mma_bf16(Y[1], af, x[2], x[3]);
+            ldsm_x4_t(blk(d + SM::kU + kHV * L * 2, 2 * ks + i0, 2 * q + i1, L / 8, l7), x[0], x[1], x[2], x[3]);
+            mma_bf16(X[0], ad, x[0], x[1]);
+            mma_bf16(X[1], ad, x[2], x[3]);
+          }
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {                   // dO S_0 (hi + lo), F S_0, U dS
+            uint32_t x[4];
+            const int cb = 2 * (q * NP + p) + i1;
+            ldsm_x4_t(blk(d + SM::kS, 2 * ks + i0, cb, DK / 8, l7), x[0], x[1], x[2], x[3]);
+            mma_bf16(QI[2 * p], ad, x[0], x[1]);
+            mma_bf16(QI[2 * p + 1], ad, x[2], x[3]);
+            mma_bf16(FS[2 * p], af, x[0], x[1]);
+            mma_bf16(FS[2 * p + 1], af, x[2], x[3]);
+            ldsm_x4_t(blk(d + SM::kS + kHV * DK * 2, 2 * ks + i0, cb, DK / 8, l7), x[0], x[1], x[2], x[3]);
+            mma_bf16(QI[2 * p], ad, x[0], x[1]);
+            mma_bf16(QI[2 * p + 1], ad, x[2], x[3]);
+            ldsm_x4_t(blk(d + SM::kG, 2 * ks + i0, cb, DK / 8, l7), x[0], x[1], x[2], x[3]);
+            mma_bf16(US[2 * p], au, x[0], x[1]);
+            mma_bf16(US[2 * p + 1], au, x[2], x[3]);
           }
         }
+        buf ^= 1;
+      }
+      const float* scal = reinterpret_cast<const float*>(sm + SM::kC);
+      if (NH == 1) {                                       // K, Q and the small things (else: waited for with the second half)
+        cp_async_wait<1>();
+        __syncthreads();
+      }
+      // ---- W and Z from dO U^T and F U^T
+      if (q <= m) {
+        const float ha = scal[kGhi * L + ta], oa = scal[kGlo * L + ta], hb = scal[kGhi * L + tb], ob = scal[kGlo * L + tb];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int s = 32 * half + 8 * n + t2;
+        for (int n = 0; n < 2; ++n) {
+          const int s = 16 * q + 8 * n + t2;
+          const float2 hs = *reinterpret_cast<const float2*>(scal + kGhi * L + s);
+          const float2 os = *reinterpret_cast<const float2*>(scal + kGlo * L + s);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int t = i ? tb : ta;
-            float w[2], z[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float d = s + e <= t ? expf((scal[kGhi * L + t] - scal[kGhi * L + s + e]) +
-                                                (scal[kGlo * L + t] - scal[kGlo * L + s + e]))
-                                         : 0.f;
-              w[e] = s + e <= t ? a.scale * d * X[n][2 * i + e] : 0.f;
-              z[e] = s + e < t ? -d * Y[n][2 * i + e] : 0.f;
-            }
+            const float gh = i ? hb : ha, go = i ? ob : oa;
+            const float d0 = s <= t ? expf((gh - hs.x) + (go - os.x)) : 0.f;
+            const float d1 = s + 1 <= t ? expf((gh - hs.y) + (go - os.y)) : 0.f;
             uint32_t hi, lo;
-            split2(w[0], w[1], hi, lo);
+            split2(a.scale * d0 * X[n][2 * i], a.scale * d1 * X[n][2 * i + 1], hi, lo);
             const uint32_t off = swz<64>(t, s >> 3) + t2 * 2;
             *reinterpret_cast<uint32_t*>(sm + SM::kW + off) = hi;
             *reinterpret_cast<uint32_t*>(sm + SM::kW + kImg + off) = lo;
-            *reinterpret_cast<uint32_t*>(sm + SM::kZ + off) = pack_bf16(z[0], z[1]);
+            *reinterpret_cast<uint32_t*>(sm + SM::kZ + off) =
+                pack_bf16(s < t ? -d0 * Y[n][2 * i] : 0.f, s + 1 < t ? -d1 * Y[n][2 * i + 1] : 0.f);
+          }
+        }
+      }
+      __syncthreads();
+      // ---- dQ of this head: scale e^G dO S_0 + W K, and q.dq per token
+      const float ea = scal[kEG * L + ta], eb = scal[kEG * L + tb], la = scal[kLam * L + ta], lb = scal[kLam * L + tb];
+#pragma unroll
+      for (int n = 0; n < 2 * NP; ++n) {
+        QI[n][0] *= a.scale * ea; QI[n][1] *= a.scale * ea;
+        QI[n][2] *= a.scale * eb; QI[n][3] *= a.scale * eb;
+        dK[n][0] += la * US[n][0] - ea * FS[n][0]; dK[n][1] += la * US[n][1] - ea * FS[n][1];
+        dK[n][2] += lb * US[n][2] - eb * FS[n][2]; dK[n][3] += lb * US[n][3] - eb * FS[n][3];
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t wh[4], wl[4], z[4], w[4], y[4];
+        if (ks <= m) {
+          const uint32_t off = swz<64>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane));
+          ldsm_x4(s0 + SM::kW + off, wh[0], wh[1], wh[2], wh[3]);
+          ldsm_x4(s0 + SM::kW + kImg + off, wl[0], wl[1], wl[2], wl[3]);
+          ldsm_x4(s0 + SM::kZ + off, z[0], z[1], z[2], z[3]);
+        }
+        if (ks >= m) {
+          const uint32_t off = swz<64>(16 * ks + ldn_row(lane), 2 * m + ldn_col(lane));
+          ldsm_x4_t(s0 + SM::kW + off, w[0], w[1], w[2], w[3]);
+          ldsm_x4_t(s0 + SM::kZ + off, y[0], y[1], y[2], y[3]);
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          uint32_t x[4];
+          const uint32_t off = swz<DK>(16 * ks + ldt_row(lane), 2 * (q * NP + p) + ldt_col(lane));
+          ldsm_x4_t(s0 + SM::kK + off, x[0], x[1], x[2], x[3]);
+          if (ks <= m) {                                   // W K; Z K
+            mma_bf16(QI[2 * p], wh, x[0], x[1]);
+            mma_bf16(QI[2 * p + 1], wh, x[2], x[3]);
+            mma_bf16(QI[2 * p], wl, x[0], x[1]);
+            mma_bf16(QI[2 * p + 1], wl, x[2], x[3]);
+            mma_bf16(dK[2 * p], z, x[0], x[1]);
+            mma_bf16(dK[2 * p + 1], z, x[2], x[3]);
+          }
+          if (ks >= m) {                                   // Z^T K; W^T Q
+            mma_bf16(dK[2 * p], y, x[0], x[1]);
+            mma_bf16(dK[2 * p + 1], y, x[2], x[3]);
+            ldsm_x4_t(s0 + SM::kQ + off, x[0], x[1], x[2], x[3]);
+            mma_bf16(dK[2 * p], w, x[0], x[1]);
+            mma_bf16(dK[2 * p + 1], w, x[2], x[3]);
+          }
+        }
+      }
+      {
+        float da = 0.f, dbb = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2 * NP; ++n) {
+          const int cc = q * 2 * NP + n;
+          const uint32_t qa = *reinterpret_cast<const uint32_t*>(sm + SM::kQ + swz<DK>(ta, cc) + t2 * 2);
+          const uint32_t qb = *reinterpret_cast<const uint32_t*>(sm + SM::kQ + swz<DK>(tb, cc) + t2 * 2);
+          da = fmaf(QI[n][0], bf_lo(qa), fmaf(QI[n][1], bf_hi(qa), da));
+          dbb = fmaf(QI[n][2], bf_lo(qb), fmaf(QI[n][3], bf_hi(qb), dbb));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dQ[n][e] += QI[n][e];
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          da += __shfl_xor_sync(0xffffffffu, da, o);
+          dbb += __shfl_xor_sync(0xffffffffu, dbb, o);
+        }
+        if ((lane & 3) == 0) {
+          qdq[q * L + ta] = da;
+          qdq[q * L + tb] = dbb;
+        }
+      }
+      __syncthreads();                                     // q.dq of all quarters; W and Z have been read
+      // ---- gates: db_t = u.y / b, dg_t = <dS_0, S_0> - sum_{t' < t} (q.dq - v.dv)
+      if (warp == 15) {                                    // (the warps with q > m have less to do before)
+        constexpr int strips = DV / 16;
+        const float* xp = reinterpret_cast<const float*>(sm + SM::kX) + 2 * lane;
+        const float* inner = reinterpret_cast<const float*>(sm + SM::kI);
+        double in = 0.0;
+        float x[2] = {0.f, 0.f}, vf[2] = {0.f, 0.f}, qd[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < strips; ++i) {
+          in += (double)inner[i];
+          const float2 p = *reinterpret_cast<const float2*>(xp + i * 2 * L);
+          const float2 w = *reinterpret_cast<const float2*>(xp + i * 2 * L + L);
+          x[0] += p.x;
+          x[1] += p.y;
+          vf[0] += w.x;
+          vf[1] += w.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qd[0] += qdq[i * L + 2 * lane];
+          qd[1] += qdq[i * L + 2 * lane + 1];
+        }
+        const double y0 = (double)qd[0] - vf[0], y1 = (double)qd[1] - vf[1];
+        double sum = y0 + y1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const double first = in - (sum - y1 - y0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = t0 + 2 * lane + i;
+          if (t < len) {
+            const long long gi = ((long long)b * a.T + t) * a.H + h;
+            ga.dg[gi] = (float)(i ? first - y0 : first);
+            ga.db[gi] = x[i] / scal[kBeta * L + 2 * lane + i];
           }
         }
       }
     }
-    cp_async_wait<0>();
+    // ---- dQ, dK as bf16 token rows, through the K and Q tiles (all warps are past them)
+#pragma unroll
+    for (int n = 0; n < 2 * NP; ++n) {
+      const int cc = q * 2 * NP + n;
+      *reinterpret_cast<uint32_t*>(sm + SM::kQ + swz<DK>(ta, cc) + t2 * 2) = pack_bf16(dQ[n][0], dQ[n][1]);
+      *reinterpret_cast<uint32_t*>(sm + SM::kQ + swz<DK>(tb, cc) + t2 * 2) = pack_bf16(dQ[n][2], dQ[n][3]);
+      *reinterpret_cast<uint32_t*>(sm + SM::kK + swz<DK>(ta, cc) + t2 * 2) = pack_bf16(dK[n][0], dK[n][1]);
+      *reinterpret_cast<uint32_t*>(sm + SM::kK + swz<DK>(tb, cc) + t2 * 2) = pack_bf16(dK[n][2], dK[n][3]);
+    }
     __syncthreads();
-    const float ea = scal[kEG * L + ta], eb = scal[kEG * L + tb];
-    float acc[2 * NP][4];
-    // ---- dQ of this head: scale e^G dO S_0 + W K, and q.dq per token
-#pragma unroll
-    for (int n = 0; n < 2 * NP; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < DV / 16; ++ks) {
-      uint32_t ad[4];
-      ldsm_x4(s0 + SM::kD + swz<DV>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane)), ad[0], ad[1], ad[2], ad[3]);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        uint32_t x[4];
-        const int cb = 2 * (half * NP + p) + i1;
-        ldsm_x4_t(blk(s0 + SM::kS, 2 * ks + i0, cb, DK / 8, l7), x[0], x[1], x[2], x[3]);
-        mma_bf16(acc[2 * p], ad, x[0], x[1]);
-        mma_bf16(acc[2 * p + 1], ad, x[2], x[3]);
-        ldsm_x4_t(blk(s0 + SM::kS + DV * DK * 2, 2 * ks + i0, cb, DK / 8, l7), x[0], x[1], x[2], x[3]);
-        mma_bf16(acc[2 * p], ad, x[0], x[1]);
-        mma_bf16(acc[2 * p + 1], ad, x[2], x[3]);
+    for (int i = tid; i < L * (DK / 8); i += kGradThreads) {
+      const int t = i / (DK / 8), cc = i % (DK / 8);
+      if (t0 + t < len) {
+        const long long o = (((long long)b * a.T + t0 + t) * a.Hk + hk) * DK + cc * 8;
+        *reinterpret_cast<uint4*>(ga.dq + o) = *reinterpret_cast<const uint4*>(sm + SM::kQ + swz<DK>(t, cc));
+        *reinterpret_cast<uint4*>(ga.dk + o) = *reinterpret_cast<const uint4*>(sm + SM::kK + swz<DK>(t, cc));
       }
     }
-#pragma unroll
-    for (int n = 0; n < 2 * NP; ++n) {
-      acc[n][0] *= a.scale * ea; acc[n][1] *= a.scale * ea;
-      acc[n][2] *= a.scale * eb; acc[n][3] *= a.scale * eb;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks <= m) {
-        uint32_t wh[4], wl[4];
-        const uint32_t off = swz<64>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane));
-        ldsm_x4(s0 + SM::kW + off, wh[0], wh[1], wh[2], wh[3]);
-        ldsm_x4(s0 + SM::kW + kImg + off, wl[0], wl[1], wl[2], wl[3]);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          uint32_t x[4];
-          ldsm_x4_t(s0 + SM::kK + swz<DK>(16 * ks + ldt_row(lane), 2 * (half * NP + p) + ldt_col(lane)), x[0], x[1],
-                    x[2], x[3]);
-          mma_bf16(acc[2 * p], wh, x[0], x[1]);
-          mma_bf16(acc[2 * p + 1], wh, x[2], x[3]);
-          mma_bf16(acc[2 * p], wl, x[0], x[1]);
-          mma_bf16(acc[2 * p + 1], wl, x[2], x[3]);
-        }
-      }
-    }
-    {
-      float da = 0.f, dbb = 0.f;
-#pragma unroll
-      for (int n = 0; n < 2 * NP; ++n) {
-        const int cc = half * 2 * NP + n;
-        const uint32_t qa = *reinterpret_cast<const uint32_t*>(sm + SM::kQ + swz<DK>(ta, cc) + t2 * 2);
-        const uint32_t qb = *reinterpret_cast<const uint32_t*>(sm + SM::kQ + swz<DK>(tb, cc) + t2 * 2);
-        da = fmaf(acc[n][0], bf_lo(qa), fmaf(acc[n][1], bf_hi(qa), da));
-        dbb = fmaf(acc[n][2], bf_lo(qb), fmaf(acc[n][3], bf_hi(qb), dbb));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dQ[n][e] += acc[n][e];
-      }
-#pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        da += __shfl_xor_sync(0xffffffffu, da, o);
-        dbb += __shfl_xor_sync(0xffffffffu, dbb, o);
-      }
-      if ((lane & 3) == 0) {
-        qdq[half * L + ta] = da;
-        qdq[half * L + tb] = dbb;
-      }
-    }
-    // ---- dK of this head; rows are the tokens s
-    const float la = scal[kLam * L + ta], lb = scal[kLam * L + tb];
-#pragma unroll
-    for (int n = 0; n < 2 * NP; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < DV / 16; ++ks) {                 // U dS
-      uint32_t au[4];
-      ldsm_x4_t(blk(s0 + SM::kU, 2 * ks + i1, 2 * m + i0, L / 8, l7), au[0], au[1], au[2], au[3]);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        uint32_t x[4];
-        ldsm_x4_t(blk(s0 + SM::kG, 2 * ks + i0, 2 * (half * NP + p) + i1, DK / 8, l7), x[0], x[1], x[2], x[3]);
-        mma_bf16(acc[2 * p], au, x[0], x[1]);
-        mma_bf16(acc[2 * p + 1], au, x[2], x[3]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < 2 * NP; ++n) {
-      dK[n][0] = fmaf(la, acc[n][0], dK[n][0]); dK[n][1] = fmaf(la, acc[n][1], dK[n][1]);
-      dK[n][2] = fmaf(lb, acc[n][2], dK[n][2]); dK[n][3] = fmaf(lb, acc[n][3], dK[n][3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-    }
-#pragma unroll
-    for (int ks = 0; ks < DV / 16; ++ks) {                 // F S_0
-      uint32_t af[4];
-      ldsm_x4_t(blk(s0 + SM::kF, 2 * ks + i1, 2 * m + i0, L / 8, l7), af[0], af[1], af[2], af[3]);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        uint32_t x[4];
-        ldsm_x4_t(blk(s0 + SM::kS, 2 * ks + i0, 2 * (half * NP + p) + i1, DK / 8, l7), x[0], x[1], x[2], x[3]);
-        mma_bf16(acc[2 * p], af, x[0], x[1]);
-        mma_bf16(acc[2 * p + 1], af, x[2], x[3]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < 2 * NP; ++n) {
-      dK[n][0] = fmaf(-ea, acc[n][0], dK[n][0]); dK[n][1] = fmaf(-ea, acc[n][1], dK[n][1]);
-      dK[n][2] = fmaf(-eb, acc[n][2], dK[n][2]); dK[n][3] = fmaf(-eb, acc[n][3], dK[n][3]);
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t z[4], w[4], y[4];
-      if (ks <= m) ldsm_x4(s0 + SM::kZ + swz<64>(16 * m + ldt_row(lane), 2 * ks + ldt_col(lane)), z[0], z[1], z[2], z[3]);
-      if (ks >= m) {
-        const uint32_t off = swz<64>(16 * ks + ldn_row(lane), 2 * m + ldn_col(lane));
-        ldsm_x4_t(s0 + SM::kW + off, w[0], w[1], w[2], w[3]);
-        ldsm_x4_t(s0 + SM::kZ + off, y[0], y[1], y[2], y[3]);
-      }
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        uint32_t x[4];
-        const uint32_t off = swz<DK>(16 * ks + ldt_row(lane), 2 * (half * NP + p) + ldt_col(lane));
-        ldsm_x4_t(s0 + SM::kK + off, x[0], x[1], x[2], x[3]);
-        if (ks <= m) {                                     // Z K
-          mma_bf16(dK[2 * p], z, x[0], x[1]);
-          mma_bf16(dK[2 * p + 1], z, x[2], x[3]);
-        }
-        if (ks >= m) {                                     // Z^T K + W^T Q
-          mma_bf16(dK[2 * p], y, x[0], x[1]);
-          mma_bf16(dK[2 * p + 1], y, x[2], x[3]);
-          ldsm_x4_t(s0 + SM::kQ + off, x[0], x[1], x[2], x[3]);
-          mma_bf16(dK[2 * p], w, x[0], x[1]);
-          mma_bf16(dK[2 * p + 1], w, x[2], x[3]);
-        }
-      }
-    }
-    __syncthreads();                                       // q.dq of both halves
-    // ---- gates: db_t = u.y / b, dg_t = <dS_0, S_0> - sum_{t' < t} (q.dq - v.dv)
-    if (warp == 0) {
-      constexpr int strips = DV / 16;
-      const float* xp = ga.x + img * strips * (2 * L) + 2 * lane;
-      double in = 0.0;
-      float x[2] = {0.f, 0.f}, vf[2] = {0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < strips; ++i) {
-        in += (double)ga.inner[img * strips + i];
-        const float2 p = *reinterpret_cast<const float2*>(xp + i * 2 * L);
-        const float2 q = *reinterpret_cast<const float2*>(xp + i * 2 * L + L);
-        x[0] += p.x;
-        x[1] += p.y;
-        vf[0] += q.x;
-        vf[1] += q.y;
-      }
-      const double y0 = (double)(qdq[2 * lane] + qdq[L + 2 * lane]) - vf[0];
-      const double y1 = (double)(qdq[2 * lane + 1] + qdq[L + 2 * lane + 1]) - vf[1];
-      double sum = y0 + y1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      const double first = in - (sum - y1 - y0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t0 + 2 * lane + i;
-        if (t < len) {
-          const long long gi = ((long long)b * a.T + t) * a.H + h;
-          ga.dg[gi] = (float)(i ? first - y0 : first);
-          ga.db[gi] = x[i] / scal[kBeta * L + 2 * lane + i];
-        }
-      }
-    }
+    it = it1;
   }
-  // ---- dQ, dK as bf16 token rows, through the K and Q tiles
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < 2 * NP; ++n) {
-    const int cc = half * 2 * NP + n;
-    *reinterpret_cast<uint32_t*>(sm + SM::kQ + swz<DK>(ta, cc) + t2 * 2) = pack_bf16(dQ[n][0], dQ[n][1]);
-    *reinterpret_cast<uint32_t*>(sm + SM::kQ + swz<DK>(tb, cc) + t2 * 2) = pack_bf16(dQ[n][2], dQ[n][3]);
-    *reinterpret_cast<uint32_t*>(sm + SM::kK + swz<DK>(ta, cc) + t2 * 2) = pack_bf16(dK[n][0], dK[n][1]);
-    *reinterpret_cast<uint32_t*>(sm + SM::kK + swz<DK>(tb, cc) + t2 * 2) = pack_bf16(dK[n][2], dK[n][3]);
-  }
-  __syncthreads();
-  for (int i = tid; i < L * (DK / 8); i += 256) {
-    const int t = i / (DK / 8), cc = i % (DK / 8);
-    if (t0 + t < len) {
-      const long long o = (((long long)b * a.T + t0 + t) * a.Hk + hk) * DK + cc * 8;
-      *reinterpret_cast<uint4*>(ga.dq + o) = *reinterpret_cast<const uint4*>(sm + SM::kQ + swz<DK>(t, cc));
-      *reinterpret_cast<uint4*>(ga.dk + o) = *reinterpret_cast<const uint4*>(sm + SM::kK + swz<DK>(t, cc));
-    }
-  }
+  cp_async_wait<0>();
+}
+
+template <int DK, int DV, bool SHARED>
+cudaError_t grad_as(const GradArgs& a, int B, cudaStream_t stream) {
+  constexpr int smem = GradSmem<DK>::kTotal;
+  cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<DK, DV, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int items = B * a.f.Hk * a.f.chunks;
+  delta_grad_kernel<DK, DV, SHARED><<<items < 148 ? items : 148, kGradThreads, smem, stream>>>(a, items);
+  return cudaGetLastError();
 }
 
 template <int DK, int DV>
 cudaError_t grad(const GradArgs& a, int B, cudaStream_t stream) {
-  constexpr int smem = GradSmem<DK, DV>::kTotal;
-  cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  delta_grad_kernel<DK, DV><<<(unsigned)(B * a.f.Hk) * a.f.chunks, 256, smem, stream>>>(a);
-  return cudaGetLastError();
+  return a.f.H == a.f.Hk ? grad_as<DK, DV, false>(a, B, stream) : grad_as<DK, DV, true>(a, B, stream);
 }
 
 // workspace: records, then the images and partial sums, each rounded up to 256 bytes
