@@ -19,7 +19,7 @@
 // with dS, F and dV (delta_back_tc.cu), then all chunks at once for dQ, dK, dg and
 // db (here).  The sums over value channels and over the heads that
 // share a key run in a fixed order: no atomics.
-#include "delta_chunk.cuh"
+#include "delta_chain_tc.cuh"
 
 namespace lte {
 namespace delta {
@@ -29,8 +29,8 @@ namespace delta {
 // (m, q) has token rows 16 m .. + 15 and a quarter of the columns of every product
 // (warp MMAs: the operands are small, all in shared memory, and each result's rows
 // are scaled, summed or masked before its next use).  The value channels come in
-// halves, two buffers deep: the next half, of the next head or chunk too, loads by
-// cp.async while this one is in use.  The value heads that share a key head follow
+// halves, two buffers deep: the next half, of the next head or chunk too, loads
+// while this one is in use (images by bulk copies, token rows by cp.async).  The value heads that share a key head follow
 // one another; dQ and dK stay in registers over them and are rounded once.
 // Bound by what it reads: 224 KB per chunk and head, 176 of them images.
 constexpr int kGradThreads = 512;
@@ -43,7 +43,7 @@ struct GradSmem {
   static constexpr int kK = 2 * kStage, kQ = kK + L * DK * 2, kW = kQ + L * DK * 2, kZ = kW + 2 * kImg;
   static constexpr int kR = kZ + kImg, kC = kR + 4 * L * 4;
   // a head's scalars and its partial sums of u.y, v.dv and <dS_0, S_0> (up to 8 strips)
-  static constexpr int kX = kC + kScal, kI = kX + 8 * 2 * L * 4, kTotal = kI + 32;
+  static constexpr int kX = kC + kScal, kI = kX + 8 * 2 * L * 4, kBar = kI + 32, kTotal = kBar + 32;
 };
 
 // SHARED: several value heads to a key head, whose dQ and dK are kept in registers
@@ -57,7 +57,8 @@ delta_grad_kernel(const GradArgs ga, int items) {
   extern __shared__ __align__(128) uint8_t sm[];
   constexpr int NP = DK / 64, NH = DV / kHV;               // column pairs of 16 per warp in dQ, dK; halves
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-  const int m = warp & 3, q = warp >> 2, rep = SHARED ? a.H / a.Hk : 1;
+  // (m differs among the warps of a scheduler: work on and below the diagonal grows with it)
+  const int q = warp >> 2, m = (warp + q) & 3, rep = SHARED ? a.H / a.Hk : 1;
   const uint32_t s0 = smem_u32(sm);
   const int l7 = lane & 7, i0 = (lane >> 3) & 1, i1 = lane >> 4;
   // operands from 8 x 8 blocks: [k][n] as B (both 8-row halves of k, two n-tiles); [k][m] as A
@@ -72,19 +73,32 @@ delta_grad_kernel(const GradArgs ga, int items) {
     const int c = it % a.chunks, bh = it / a.chunks, b = bh / a.Hk, h = (bh % a.Hk) * rep + r;
     const long long img = ((long long)b * a.H + h) * a.chunks + c;
     const uint32_t d = s0 + buf * SM::kStage;
+    load_rows<kHV, kGradThreads>(d + SM::kD, ga.dO + b * ga.dos.b + h * ga.dos.h + hv * kHV, ga.dos.t, c * L, len_of(it));
+    if (tid != 0) return;
+    const uint32_t bar = s0 + SM::kBar + 8 * buf;
+    chaintc::mbar_expect_tx(bar, SM::kStage - SM::kU);
     const uint8_t* us = reinterpret_cast<const uint8_t*>(a.u) + img * (2 * DV * L * 2) + hv * (kHV * L * 2);
     const uint8_t* ss = reinterpret_cast<const uint8_t*>(a.s0) + img * (2 * DV * DK * 2) + hv * (kHV * DK * 2);
-    load_rows<kHV, kGradThreads>(d + SM::kD, ga.dO + b * ga.dos.b + h * ga.dos.h + hv * kHV, ga.dos.t, c * L, len_of(it));
-    load_linear<kHV * L * 2, kGradThreads>(d + SM::kU, us);
-    load_linear<kHV * L * 2, kGradThreads>(d + SM::kU + kHV * L * 2, us + DV * L * 2);
-    load_linear<kHV * L * 2, kGradThreads>(d + SM::kF, reinterpret_cast<const uint8_t*>(ga.fimg) + img * (DV * L * 2) + hv * (kHV * L * 2));
-    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kS, ss);
-    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kS + kHV * DK * 2, ss + DV * DK * 2);
-    load_linear<kHV * DK * 2, kGradThreads>(d + SM::kG, reinterpret_cast<const uint8_t*>(ga.ds) + img * (DV * DK * 2) + hv * (kHV * DK * 2));
+    chaintc::bulk_load(d + SM::kU, us, kHV * L * 2, bar);
+    chaintc::bulk_load(d + SM::kU + kHV * L * 2, us + DV * L * 2, kHV * L * 2, bar);
+    chaintc::bulk_load(d + SM::kF, reinterpret_cast<const uint8_t*>(ga.fimg) + img * (DV * L * 2) + hv * (kHV * L * 2), kHV * L * 2, bar);
+    chaintc::bulk_load(d + SM::kS, ss, kHV * DK * 2, bar);
+    chaintc::bulk_load(d + SM::kS + kHV * DK * 2, ss + DV * DK * 2, kHV * DK * 2, bar);
+    chaintc::bulk_load(d + SM::kG, reinterpret_cast<const uint8_t*>(ga.ds) + img * (DV * DK * 2) + hv * (kHV * DK * 2), kHV * DK * 2, bar);
   };
   float* qdq = reinterpret_cast<float*>(sm + SM::kR);
   const int ta = 16 * m + g, tb = ta + 8;                  // this thread's token rows
-  int it = next((int)blockIdx.x - (int)gridDim.x), buf = 0;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::kBar + 16);
+  if (tid == 0) {
+    chaintc::mbar_init(s0 + SM::kBar, 1);
+    chaintc::mbar_init(s0 + SM::kBar + 8, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  uint32_t halves = 0;                                     // halves waited for; buffer = halves mod 2
+  bool ok = true;
+  int it = next((int)blockIdx.x - (int)gridDim.x);
   if (it < items) load_half(it, 0, 0, 0);
   cp_async_commit();
   while (it < items) {
@@ -109,8 +123,12 @@ delta_grad_kernel(const GradArgs ga, int items) {
       }
 #pragma unroll 1
       for (int hv = 0; hv < NH; ++hv) {
+        const int buf = halves & 1;
         cp_async_wait<0>();
-        __syncthreads();                                   // this half has landed; the one before has been read
+        ok = chaintc::mbar_wait(s0 + SM::kBar + 8 * buf, (halves >> 1) & 1, abort_flag, nullptr, 0);
+        ++halves;
+        // this half has landed; the one before has been read
+        if (!(ok = __syncthreads_and(ok))) break;
         if (r == 0 && hv == 0) {                           // (and so have the chunk before's K and Q)
           load_rows<DK, kGradThreads>(s0 + SM::kK, a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, t0, len);
           load_rows<DK, kGradThreads>(s0 + SM::kQ, a.q + b * a.qs.b + hk * a.qs.h, a.qs.t, t0, len);
@@ -160,8 +178,8 @@ delta_grad_kernel(const GradArgs ga, int items) {
             mma_bf16(US[2 * p + 1], au, x[2], x[3]);
           }
         }
-        buf ^= 1;
       }
+      if (!ok) break;
       const float* scal = reinterpret_cast<const float*>(sm + SM::kC);
       if (NH == 1) {                                       // K, Q and the small things (else: waited for with the second half)
         cp_async_wait<1>();
@@ -301,6 +319,7 @@ delta_grad_kernel(const GradArgs ga, int items) {
         }
       }
     }
+    if (!ok) break;
     // ---- dQ, dK as bf16 token rows, through the K and Q tiles (all warps are past them)
 #pragma unroll
     for (int n = 0; n < 2 * NP; ++n) {
@@ -322,6 +341,14 @@ delta_grad_kernel(const GradArgs ga, int items) {
     it = it1;
   }
   cp_async_wait<0>();
+  if (!ok && it < items) {                                 // a copy did not land: visible in the gates' gradients
+    if (tid == 0) {
+      const int b = it / a.chunks / a.Hk;
+      ga.dg[((long long)b * a.T + (it % a.chunks) * L) * a.H + (it / a.chunks % a.Hk) * rep] = __int_as_float(0x7fc00000);
+      chaintc::mbar_drain(s0 + SM::kBar + 8 * ((halves - 1) & 1), ((halves - 1) >> 1) & 1);
+    }
+    __syncthreads();
+  }
 }
 
 template <int DK, int DV, bool SHARED>
