@@ -185,8 +185,11 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks)
-            mma_f16_ts(tmem + kColO, tmem + kColSh + 8 * ks, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4), id_tok, ks > 0);
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks)
+              mma_f16_ts(tmem + kColO, tmem + (p ? kColSl : kColSh) + 8 * ks, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                         id_tok, p + ks > 0);
           mma_commit(bar(bQS));
         }
       }
