@@ -318,6 +318,83 @@ def test_prefill_on_another_stream_and_in_graphs(layer):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_backward_in_a_graph(layer):
+    """A captured gradient pass, replayed with new inputs in its buffers."""
+    x, y = inputs(60, 2, 100, 4, 2, 128, 64), inputs(61, 2, 100, 4, 2, 128, 64)
+    names = ("q", "k", "v", "g", "beta")
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    want = layer.delta_backward(*(y[n] for n in names), do, state=y["state"])
+    layer.delta_backward(*(x[n] for n in names), do, state=x["state"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer.delta_backward(*(x[n] for n in names), do, state=x["state"])
+    for n in (*names, "state"):
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(layer):
+    """A sequence whose tensors have over 2^31 elements: its last tokens, and the state, equal those of
+    the same tokens in a call of their own behind the state of the others."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    T, tail, H, D = (1 << 20) + 320, 200, 16, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v = randn(1, T, H, D), randn(1, T, H, D), randn(1, T, H, D)
+    k /= k.norm(dim=-1, keepdim=True)
+    gate = -0.01 * torch.rand(1, T, H, generator=g, device="cuda")
+    beta = torch.rand(1, T, H, generator=g, device="cuda")
+    assert q.numel() > 1 << 31
+    o, S = layer.delta_prefill(q, k, v, gate, beta)
+    n = T - tail
+    _, S0 = layer.delta_prefill(q[:, :n], k[:, :n], v[:, :n], gate[:, :n], beta[:, :n])
+    o1, S1 = layer.delta_prefill(q[:, n:], k[:, n:], v[:, n:], gate[:, n:], beta[:, n:], state=S0)
+    assert torch.isfinite(S).all()
+    # the chunks of the two calls start at other tokens: equal within the bounds of each
+    assert rel(S, f64(S1)) <= 2 * STATE_TOL
+    assert rel(o[:, n:], f64(o1)) <= 2 * BF16_TOL
+
+
+def test_hybrid_layer_together(layer):
+    """The linear layer of a hybrid as it is used: unit keys by the L2 norm, the prompt, its gradients
+    back through the norm, and decoding that goes on from the prompt's state."""
+    B, T, steps, H, Hk, D = 2, 90, 4, 4, 2, 64
+    g = torch.Generator().manual_seed(8)
+    randn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    q, k, v = (randn(B, T + steps, h, D).bfloat16().cuda() for h in (Hk, Hk, H))
+    gate, beta = (-0.1 * torch.rand(B, T + steps, H, generator=g)).cuda(), torch.rand(B, T + steps, H, generator=g).cuda()
+    norm = layer.QKNorm("l2")
+    cut = lambda x: x[:, :T].contiguous()  # noqa: E731
+    qn, kn = layer.qk_norm_rope(cut(q), cut(k), norm)
+    o, S = layer.delta_prefill(qn, kn, cut(v), cut(gate), cut(beta))
+    prompt = S.clone()
+    outs = []
+    for t in range(T, T + steps):
+        qt, kt = layer.qk_norm_rope(q[:, t:t + 1].contiguous(), k[:, t:t + 1].contiguous(), norm)
+        outs.append(layer.delta_step(qt[:, 0], kt[:, 0], v[:, t].contiguous(), gate[:, t].contiguous(),
+                                     beta[:, t].contiguous(), S))
+    # the oracle on the normed q, k as the norm rounds them
+    qa, ka = layer.qk_norm_rope(q, k, norm)
+    o_ref, S_ref = DO.delta(f64(qa), f64(ka), f64(v), f64(gate), f64(beta))
+    assert rel(torch.cat([o, torch.stack(outs, 1)], 1), o_ref) <= BF16_TOL
+    assert rel(S, S_ref) <= STATE_TOL
+    do = randn(B, T, H, D).bfloat16().cuda()
+    dq, dk, *_ = layer.delta_backward(qn, kn, cut(v), cut(gate), cut(beta), do)
+    dxq, dxk, dwq, dwk = layer.qk_norm_rope_backward(cut(q), cut(k), dq, dk, norm)
+    assert dwq is None and dwk is None and not torch.equal(prompt, S)
+    r = DO.delta_backward(f64(qn), f64(kn), f64(cut(v)), f64(gate[:, :T]), f64(beta[:, :T]), f64(do))
+    for x, d, got in ((q, r[0], dxq), (k, r[1], dxk)):
+        ref, _ = DO.qk_norm_backward(f64(cut(x)), None, d, "l2", 1e-6)
+        # the rule's gradient, then one more rounding; the norm takes the part along x away, which
+        # leaves the rest's error as it was and the rest smaller: by at most the ratio of the two
+        shrink = np.linalg.norm(d / np.linalg.norm(f64(cut(x)), axis=-1, keepdims=True)) / np.linalg.norm(ref)
+        assert rel(got, ref) <= GRAD_TOL * max(shrink, 1) + 2.0 ** -8
+
+
 def test_refusals(layer):
     x = inputs(1, 1, 8, 2, 2, 64, 64)
     call = lambda **c: layer.delta_prefill(**{**{n: x[n] for n in ("q", "k", "v", "g", "beta", "state")}, **c})  # noqa: E731
