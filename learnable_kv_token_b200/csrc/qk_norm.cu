@@ -8,10 +8,13 @@
 //   dx = r w dn - x c r^3 <w dn, x>,   dw = sum over rows of dn x r.
 //
 // Both are bound by memory: every row is read once and written once.  D / 8
-// lanes hold a row, 8 channels (16 bytes of bf16) each; the sums and the
-// partner channels of the (i, i + R/2) pairs go by shuffles.  A group of lanes
-// takes several rows of the same token, so its cosines and sines (more bytes
-// than a bf16 row) are read once, and the rows' loads are in flight together.
+// lanes hold a row, two groups of 4 channels each, chosen so that both members
+// of every pair are in one lane: channels 4 l and R/2 + 4 l on for the (i, i + R/2)
+// pairs, 8 l and 8 l + 4 on otherwise.  Only the sums go by shuffles (with the
+// partners fetched by shuffles too, waits for them were 30 to 44 % of all stalls:
+// 277 us instead of 213 for 32 x 4096 tokens of 20 heads).  A group of lanes takes
+// several rows of the same token, so its cosines and sines (as many bytes as a
+// bf16 row) are read once, and the rows' loads are in flight together.
 #include "lte_common.cuh"
 #include "lte_internal.h"
 
@@ -34,17 +37,21 @@ struct Args {
   float c, eps;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+// a lane's 8 channels: 4 from channel a0 on, 4 from a1 on
+struct Cols {
+  int a0, a1;
+};
+__device__ __forceinline__ void load8(const float* p, Cols c, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p + c.a0), b = *reinterpret_cast<const float4*>(p + c.a1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-// eight channels as they lie in memory: rows in flight take 4 registers in bf16, 8 in fp32
+// as they lie in memory: rows in flight take 4 registers in bf16, 8 in fp32
 template <typename T> struct Raw8;
 template <> struct Raw8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+  __device__ __forceinline__ void load(const float* p, Cols c) {
+    a = *reinterpret_cast<const float4*>(p + c.a0);
+    b = *reinterpret_cast<const float4*>(p + c.a1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -52,11 +59,14 @@ template <> struct Raw8<float> {
   }
 };
 template <> struct Raw8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, Cols c) {
+    a = *reinterpret_cast<const uint2*>(p + c.a0);
+    b = *reinterpret_cast<const uint2*>(p + c.a1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint2(0, 0); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    const uint32_t u[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(u[i] << 16);
@@ -64,18 +74,19 @@ template <> struct Raw8<__nv_bfloat16> {
     }
   }
 };
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* p, Cols c, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p + c.a0) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + c.a1) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, Cols c, const float (&v)[8]) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  *reinterpret_cast<uint2*>(p + c.a0) = make_uint2(u[0], u[1]);
+  *reinterpret_cast<uint2*>(p + c.a1) = make_uint2(u[2], u[3]);
 }
 template <int LPR>
 __device__ __forceinline__ float row_sum(float s) {
@@ -84,56 +95,50 @@ __device__ __forceinline__ float row_sum(float s) {
   return s;
 }
 
-// The rotation's factors for one lane's 8 channels: cos and sin of the pair of
-// each channel, sin negated on the pair's first member (y = x cos + partner sin).
-// A position outside the table gives NaN, which reaches the output.
+// lane lg of a row: its channels
+__device__ __forceinline__ Cols cols_of(const Args& a, int lg) {
+  if (!a.inter && 8 * lg < a.rot) return Cols{4 * lg, a.rot / 2 + 4 * lg};
+  return Cols{8 * lg, 8 * lg + 4};
+}
+// The rotation's factors for one lane's four pairs.  Lanes behind R turn by nothing;
+// a position outside the table gives NaN, which reaches the output.
 struct Turn {
-  float c[8], s[8];
-  int src;                     // lane that holds the partner channels ((i, i + R/2) pairs)
+  float c[4], s[4];
 };
-template <int LPR>
 __device__ __forceinline__ void load_turn(const Args& a, int lg, unsigned token, int pos, float dir, Turn& t) {
-  const int lane = threadIdx.x & 31, e0 = lg * 8, R = a.rot;
-  t.src = lane;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     t.c[i] = 1.f;
     t.s[i] = 0.f;
   }
-  if (e0 >= R) return;
+  if (8 * lg >= a.rot) return;
   const int p = a.pos != nullptr ? a.pos[token] : pos;
   const bool ok = p >= 0 && p < a.n_pos;
-  const float* row = a.table + (long long)(ok ? p : 0) * R;
+  const float* row = a.table + (long long)(ok ? p : 0) * a.rot + 4 * lg;
+  const float4 c4 = *reinterpret_cast<const float4*>(row), s4 = *reinterpret_cast<const float4*>(row + a.rot / 2);
   const float bad = __int_as_float(0x7fc00000);
-  if (a.inter) {
-    const float4 c4 = *reinterpret_cast<const float4*>(row + e0 / 2);
-    const float4 s4 = *reinterpret_cast<const float4*>(row + R / 2 + e0 / 2);
-    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t.c[2 * i] = t.c[2 * i + 1] = ok ? cc[i] : bad;
-      t.s[2 * i] = -dir * ss[i];
-      t.s[2 * i + 1] = dir * ss[i];
-    }
-  } else {
-    const bool first = e0 < R / 2;
-    const int i0 = first ? e0 : e0 - R / 2;
-    t.src = first ? lane + R / 16 : lane - R / 16;
-    load8(row + i0, t.c);
-    load8(row + R / 2 + i0, t.s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t.c[i] = ok ? t.c[i] : bad;
-      t.s[i] *= first ? -dir : dir;
-    }
-  }
+  t.c[0] = ok ? c4.x : bad; t.c[1] = ok ? c4.y : bad; t.c[2] = ok ? c4.z : bad; t.c[3] = ok ? c4.w : bad;
+  t.s[0] = dir * s4.x; t.s[1] = dir * s4.y; t.s[2] = dir * s4.z; t.s[3] = dir * s4.w;
 }
 __device__ __forceinline__ void turn8(const Turn& t, bool inter, float (&v)[8]) {
   float o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = inter ? v[i ^ 1] : __shfl_sync(0xffffffffu, v[i], t.src);
+  for (int i = 0; i < 4; ++i) {
+    const float x = inter ? v[2 * i] : v[i], y = inter ? v[2 * i + 1] : v[i + 4];
+    const float p = fmaf(x, t.c[i], -y * t.s[i]), q = fmaf(y, t.c[i], x * t.s[i]);
+    o[i] = p;
+    o[i + 4] = q;
+  }
+  if (inter) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], t.c[i], o[i] * t.s[i]);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = o[i];
+      v[2 * i + 1] = o[i + 4];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = o[i];
+  }
 }
 
 // A group of lanes takes rows [h0, h0 + rows) of one token's queries or keys.
@@ -156,7 +161,7 @@ __device__ __forceinline__ Group group_of(const Args& a, unsigned gi, int which,
 }
 
 template <typename T, int D, int RPG>
-__global__ void __launch_bounds__(kThreads, 4) qk_norm_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 5) qk_norm_kernel(const Args a) {
   constexpr int LPR = D / 8, kGroups = kThreads / LPR;
   const int lg = threadIdx.x % LPR;
   const unsigned partsq = (a.H[0] + RPG - 1) / RPG, parts = partsq + (a.H[1] + RPG - 1) / RPG;
@@ -165,18 +170,19 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_kernel(const Args a) {
   if (!live) gi = 0;                                       // the lanes stay for the shuffles
   const int which = gi % parts >= partsq;
   const Group g = group_of<RPG>(a, gi, which, parts, which ? partsq : 0);
-  const T* x = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h + lg * 8;
-  T* y = (T*)a.y[which] + ((long long)g.token * a.H[which] + g.h0) * D + lg * 8;
+  const T* x = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h;
+  T* y = (T*)a.y[which] + ((long long)g.token * a.H[which] + g.h0) * D;
+  const Cols cols = cols_of(a, lg);
   Raw8<T> raw[RPG];
 #pragma unroll
   for (int i = 0; i < RPG; ++i) {
-    if (i < g.rows) raw[i].load(x + i * a.xs[which].h);
+    if (i < g.rows) raw[i].load(x + i * a.xs[which].h, cols);
     else raw[i].zero();
   }
   Turn turn;
-  load_turn<LPR>(a, lg, g.token, (int)g.t, 1.f, turn);
+  load_turn(a, lg, g.token, (int)g.t, 1.f, turn);
   float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-  if (a.norm && a.w[which] != nullptr) load8(a.w[which] + lg * 8, w);
+  if (a.norm && a.w[which] != nullptr) load8(a.w[which], cols, w);
 #pragma unroll
   for (int i = 0; i < RPG; ++i) {
     float v[8];
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_kernel(const Args a) {
       for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
     }
     if (a.rot) turn8(turn, a.inter, v);
-    if (live && i < g.rows) store8(y + i * D, v);
+    if (live && i < g.rows) store8(y + i * D, cols, v);
   }
 }
 
@@ -206,33 +212,34 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_backward_kernel(const Arg
   const int which = (int)blockIdx.x >= blocks_q;
   const unsigned block = which ? blockIdx.x - blocks_q : blockIdx.x, blocks = which ? gridDim.x - blocks_q : blocks_q;
   const unsigned parts = (a.H[which] + RPG - 1) / RPG, total = (unsigned)a.tokens * parts;
+  const Cols cols = cols_of(a, lg);
   float dw[8], w[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     dw[e] = 0.f;
     w[e] = 1.f;
   }
-  if (a.norm && a.w[which] != nullptr) load8(a.w[which] + lg * 8, w);
+  if (a.norm && a.w[which] != nullptr) load8(a.w[which], cols, w);
   for (unsigned g0 = block * kGroups; g0 < total; g0 += blocks * kGroups) {
     const bool live = g0 + grp < total;
     const Group g = group_of<RPG>(a, live ? g0 + grp : 0, which, parts, 0);
-    const T* xp = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h + lg * 8;
-    const long long at = ((long long)g.token * a.H[which] + g.h0) * D + lg * 8;
+    const T* xp = (const T*)a.x[which] + g.b * a.xs[which].b + g.t * a.xs[which].t + g.h0 * a.xs[which].h;
+    const long long at = ((long long)g.token * a.H[which] + g.h0) * D;
     const TG* dp = (const TG*)a.dy[which] + at;
     Raw8<T> rx[RPG];
     Raw8<TG> rd[RPG];
 #pragma unroll
     for (int i = 0; i < RPG; ++i) {
       if (live && i < g.rows) {
-        rd[i].load(dp + i * D);
-        rx[i].load(xp + i * a.xs[which].h);
+        rd[i].load(dp + i * D, cols);
+        rx[i].load(xp + i * a.xs[which].h, cols);
       } else {                                             // zeros add nothing to the weight gradients
         rd[i].zero();
         rx[i].zero();
       }
     }
     Turn turn;
-    load_turn<LPR>(a, lg, g.token, (int)g.t, -1.f, turn);
+    load_turn(a, lg, g.token, (int)g.t, -1.f, turn);
 #pragma unroll
     for (int i = 0; i < RPG; ++i) {
       const bool on = live && i < g.rows;
@@ -255,11 +262,11 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_backward_kernel(const Arg
           dn[e] = fmaf(r * w[e], dn[e], -m * v[e]);
         }
       }
-      if (on) store8((T*)a.y[which] + at + i * D, dn);
+      if (on) store8((T*)a.y[which] + at + i * D, cols, dn);
     }
   }
   if (a.part == nullptr) return;
-  store8(&red[grp][lg * 8], dw);
+  store8(&red[grp][0], cols, dw);
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
