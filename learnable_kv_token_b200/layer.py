@@ -457,12 +457,20 @@ def delta_step(q_t, k_t, v_t, g_t, beta_t, state, scale=None, out=None):
     B, H, dv = v_t.shape
     dt, dev = q_t.dtype, q_t.device
     Hk, dk = q_t.shape[1:]
-    _check(q_t, "q_t", (B, Hk, dk), dt, dev)
-    _check(k_t, "k_t", (B, Hk, dk), dt, dev)
-    _check(v_t, "v_t", (B, H, dv), dt, dev)
-    _check(g_t, "g_t", (B, H), torch.float32, dev)
-    _check(beta_t, "beta_t", (B, H), torch.float32, dev)
-    _check(state, "state", (B, H, dv, dk), torch.float32, dev)
+    # one call per token and layer: the common case in as few steps as it takes, else the reason
+    at, f32 = dev.index, torch.float32
+    if not (q_t.shape == k_t.shape and q_t.shape[0] == B and g_t.shape == beta_t.shape == v_t.shape[:2]
+            and state.shape == (B, H, dv, dk) and k_t.dtype is v_t.dtype is dt
+            and g_t.dtype is beta_t.dtype is state.dtype is f32
+            and k_t.get_device() == v_t.get_device() == g_t.get_device() == beta_t.get_device() == state.get_device() == at
+            and q_t.is_contiguous() and k_t.is_contiguous() and v_t.is_contiguous() and g_t.is_contiguous()
+            and beta_t.is_contiguous() and state.is_contiguous()):
+        _check(q_t, "q_t", (B, Hk, dk), dt, dev)
+        _check(k_t, "k_t", (B, Hk, dk), dt, dev)
+        _check(v_t, "v_t", (B, H, dv), dt, dev)
+        _check(g_t, "g_t", (B, H), f32, dev)
+        _check(beta_t, "beta_t", (B, H), f32, dev)
+        _check(state, "state", (B, H, dv, dk), f32, dev)
     if out is None:
         out = torch.empty_like(v_t)
     else:

@@ -155,9 +155,9 @@ def _strides(t):
 
 
 def dtype_code(dt: torch.dtype) -> int:
-    if dt == torch.bfloat16:
+    if dt is torch.bfloat16:
         return LTE_BF16
-    if dt == torch.float32:
+    if dt is torch.float32:
         return LTE_F32
     raise ValueError(f"unsupported dtype {dt}")
 
