@@ -6,7 +6,14 @@
 
 namespace lte {
 
-bool delta_chunked(const lte_gdr_dims* d) { return d->dtype == LTE_BF16 && d->T > delta::kFewTokens; }
+// Few tokens run token by token: a chunk costs its two launches (16 us, 49 for 512
+// heads) however empty it is, a token 0.34 us while its CTAs (one per 16 value
+// channels of a head) find an SM each, 0.5 at 512 of them, 3.1 at 4096.  Measured
+// crossings: 40 tokens for 4 heads of 128 channels, 28 for 64, 15 for 512.
+bool delta_chunked(const lte_gdr_dims* d) {
+  const long long strips = (long long)d->B * d->H * (d->dv / 16);
+  return d->dtype == LTE_BF16 && d->T > (strips <= 148 ? 40 : strips <= 512 ? 28 : 15);
+}
 
 namespace {
 // workspace: records, then the segments' maps and states

@@ -78,7 +78,7 @@ def test_pointers_strides_and_workspace(L):
     need = L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD)
     assert need > 0 and backward(L, d, need - 1) == WORKSPACE and backward(L, d, ws=None) == WORKSPACE
     # fp32 and few tokens run token by token, without a workspace; gradients are bf16 only
-    for d in (dims(L, dtype=L.LTE_F32), dims(L, T=16)):
+    for d in (dims(L, dtype=L.LTE_F32), dims(L, T=15)):
         assert L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL) == 0
     d = dims(L, dtype=L.LTE_F32)
     assert L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD) == 0 and backward(L, d, 1 << 40) == UNSUPPORTED
