@@ -12,11 +12,11 @@
 // Columns: dS (DK), dS hi, lo (DK / 2 each), P or dU (64), F (64), X, then F as
 // fp32 (64), dO^T, then scale e^G dO^T as hi + lo (64).
 //
-// Warps 0-7 keep the chain; 8-15 scale dO, write the images of dS and F and dV,
-// and take the sums over value channels that the gates' gradients need: u.F / b
-// and v.F per token, <dS, S> per chunk (two threads per value channel, half of the
-// columns each, here too); 16 loads; 17 issues the MMAs.  Registers: 112 for the
-// chain, 104 for the sums, 48 for the rest; one spilled costs a trip to L2.
+// Warps 0-7 keep the chain.  8-11 scale dO, write the image of dS and take <dS, S>;
+// 12-15 write dV and the image of F and take the sums over value channels u.F / b
+// and v.F per token (the sums are what the gates' gradients need).  16 loads; 17
+// issues the MMAs.  Registers: 112 for the chain, 104 for the sums, 48 for the rest;
+// one spilled costs a trip to L2.
 // The products of dO with Q run while the chain warps turn F, so the chain of a
 // chunk is P -> dU -> F -> dS as in the forward pass.
 #include <math.h>
@@ -39,7 +39,7 @@ constexpr uint32_t kIdent = 2 * kStage, kOut = kIdent + kImg, kBars = kOut + 2 *
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bX = 7, bP = 8, bUr = 9, bF = 10, bFr = 11, bFx = 12, bXf = 13,
-             bDr = 14, bS = 15, bSread = 17, bDrain = 18, kBarCount = 19 };
+             bDr = 14, bS = 15, bSread = 17, bD = 18, bDrain = 19, kBarCount = 20 };
 constexpr uint32_t kColS = 0, kColP = 256, kColF = 320, kColX = 384, kColD = 448;
 
 // z[j] summed over the warp's lanes; lane j gets the sum of z[j].  At each step
@@ -100,8 +100,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
       const bool chain = i == bSr || i == bSr + 1 || i == bUr || i == bFr || i == bFx;     // 8 chain warps
-      const bool out = i == bDr || i == bXf || i == bSread;                                // 8 output warps
-      mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain || out ? 8 : 1);
+      const bool out = i == bDr || i == bXf || i == bSread;                                // one output group
+      mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -174,22 +174,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const int s = i & 1, ph = i & 1;
       const uint32_t d = s0 + s * kStage;
       if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
-      if (i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
       tc_fence_after();
       issued = true;
       const uint64_t dk = sdesc(d + kK, 16, 1024), dd = sdesc(d + kD, kHalf, 1024), dt = sdesc(d + kR, kHalf, 1024);
-      if (elect_one()) {                                       // dO^T, and X = dO^T A
-#pragma unroll
-        for (int ks = 0; ks < L / 16; ++ks)
-          mma_f16(tmem + kColD, dd + ((ks * 2048) >> 4), ident + ((ks * 32) >> 4), id_dt, ks > 0);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = L / 16 - 1; ks >= 0; --ks)
-            mma_f16(tmem + kColX, dd + ((ks * 2048) >> 4), dt + (((2 + p) * kImg + ks * 2048) >> 4),
-                    idesc2(128, 16 * (ks + 1), true, true), !(p == 0 && ks == L / 16 - 1));
-        mma_commit(bar(bX));
-      }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {                            // P = dS K^T, by halves of dS's columns
         if (ok) ok = wwait(bar(bSr + p), ph, abort_flag, nullptr, 0);
@@ -206,6 +193,22 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
       }
       if (!ok) break;
+      // (X's columns still hold the F of the chunk before until its sums have been taken)
+      if (i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      tc_fence_after();
+      if (elect_one()) {                                       // X = dO^T A, and dO^T
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = L / 16 - 1; ks >= 0; --ks)
+            mma_f16(tmem + kColX, dd + ((ks * 2048) >> 4), dt + (((2 + p) * kImg + ks * 2048) >> 4),
+                    idesc2(128, 16 * (ks + 1), true, true), !(p == 0 && ks == L / 16 - 1));
+        mma_commit(bar(bX));
+#pragma unroll
+        for (int ks = 0; ks < L / 16; ++ks)
+          mma_f16(tmem + kColD, dd + ((ks * 2048) >> 4), ident + ((ks * 32) >> 4), id_dt, ks > 0);
+        mma_commit(bar(bD));
+      }
       if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
       tc_fence_after();
       if (elect_one()) {                                       // F = dU T, columns s < 16 (ks + 1)
@@ -409,216 +412,227 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
     }
   } else if (warp < 16) {
-    // =============================================== dO, images, dV, sums
-    regs_inc<104>();
-    const int quad = warp & 3, oh = (warp >> 2) & 1, row = quad * 32 + lane;   // oh: which half of the columns
+    // ================================================= the two output groups
+    const int quad = warp & 3, row = quad * 32 + lane;
     const bool mine = quad * 32 < DV;                          // a warp of value channels that exist
     const int rb = row >> 3, r7 = row & 7;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    __nv_bfloat16* dvp = ga.dv + ((long long)b * a.T * a.H + h) * DV;
-    // this row's 16 bytes in column block 0 of the images of S_0, dS, U and F of a chunk
+    // this row's 16 bytes in column block 0 of the images of S_0, dS, U and F
     const int at_s = rb * (DK / 8) * 128 + r7 * 16, at_t = rb * (L / 8) * 128 + r7 * 16;
     const uint8_t* s_img = reinterpret_cast<const uint8_t*>(a.s0) + (long long)u * a.chunks * (DV * DK * 4) + at_s;
-    const uint8_t* u_img = reinterpret_cast<const uint8_t*>(a.u) + (long long)u * a.chunks * (DV * L * 4) + at_t;
-    uint8_t* d_img = reinterpret_cast<uint8_t*>(ga.ds) + (long long)u * a.chunks * (DV * DK * 2) + at_s;
-    uint8_t* f_img = reinterpret_cast<uint8_t*>(ga.fimg) + (long long)u * a.chunks * (DV * L * 2) + at_t;
-    auto put_inner = [&](int c, float s) {
+    if (warp < 12) {
+      regs_inc<120>();
+      // ---- scale e^G dO, the image of dS, <dS, S>
+      uint8_t* d_img = reinterpret_cast<uint8_t*>(ga.ds) + (long long)u * a.chunks * (DV * DK * 2) + at_s;
+      constexpr int kAhead = 4;
+      auto put_inner = [&](int c, float s) {
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0 && mine) ga.inner[((long long)u * a.chunks + c) * kStrips + 2 * quad + oh] = s;
-    };
-    for (int i = 0; i < n; ++i) {
-      const int s = i & 1, ph = i & 1, c = n - 1 - i;
-      // (a warp whose wait gave up still meets the others at the vote below)
-      ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
-      const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
-      const long long img = (long long)u * a.chunks + c;
-      // ---- the state of the chunk behind, hi and lo: on its way long before its use
-      uint4 st[2][8];
-      const bool inner = mine && i > 0;
-      auto fetch_state = [&](int j) {
-        const uint8_t* p = s_img + (long long)(c + 1) * (DV * DK * 4) + (oh * (DK / 64) + j) * 512;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          st[j][e] = load_once(p + e * 128);
-          st[j][4 + e] = load_once(p + DV * DK * 2 + e * 128);
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0 && mine) {                               // (the warp's second strip of 16: nothing)
+          float* p = ga.inner + ((long long)u * a.chunks + c) * kStrips + 2 * quad;
+          p[0] = s;
+          p[1] = 0.f;
         }
       };
-      if (inner) fetch_state(0);
-      // ---- scale e^G dO^T as hi and lo
-      ok = ok && wwait(bar(bX), ph, abort_flag, nullptr, 0);
-      tc_fence_after();
-      {
-        uint32_t hi[16], lo[16];
+      for (int i = 0; i < n; ++i) {
+        const int s = i & 1, ph = i & 1, c = n - 1 - i;
+        if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+        const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
+        // the state of the chunk behind, hi and lo, 16 key channels at a time, asked for
+        // kAhead pieces ahead of their use: as much in flight as registers hold
+        uint4 st[kAhead + 1][4];
+        const bool inner = mine && i > 0;
+        auto fetch_state = [&](int j) {
+          const uint8_t* p = s_img + (long long)(c + 1) * (DV * DK * 4) + j * 256;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {                          // 16 columns at a time
-          uint32_t r[16];
-          tmem_ld16(la + kColD + 32 * oh + 16 * q, r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * oh + 16 * q + 4 * e);
-            split_pair(mul2(pair_of(r + 4 * e), f2(a.scale * g.x, a.scale * g.y)), hi[8 * q + 2 * e], lo[8 * q + 2 * e]);
-            split_pair(mul2(pair_of(r + 4 * e + 2), f2(a.scale * g.z, a.scale * g.w)), hi[8 * q + 2 * e + 1], lo[8 * q + 2 * e + 1]);
+          for (int e = 0; e < 2; ++e) {
+            st[j % (kAhead + 1)][e] = load_once(p + e * 128);
+            st[j % (kAhead + 1)][2 + e] = load_once(p + DV * DK * 2 + e * 128);
           }
+        };
+        if (inner)
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) fetch_state(j);
+        // scale e^G dO^T as hi and lo
+        if (!(ok = wwait(bar(bD), ph, abort_flag, nullptr, 0))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {                        // 16 columns at a time
+            uint32_t r[16];
+            tmem_ld16(la + kColD + 32 * j + 16 * q, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 g = *reinterpret_cast<const float4*>(scal + kEG * L + 32 * j + 16 * q + 4 * e);
+              split_pair(mul2(pair_of(r + 4 * e), f2(a.scale * g.x, a.scale * g.y)), hi[8 * q + 2 * e], lo[8 * q + 2 * e]);
+              split_pair(mul2(pair_of(r + 4 * e + 2), f2(a.scale * g.z, a.scale * g.w)), hi[8 * q + 2 * e + 1], lo[8 * q + 2 * e + 1]);
+            }
+          }
+          tmem_st16(la + kColD + 32 * j, hi);
+          tmem_st16(la + kColD + 32 * j + 16, lo);
         }
-        tmem_st16(la + kColD + 32 * oh, hi);
-        tmem_st16(la + kColD + 32 * oh + 16, lo);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bDr));
-      // ---- dS: its image (hi), and <dS, S_0> with the state of the chunk behind
-      if (inner && DK > 64) fetch_state(1);
-      ok = ok && wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0);
-      tc_fence_after();
-      {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(bDr));
+          mbar_arrive(bar(bEmpty + s));
+        }
+        // dS: its image (hi), and <dS, S_0> with the state of the chunk behind
+        if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0))) break;
+        tc_fence_after();
         float in = 0.f;
         uint8_t* im = d_img + (long long)c * (DV * DK * 2);
 #pragma unroll
-        for (int j = 0; j < DK / 64; ++j) {                    // 32 key channels: 16 words each of hi and lo
-          const int jc = oh * (DK / 64) + j;
-          uint32_t hi[16], lo[16];
-          tmem_ld16(la + kColSh + 16 * jc, hi);
-          tmem_ld16(la + kColSl + 16 * jc, lo);
+        for (int j = 0; j < DK / 16; ++j) {                    // 16 key channels: 8 words each of hi and lo
+          uint32_t hi[8], lo[8];
+          if (inner && j + kAhead < DK / 16) fetch_state(j + kAhead);
+          tm_ld(la + kColSh + 8 * j, hi);
+          tm_ld(la + kColSl + 8 * j, lo);
           tmem_wait_ld();
+          if (j == DK / 16 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bSread));
+          }
           if (mine) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(im + (4 * jc + e) * 128) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
           }
           if (inner) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               float x[8];
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 x[2 * f] = bf_lo(hi[4 * e + f]) + bf_lo(lo[4 * e + f]);
                 x[2 * f + 1] = bf_hi(hi[4 * e + f]) + bf_hi(lo[4 * e + f]);
               }
-              in = dot8(st[j][e], st[j][4 + e], x, in);
+              in = dot8(st[j % (kAhead + 1)][e], st[j % (kAhead + 1)][2 + e], x, in);
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bSread));
         if (i > 0) put_inner(c + 1, in);
       }
-      // ---- F: image, dV, u.F / b and v.F per token (32 tokens)
-      uint4 uw[8];
-      const int j = oh;
-      auto fetch_u = [&]() {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint8_t* p = u_img + (long long)c * (DV * L * 4) + (4 * j + e) * 128;
-          uw[e] = load_once(p);
-          uw[4 + e] = load_once(p + DV * L * 2);
-        }
-      };
-      if (mine) fetch_u();
-      ok = ok && wwait(bar(bFx), ph, abort_flag, nullptr, 0);
-      tc_fence_after();
-      if (tid == 256) bulk_wait_read();                        // the chunk before has left the buffer
-      if (!(ok = bar_and(1, 256, ok))) break;
-      const uint32_t colv = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
-      const int cv = (row & 63) >> 3;
-      uint8_t* im = f_img + (long long)c * (DV * L * 2);
-      float* xp = ga.x + (img * kStrips + 2 * quad) * (2 * L);
-      {
-        uint32_t F[32];
-        tmem_ld32(la + kColX + 32 * j, F);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bXf));
-        if (mine) {
-          float z[32];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t wh[4] = {uw[e].x, uw[e].y, uw[e].z, uw[e].w};
-            const uint32_t wl[4] = {uw[4 + e].x, uw[4 + e].y, uw[4 + e].z, uw[4 + e].w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              z[8 * e + 2 * f] = __uint_as_float(F[8 * e + 2 * f]) * (bf_lo(wh[f]) + bf_lo(wl[f]));
-              z[8 * e + 2 * f + 1] = __uint_as_float(F[8 * e + 2 * f + 1]) * (bf_hi(wh[f]) + bf_hi(wl[f]));
-            }
-          }
-          const float x = lane_sums(z, lane) / scal[kBeta * L + 32 * j + lane];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int t = 32 * j + e;
-            z[e] = __uint_as_float(F[e]) *
-                   __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + s * kStage + kV + colv + t * 128 + ((cv ^ (t & 7)) << 4)));
-          }
-          const float v = lane_sums(z, lane);
-          xp[32 * j + lane] = x;
-          xp[L + 32 * j + lane] = v;
-          xp[2 * L + 32 * j + lane] = 0.f;                     // the warp's second strip of 16
-          xp[3 * L + 32 * j + lane] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              w[f] = pack_bf16(__uint_as_float(F[8 * e + 2 * f]), __uint_as_float(F[8 * e + 2 * f + 1]));
-              const int t = 32 * j + 8 * e + 2 * f;
-              *reinterpret_cast<uint16_t*>(sm + kOut + colv + t * 128 + ((cv ^ (t & 7)) << 4)) = (uint16_t)(w[f] & 0xffff);
-              *reinterpret_cast<uint16_t*>(sm + kOut + colv + (t + 1) * 128 + ((cv ^ ((t + 1) & 7)) << 4)) = (uint16_t)(w[f] >> 16);
-            }
-            *reinterpret_cast<uint4*>(im + (4 * j + e) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bEmpty + s));
-      const int nt = len - c * L;
-      if (nt >= L) {
-        fence_proxy_async();
-        bar_sync(1, 256);
-        if (tid == 256) {
-          for (int j = 0; j < kHV; ++j) tma_store_4d(&tm_dv, s0 + kOut + j * kHalf, 64 * j, h, c * L, b);
-          bulk_commit();
-        }
-      } else {
-        bar_sync(1, 256);
-        for (int j = tid - 256; j < nt * (DV / 8); j += 256) {
-          const int t = j / (DV / 8), cc = j % (DV / 8);
-          *reinterpret_cast<uint4*>(dvp + (long long)(c * L + t) * a.H * DV + cc * 8) =
-              *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
-        }
-      }
-    }
-    // ---- the gradient of the initial state with that state
-    if (ok && n > 0) {
-      ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
-      tc_fence_after();
-      if (ok) {
+      // the gradient of the initial state with that state
+      if (ok && n > 0 && wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) &&
+          wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0)) {
+        tc_fence_after();
         float in = 0.f;
 #pragma unroll
-        for (int k = 0; k < DK / 32; ++k) {
-          const int j = oh * (DK / 32) + k;
+        for (int j = 0; j < DK / 16; ++j) {
           uint32_t r[16];
           tmem_ld16(la + kColS + 16 * j, r);
           tmem_wait_ld();
           if (mine) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint4 sh = load_once(s_img + (2 * j + e) * 128);
-              const uint4 sl = load_once(s_img + DV * DK * 2 + (2 * j + e) * 128);
               float x[8];
 #pragma unroll
               for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(r[8 * e + f]);
-              in = dot8(sh, sl, x, in);
+              in = dot8(load_once(s_img + (2 * j + e) * 128), load_once(s_img + DV * DK * 2 + (2 * j + e) * 128), x, in);
             }
           }
         }
         put_inner(0, in);
       }
+    } else {
+      regs_dec<88>();
+      // ---- F: image, dV, u.F / b and v.F per token
+      const uint8_t* u_img = reinterpret_cast<const uint8_t*>(a.u) + (long long)u * a.chunks * (DV * L * 4) + at_t;
+      uint8_t* f_img = reinterpret_cast<uint8_t*>(ga.fimg) + (long long)u * a.chunks * (DV * L * 2) + at_t;
+      __nv_bfloat16* dvp = ga.dv + ((long long)b * a.T * a.H + h) * DV;
+      const uint32_t colv = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
+      const int cv = (row & 63) >> 3;
+      for (int i = 0; i < n; ++i) {
+        const int s = i & 1, ph = i & 1, c = n - 1 - i;
+        const long long img = (long long)u * a.chunks + c;
+        // (a warp whose wait gave up still meets the others at the vote below)
+        ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
+        const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
+        uint4 uw[2][4];
+        auto fetch_u = [&](int j) {                            // 16 tokens, hi and lo
+          const uint8_t* p = u_img + (long long)c * (DV * L * 4) + j * 256;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uw[j & 1][e] = load_once(p + e * 128);
+            uw[j & 1][2 + e] = load_once(p + DV * L * 2 + e * 128);
+          }
+        };
+        if (mine) fetch_u(0);
+        ok = ok && wwait(bar(bFx), ph, abort_flag, nullptr, 0);
+        tc_fence_after();
+        if (tid == 384) bulk_wait_read();                      // the chunk before has left the buffer
+        if (!(ok = bar_and(1, 128, ok))) break;
+        uint8_t* im = f_img + (long long)c * (DV * L * 2);
+        float* xp = ga.x + (img * kStrips + 2 * quad) * (2 * L);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                          // 16 tokens
+          uint32_t F[16];
+          if (mine && j < 3) fetch_u(j + 1);
+          tmem_ld16(la + kColX + 16 * j, F);
+          tmem_wait_ld();
+          if (j == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bXf));
+          }
+          if (mine) {
+            float z[32];                                       // 16 products with u, 16 with v
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 h4 = uw[j & 1][e], l4 = uw[j & 1][2 + e];
+              const uint32_t wh[4] = {h4.x, h4.y, h4.z, h4.w}, wl[4] = {l4.x, l4.y, l4.z, l4.w};
+              uint32_t w[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const int k = 8 * e + 2 * f, t = 16 * j + k;
+                const float f0 = __uint_as_float(F[k]), f1 = __uint_as_float(F[k + 1]);
+                const uint32_t a0 = colv + t * 128 + ((cv ^ (t & 7)) << 4), a1 = colv + (t + 1) * 128 + ((cv ^ ((t + 1) & 7)) << 4);
+                const uint32_t v0 = *reinterpret_cast<const uint16_t*>(sm + s * kStage + kV + a0);
+                const uint32_t v1 = *reinterpret_cast<const uint16_t*>(sm + s * kStage + kV + a1);
+                z[k] = f0 * (bf_lo(wh[f]) + bf_lo(wl[f]));
+                z[k + 1] = f1 * (bf_hi(wh[f]) + bf_hi(wl[f]));
+                z[16 + k] = f0 * bf_lo(v0);
+                z[17 + k] = f1 * bf_lo(v1);
+                w[f] = pack_bf16(f0, f1);
+                *reinterpret_cast<uint16_t*>(sm + kOut + a0) = (uint16_t)(w[f] & 0xffff);
+                *reinterpret_cast<uint16_t*>(sm + kOut + a1) = (uint16_t)(w[f] >> 16);
+              }
+              *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            const float sum = lane_sums(z, lane);              // lanes 0-15: u.F, 16-31: v.F of token lane mod 16
+            const int t = 16 * j + (lane & 15);
+            xp[(lane >> 4) * L + t] = lane < 16 ? sum / scal[kBeta * L + t] : sum;
+            xp[2 * L + (lane >> 4) * L + t] = 0.f;             // the warp's second strip of 16
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bEmpty + s));
+        const int nt = len - c * L;
+        if (nt >= L) {
+          fence_proxy_async();
+          bar_sync(1, 128);
+          if (tid == 384) {
+            for (int j = 0; j < kHV; ++j) tma_store_4d(&tm_dv, s0 + kOut + j * kHalf, 64 * j, h, c * L, b);
+            bulk_commit();
+          }
+        } else {
+          bar_sync(1, 128);
+          for (int j = tid - 384; j < nt * (DV / 8); j += 128) {
+            const int t = j / (DV / 8), cc = j % (DV / 8);
+            *reinterpret_cast<uint4*>(dvp + (long long)(c * L + t) * a.H * DV + cc * 8) =
+                *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
+          }
+        }
+      }
     }
   }
-  if (tid == 256) bulk_wait_all();                             // output stores complete before exit
+  if (tid == 384) bulk_wait_all();                             // output stores complete before exit
   // copies in flight land before exit (only after a wait gave up)
   if (warp == 16 && *abort_flag) {
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)

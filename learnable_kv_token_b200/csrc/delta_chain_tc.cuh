@@ -66,6 +66,11 @@ __device__ __forceinline__ void split_pairs(const uint64_t (&x)[N], uint32_t (&h
 // columns of this warp's lanes <-> registers, by count
 __device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[32]) { tmem_ld32(t, r); }
 __device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
 __device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[32]) { tmem_st32(t, r); }
 __device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
 __device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&r)[8]) {
