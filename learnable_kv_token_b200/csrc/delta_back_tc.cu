@@ -34,12 +34,12 @@ constexpr int kThreads = 640;
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kD = 4 * kHalf, kV = 6 * kHalf, kR = 8 * kHalf;
 constexpr uint32_t kScalOff = kR + 4 * kImg;
 constexpr uint32_t kStage = (kScalOff + kScal + 1023) / 1024 * 1024;
-// then the identity and a chunk of dV as token rows
-constexpr uint32_t kIdent = 2 * kStage, kOut = kIdent + kImg, kBars = kOut + 2 * kHalf, kSmem = kBars + 256;
+// then the identity and the last 32 of 128 key channels of a state (128 rows, hi and lo)
+constexpr uint32_t kIdent = 2 * kStage, kState = kIdent + kImg, kBars = kState + 2 * 128 * 64, kSmem = kBars + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 enum : int { bFull = 0, bEmpty = 2, bTail = 4, bSr = 5, bX = 7, bP = 8, bUr = 9, bF = 10, bFr = 11, bFx = 12, bXf = 13,
-             bDr = 14, bS = 15, bSread = 17, bD = 18, bDrain = 19, kBarCount = 20 };
+             bDr = 14, bS = 15, bSread = 17, bD = 18, bSt = 19, bStFree = 20, bDrain = 21, kBarCount = 22 };
 constexpr uint32_t kColS = 0, kColP = 256, kColF = 320, kColX = 384, kColD = 448;
 
 // z[j] summed over the warp's lanes; lane j gets the sum of z[j].  At each step
@@ -100,7 +100,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
       const bool chain = i == bSr || i == bSr + 1 || i == bUr || i == bFr || i == bFx;     // 8 chain warps
-      const bool out = i == bDr || i == bXf || i == bSread;                                // one output group
+      const bool out = i == bDr || i == bXf || i == bSread || i == bStFree;                                // one output group
       mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
@@ -148,6 +148,16 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         prefetch_l2(reinterpret_cast<const uint8_t*>(a.s0 + img * DV * DK) + lane * (DV * DK / 8), DV * DK / 8);
       }
       ++loaded;
+      if (DK == 128 && i > 0) {                                // the state of the chunk behind, key channels 96 on
+        if (i > 1 && !(ok = wwait(bar(bStFree), i & 1, abort_flag, nullptr, 0))) break;
+        if (lane == 0) mbar_expect_tx(bar(bSt), DV / 8 * 2 * 512);
+        __syncwarp();
+        const int rb = lane & 15, p = lane >> 4;               // a lane per eight rows of hi or lo
+        if (rb < DV / 8)
+          bulk_load(s0 + kState + p * (128 * 64) + rb * 512,
+                    reinterpret_cast<const uint8_t*>(a.s0) + ((long long)u * a.chunks + c + 1) * (DV * DK * 4) + p * (DV * DK * 2) +
+                        rb * (DK / 8) * 128 + 12 * 128, 512, bar(bSt));
+      }
       if (tail) {
         if (!(ok = wwait(fb, 0, abort_flag, nullptr, 0))) break;
         const int r0 = len - c * L;
@@ -424,7 +434,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       regs_inc<120>();
       // ---- scale e^G dO, the image of dS, <dS, S>
       uint8_t* d_img = reinterpret_cast<uint8_t*>(ga.ds) + (long long)u * a.chunks * (DV * DK * 2) + at_s;
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 4, kPieces = DK == 128 ? 6 : DK / 16;   // (the others come to shared memory)
       auto put_inner = [&](int c, float s) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -489,7 +499,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
         for (int j = 0; j < DK / 16; ++j) {                    // 16 key channels: 8 words each of hi and lo
           uint32_t hi[8], lo[8];
-          if (inner && j + kAhead < DK / 16) fetch_state(j + kAhead);
+          if (inner && j + kAhead < kPieces) fetch_state(j + kAhead);
           tm_ld(la + kColSh + 8 * j, hi);
           tm_ld(la + kColSl + 8 * j, lo);
           tmem_wait_ld();
@@ -503,6 +513,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             for (int e = 0; e < 2; ++e)
               *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
           }
+          if (j == kPieces && i > 0 && ok) ok = wwait(bar(bSt), (i - 1) & 1, abort_flag, nullptr, 0);
           if (inner) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -512,10 +523,20 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 x[2 * f] = bf_lo(hi[4 * e + f]) + bf_lo(lo[4 * e + f]);
                 x[2 * f + 1] = bf_hi(hi[4 * e + f]) + bf_hi(lo[4 * e + f]);
               }
-              in = dot8(st[j % (kAhead + 1)][e], st[j % (kAhead + 1)][2 + e], x, in);
+              if (j < kPieces) {
+                in = dot8(st[j % (kAhead + 1)][e], st[j % (kAhead + 1)][2 + e], x, in);
+              } else {
+                const uint8_t* p = sm + kState + rb * 512 + (2 * (j - kPieces) + e) * 128 + r7 * 16;
+                in = dot8(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 128 * 64), x, in);
+              }
             }
           }
         }
+        if (DK == 128 && i > 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bStFree));
+        }
+        if (!ok) break;
         if (i > 0) put_inner(c + 1, in);
       }
       // the gradient of the initial state with that state
@@ -566,7 +587,6 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (mine) fetch_u(0);
         ok = ok && wwait(bar(bFx), ph, abort_flag, nullptr, 0);
         tc_fence_after();
-        if (tid == 384) bulk_wait_read();                      // the chunk before has left the buffer
         if (!(ok = bar_and(1, 128, ok))) break;
         uint8_t* im = f_img + (long long)c * (DV * L * 2);
         float* xp = ga.x + (img * kStrips + 2 * quad) * (2 * L);
@@ -600,8 +620,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 z[16 + k] = f0 * bf_lo(v0);
                 z[17 + k] = f1 * bf_lo(v1);
                 w[f] = pack_bf16(f0, f1);
-                *reinterpret_cast<uint16_t*>(sm + kOut + a0) = (uint16_t)(w[f] & 0xffff);
-                *reinterpret_cast<uint16_t*>(sm + kOut + a1) = (uint16_t)(w[f] >> 16);
+                // dV takes V's place (each thread its own channel), from where it is stored
+                *reinterpret_cast<uint16_t*>(sm + s * kStage + kV + a0) = (uint16_t)(w[f] & 0xffff);
+                *reinterpret_cast<uint16_t*>(sm + s * kStage + kV + a1) = (uint16_t)(w[f] >> 16);
               }
               *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -611,24 +632,25 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             xp[2 * L + (lane >> 4) * L + t] = 0.f;             // the warp's second strip of 16
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bEmpty + s));
         const int nt = len - c * L;
         if (nt >= L) {
           fence_proxy_async();
           bar_sync(1, 128);
           if (tid == 384) {
-            for (int j = 0; j < kHV; ++j) tma_store_4d(&tm_dv, s0 + kOut + j * kHalf, 64 * j, h, c * L, b);
+            for (int j = 0; j < kHV; ++j) tma_store_4d(&tm_dv, s0 + s * kStage + kV + j * kHalf, 64 * j, h, c * L, b);
             bulk_commit();
+            bulk_wait_read();
           }
         } else {
           bar_sync(1, 128);
           for (int j = tid - 384; j < nt * (DV / 8); j += 128) {
             const int t = j / (DV / 8), cc = j % (DV / 8);
             *reinterpret_cast<uint4*>(dvp + (long long)(c * L + t) * a.H * DV + cc * 8) =
-                *reinterpret_cast<const uint4*>(sm + kOut + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
+                *reinterpret_cast<const uint4*>(sm + s * kStage + kV + (cc >> 3) * kHalf + t * 128 + (((cc & 7) ^ (t & 7)) << 4));
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bEmpty + s));           // V, dV and the scalars have been read
       }
     }
   }
@@ -638,6 +660,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
       if ((n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
       else mbar_drain(bar(bTail), 0);
+    if (DK == 128 && loaded > 1) mbar_drain(bar(bSt), (loaded - 2) & 1);
   }
   tc_fence_before();
   __syncthreads();
