@@ -504,9 +504,11 @@ lte_status lte_gla_decode_step(int32_t B, int32_t H, int32_t dk, int32_t dv, int
  * contiguous); g (<= 0; -inf forgets everything), beta: fp32 [B,T,H]
  * contiguous; states: fp32 [B,H,dv,dk] contiguous.
  * lens (nullable): int32 [B] on the device, sequence b has the tokens
- * 0 .. lens[b] - 1 (clamped to [0, T]); later rows of the inputs are not read
- * and later rows of the outputs are left as they were; the state is the one
- * after the last token.
+ * 0 .. lens[b] - 1 (clamped to [0, T]); whatever later rows of the inputs hold
+ * does not matter and later rows of the outputs are left as they were; the state
+ * is the one after the last token.  A NaN or infinity in a token reaches the
+ * outputs of its head from the first token of its block of 64 on, and no other
+ * sequence or head.
  * Supported: dk, dv in {64, 128}, Hk dividing H, bf16 or fp32.
  * ------------------------------------------------------------------------- */
 typedef struct {
@@ -525,8 +527,9 @@ size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which);
  * state_out (may be the same buffer) are S before the first and after the last
  * token.  bf16: chunks of 64 tokens on tensor cores; the products behind the
  * state take fp32 operands as bf16 hi + lo pairs (relative error about 2^-17),
- * so the fp32 state keeps about 1e-5; o is rounded once to bf16.  fp32, and
- * bf16 with few tokens: token by token in fp32.  No atomics: results repeat
+ * so the fp32 state keeps about 1e-5; o is rounded once to bf16.  fp32, bf16
+ * with few tokens, and bf16 with strides that a tensor map cannot hold (2^40
+ * bytes): token by token in fp32.  No atomics: results repeat
  * bit by bit.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
                            const lte_strides* q_strides, const lte_strides* k_strides,
@@ -542,8 +545,9 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
  * dtype, contiguous; dg, dbeta fp32 [B,T,H]; dstate_in (nullable) fp32
  * [B,H,dv,dk].  Rows behind lens are left as they were.  dq, dk and dv are
  * rounded once behind bf16 products with fp32 sums; dg, dbeta and dstate_in
- * come from the hi + lo products of the forward.  bf16 only.  No atomics.
- * Workspace: lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD). */
+ * come from the hi + lo products of the forward.  No atomics.
+ * Workspace: lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD).  Errors: as above;
+ * UNSUPPORTED also for fp32 and for strides that a tensor map cannot hold. */
 lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
                             const lte_strides* q_strides, const lte_strides* k_strides,
                             const lte_strides* v_strides, const float* g, const float* beta,

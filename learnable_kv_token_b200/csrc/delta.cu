@@ -30,7 +30,9 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
 // ------------------------------------------------------------------ recurrent
 // 8 lanes hold one row of S in registers (lane l: channels 4 l + 32 j .. + 3),
 // 16 rows per CTA of 128 threads; blocks of kTok tokens of q, k and v are
-// staged in shared memory as fp32.
+// staged in shared memory as fp32.  Bound by the latency of a token's two sums:
+// 0.34 us a token for up to 148 CTAs (18 heads of 128 value channels), 0.5 for 512,
+// 3.1 for 4096.
 constexpr int kTok = 16, kRecRows = 16;
 
 struct RecArgs {
@@ -122,7 +124,9 @@ __global__ void __launch_bounds__(128) delta_recurrent_kernel(const RecArgs a) {
 // their loads are all issued first, then the two dot products of each row
 // (S k and S q) are summed over the lanes together.  With S q and k.q known,
 //   o = scale (a S q + u (k.q)),
-// so the output needs no second pass over the new state.
+// so the output needs no second pass over the new state.  8.9 us for 512 states
+// of 128 x 128 in fp32: 67 MB, the measured copy bandwidth or above (part of a
+// state that was written last may still be in L2).
 template <typename T, int DK, int ROWS>
 __global__ void __launch_bounds__(128)
 delta_step_kernel(int H, int Hk, int dv, float scale, const T* __restrict__ q, const T* __restrict__ k,

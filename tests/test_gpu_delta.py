@@ -174,6 +174,39 @@ def test_prefill_continues(layer):
     assert rel(torch.cat(parts, 1), f64(o)) <= 2 * BF16_TOL
 
 
+def test_bad_values_stay_in_their_head(layer):
+    """A NaN in one head of one sequence reaches that head from its block of 64 tokens on; every other
+    head and sequence, and the blocks before, are as without it, forwards and backwards."""
+    x = inputs(42, 2, 200, 4, 4, 128, 128)
+    names = ("q", "k", "v", "g", "beta")
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    clean = layer.delta_prefill(*(x[n] for n in names), state=x["state"])
+    grads = layer.delta_backward(*(x[n] for n in names), do, state=x["state"])
+    x["v"][1, 100, 2, 5] = float("nan")
+    o, S = layer.delta_prefill(*(x[n] for n in names), state=x["state"])
+    bad = layer.delta_backward(*(x[n] for n in names), do, state=x["state"])
+    assert torch.isnan(o[1, 100, 2]).any() and torch.isnan(S[1, 2]).any()
+    assert torch.equal(o[1, :64, 2], clean[0][1, :64, 2])
+    others = [(0, h) for h in range(4)] + [(1, h) for h in (0, 1, 3)]
+    for i, h in others:
+        assert torch.equal(o[i, :, h], clean[0][i, :, h]) and torch.equal(S[i, h], clean[1][i, h])
+        for a, b in zip(bad[:5], grads[:5]):
+            assert torch.equal(a[i, :, h], b[i, :, h])
+        assert torch.equal(bad[5][i, h], grads[5][i, h])
+
+
+def test_views_with_odd_strides_of_one(layer):
+    """A single token as a view whose unused strides are no multiples of 16 bytes."""
+    x = inputs(43, 1, 1, 2, 2, 64, 64)
+    wide = torch.zeros(1, 3, 2, 67, dtype=torch.bfloat16, device="cuda")
+    odd = wide.as_strided((1, 1, 2, 64), (7, 5, 64, 1))
+    odd.copy_(x["q"])
+    assert not odd.stride(1) % 8 == 0
+    a = layer.delta_prefill(odd, x["k"], x["v"], x["g"], x["beta"], state=x["state"])
+    b = layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_prefill_repeats(layer):
     x = inputs(5, 3, 190, 4, 2, 64, 128, lens=[190, 3, 100])
     a, b = (layer.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], state=x["state"], lens=x["lens"])
@@ -234,9 +267,12 @@ def test_backward_extreme_gates(layer, kind):
 
 def test_backward_by_differences(layer):
     """The gradient of every input along a random direction against a central difference of the
-    forward pass.  The forward's outputs are off by 2^-8 |o| per entry at random, so the difference
-    over 2 h |direction| = 0.2 of the inputs' size carries about 2^-8 |do| |o| / (0.1 sqrt(n)) ..., far
-    below the 5 % of the slope's own size (norm of the gradient times that of the step) allowed."""
+    forward pass, with steps of h = 0.05 of the input's norm along the gradient.
+    Slope: 2 h |gradient| |x|, which for v (o is linear in it) is near 0.1 |do| |o|.  Rounding: the n = 8960
+    entries of o are off by at most 2^-8 |o_i|, independently in the two losses: sqrt(2) 2^-8 |do| |o| /
+    sqrt(n) = 6e-5 |do| |o|, 6e-4 of that slope, and 6e-3 where an input moves the loss a tenth as much.
+    Curvature: h^2 / 6 = 4e-4 times a ratio of derivatives of order one.  The gradient itself: 4e-3.
+    Together below 2 %; 5 % is allowed."""
     x = inputs(200, 1, 70, 2, 1, 64, 64)
     g = torch.Generator().manual_seed(1)
     do = torch.randn(x["v"].shape, generator=g).bfloat16().cuda()
