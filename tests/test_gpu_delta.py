@@ -372,6 +372,45 @@ def test_backward_in_a_graph(layer):
         assert torch.equal(a, b)
 
 
+def test_segments_in_a_graph_over_their_own_state(layer):
+    """A long prompt of few heads, cut into segments, captured with the state updated in its place and
+    replayed beside an eager call of the same kind."""
+    x = inputs(62, 1, 3000, 2, 2, 128, 128)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    want = layer.delta_prefill(*args, state=x["state"])
+    st = x["state"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, S = layer.delta_prefill(*args, state=st, state_out=st)
+    assert S is st
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        st.copy_(x["state"])
+        graph.replay()
+        other = layer.delta_prefill(*args, state=x["state"], stream=side)
+    torch.cuda.synchronize()
+    for a, b in ((o, want[0]), (st, want[1]), (other[0], want[0]), (other[1], want[1])):
+        assert torch.equal(a, b)
+
+
+def test_gradients_on_two_streams_at_once(layer):
+    """Two gradient passes that run side by side give what each gives alone."""
+    names = ("q", "k", "v", "g", "beta")
+    xs = [inputs(63 + i, 2, 300 + 90 * i, 4, 2, 64, 128, lens=[300, 77]) for i in range(2)]
+    dos = [torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(4)).bfloat16().cuda() for x in xs]
+    call = lambda x, do, **kw: layer.delta_backward(*(x[n] for n in names), do, state=x["state"], lens=x["lens"], **kw)  # noqa: E731
+    want = [call(x, do) for x, do in zip(xs, dos)]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = [call(x, do, stream=s) for x, do, s in zip(xs, dos, sides)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        for i, j in zip(a, b):
+            assert torch.equal(i, j)
+
+
 def test_offsets_past_32_bits(layer):
     """A sequence whose tensors have over 2^31 elements: its last tokens, and the state, equal those of
     the same tokens in a call of their own behind the state of the others."""

@@ -124,6 +124,34 @@ def test_position_outside_the_table(layer):
         assert torch.isfinite(y[0, [0, 3]]).all()
 
 
+def test_in_a_graph_and_on_another_stream(layer):
+    """Both directions captured, replayed with new rows and positions, beside a call on another stream."""
+    g = torch.Generator().manual_seed(9)
+    randn = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    xs = [(randn(3, 37, 4, 64), randn(3, 37, 2, 64), randn(3, 37, 4, 64), randn(3, 37, 2, 64),
+           torch.randint(0, 64, (3, 37), generator=g, dtype=torch.int32).cuda()) for _ in range(2)]
+    w = torch.rand(2, 64, generator=g).cuda() + 0.5
+    norm = layer.QKNorm("rms", wq=w[0], wk=w[1], rot_dim=32, table=layer.rope_table(64, 32))
+
+    def both(q, k, dq, dk, pos, **kw):
+        return (*layer.qk_norm_rope(q, k, norm, positions=pos, **kw),
+                *layer.qk_norm_rope_backward(q, k, dq, dk, norm, positions=pos, **kw))
+    want = [both(*x) for x in xs]
+    buf = [t.clone() for t in xs[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(*buf)
+    side = torch.cuda.Stream()
+    for t, new in zip(buf, xs[1]):
+        t.copy_(new)
+    side.wait_stream(torch.cuda.current_stream())
+    graph.replay()
+    other = both(*xs[0], stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip((*got, *other), (*want[1], *want[0])):
+        assert torch.equal(a, b)
+
+
 def test_refusals(layer):
     q, k, p, pos, ang = setup(layer, 11, 1, 4, 2, 1, 64, torch.float32, "rms", 32, False, 0, False)
     from dataclasses import replace
