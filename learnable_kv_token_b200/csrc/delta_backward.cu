@@ -400,7 +400,7 @@ cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStre
   c.qs = a.qs; c.ks = a.ks; c.vs = a.vs; c.g = a.g; c.beta = a.beta; c.lens = a.lens; c.s_in = a.s_in;
   c.rec = ws + w.rec; c.s0 = (uint32_t*)(ws + w.s0); c.u = (uint32_t*)(ws + w.u);
   c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = (d->T + delta::L - 1) / delta::L;
-  c.scale = d->scale; c.segs = 1; c.seg_chunks = c.chunks;
+  c.scale = d->scale; c.segs = c.pieces = 1; c.seg_chunks = c.chunks;
   n.dO = (const __nv_bfloat16*)ga.dO; n.dos = ga.dos; n.ds_out = ga.ds_out; n.ds_in = ga.ds_in;
   n.dq = (__nv_bfloat16*)ga.dq; n.dk = (__nv_bfloat16*)ga.dk; n.dv = (__nv_bfloat16*)ga.dv;
   n.dg = ga.dg; n.db = ga.db; n.ds = (uint32_t*)(ws + w.ds); n.fimg = (uint32_t*)(ws + w.f);

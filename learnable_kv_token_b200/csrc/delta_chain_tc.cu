@@ -22,8 +22,8 @@
 // (e^{G_L} S, U for O); S comes and goes in two halves of its columns, so a pass
 // over one half runs beside the product on the other; products with T and A
 // leave out the columns above the diagonal.  64 chunks of 512 heads of 128
-// channels: 715 us, four waves of CTAs (one to an SM), 4400 cycles a chunk, 1300
-// of them products; 3.0 GB moved, 4.2 TB/s, which two stages of loads cover.
+// channels: 653 us (seven waves of half sequences), 4400 cycles a chunk, 1300 of
+// them products; 3.0 GB moved, 4.6 TB/s, which two stages of loads cover.
 //
 // Long sequences of few heads are cut into segments of chunks, one CTA each.  A
 // row of S goes through a segment by an affine map s -> s X + n that is the same
@@ -31,6 +31,12 @@
 // from a zero state) and X (the chain from the identity with no values); a small
 // kernel carries the states from segment to segment, and a second pass runs every
 // segment from its state for O.  Twice the work on many times the SMs.
+//
+// With more heads than SMs, sequences are cut into pieces that follow one another,
+// one CTA each, so that the last wave of CTAs is short.  A piece starts from the
+// state that the one before left in s_out.  CTAs draw their pieces in order, all
+// first ones before all second ones: what a CTA waits for was drawn before by one
+// that is running or done, so the wait ends, and as a rule is over already.
 //
 // Rows of the last chunk behind the sequence's length are set to zero in shared
 // memory before use, so what lies there (NaN, another sequence) does not enter.
@@ -61,7 +67,7 @@ constexpr uint32_t kColS = 0, kColPR = 256, kColVU = 320, kColUH = 384, kColUL =
 // what a chain leaves besides the state
 enum : int { kImages = 0, kO = 1, kStateOnly = 2 };
 
-template <int DK, int DV, int KIND>
+template <int DK, int DV, int KIND, bool PIECES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -70,20 +76,12 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
   constexpr int kHK = DK / 64, kHV = DV / 64;                // 64-channel halves
   constexpr bool OUT = KIND == kO;
-  // the unit's segment: for kStateOnly first n of segments 0 .. G - 2, then X of 1 .. G - 2
-  const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs, u = blockIdx.x / per, j0 = blockIdx.x % per;
-  const bool hom = KIND == kStateOnly && j0 >= a.segs - 1;
-  const int seg = hom ? j0 - a.segs + 2 : j0;
-  const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t s0 = sa(sm), bars = s0 + kBars;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
+  volatile int* ticket = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return bars + 8 * i; };
-  // chunks cb .. cb + n_chunks - 1 of the sequence; `len` tokens from chunk cb on
-  const int cb = seg * a.seg_chunks;
-  const int len = max(seq_len(a.lens, b, a.T) - cb * L, 0);
-  const int n_chunks = a.segs == 1 ? (len + L - 1) / L : min((len + L - 1) / L, a.seg_chunks);
   constexpr int kRecBytes = rec_bytes(KIND == kImages);
   constexpr bool kRecHasALo = KIND == kImages;
 
@@ -94,6 +92,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 13 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
+    if (PIECES) *ticket = atomicAdd(a.turn, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   write_identity(sm + kIdent, kThreads);
@@ -107,6 +106,24 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the unit's segment: for kStateOnly first n of segments 0 .. G - 2, then X of 1 .. G - 2;
+  // or its piece, all first pieces before all second ones
+  auto unit_seg = [&](int& u, int& seg) {
+    const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
+    const int units = PIECES ? gridDim.x / a.pieces : 1, i = PIECES ? *ticket : (int)blockIdx.x;
+    u = PIECES ? i % units : i / per;
+    seg = PIECES ? i / units : i % per;
+    const bool hom = KIND == kStateOnly && seg >= a.segs - 1;
+    if (hom) seg -= a.segs - 2;
+    return hom;
+  };
+  int u, seg;
+  const bool hom = unit_seg(u, seg);
+  const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
+  // chunks cb .. cb + n_chunks - 1 of the sequence; `len` tokens from chunk cb on
+  const int cb = seg * a.seg_chunks;
+  const int len = max(seq_len(a.lens, b, a.T) - cb * L, 0);
+  const int n_chunks = min((len + L - 1) / L, a.seg_chunks);
   bool ok = true;
   int loaded = 0;                                            // chunks requested (producer)
   bool issued = false;                                       // MMAs issued (MMA warp)
@@ -251,28 +268,38 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     constexpr int QC = DK / 4;                                 // S columns per thread and half
     const int row = (warp & 3) * 32 + lane, hc = warp >> 2;    // value channel = TMEM lane; which columns
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // where this row of the state comes from and goes to (NULL: zeros; nowhere)
-    const int rows = hom ? DK : DV, r_in = row < rows ? row : 0;
-    const bool joined = KIND == kO && a.segs > 1;              // (s_out may be s_in: that was read by the join)
-    const float* src = joined ? a.seg_s + seg * DV * DK : seg == 0 ? a.s_in : nullptr;
-    float* dst = KIND == kStateOnly ? (hom ? a.seg_x + ((long long)u * (a.segs - 2) + seg - 1) * DK * DK
-                                           : a.seg_n + ((long long)u * (a.segs - 1) + seg) * DV * DK)
-                 : seg == a.segs - 1 && a.s_out != nullptr ? a.s_out + (long long)u * DV * DK : nullptr;
-    if (src != nullptr) src += (long long)u * (joined ? a.segs : 1) * DV * DK + r_in * DK;
-    if (dst != nullptr) dst += r_in * DK;
-    auto first = [&](int col) {                                // four columns of the initial state
-      if (hom)
-        return make_float4(col == row ? 1.f : 0.f, col + 1 == row ? 1.f : 0.f, col + 2 == row ? 1.f : 0.f,
-                           col + 3 == row ? 1.f : 0.f);
-      return src != nullptr && row < rows ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
+    const int rows = hom ? DK : DV;
+    {                                                          // the state, while the first chunk loads
+      const bool joined = KIND == kO && a.segs > 1;            // (s_out may be s_in: that was read by the join)
+      const float* src = joined ? a.seg_s + seg * DV * DK : seg == 0 ? a.s_in : PIECES ? a.s_out : nullptr;
+      if (PIECES && seg > 0 && n_chunks > 0) ok = piece_ready(a.done + u, seg, abort_flag);
+      if (src != nullptr) src += (long long)u * (joined ? a.segs : 1) * DV * DK + row * DK;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
+        uint32_t r[QC];
+#pragma unroll
+        for (int e = 0; e < QC / 4; ++e) {
+          const int col = c0 + 4 * e;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (hom) v = make_float4(col == row, col + 1 == row, col + 2 == row, col + 3 == row);
+          else if (src != nullptr && row < DV) v = __ldcg(reinterpret_cast<const float4*>(src + col));
+          r[4 * e] = __float_as_uint(v.x);
+          r[4 * e + 1] = __float_as_uint(v.y);
+          r[4 * e + 2] = __float_as_uint(v.z);
+          r[4 * e + 3] = __float_as_uint(v.w);
+        }
+        tm_st(la + kColS + c0, r);
+      }
+      tmem_wait_st();
+    }
     auto arrive = [&](int i) {                                 // this warp's TMEM writes are done
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(i));
     };
-    for (int c = 0; c < n_chunks; ++c) {
+    for (int c = 0; ok && c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
       if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
@@ -282,23 +309,14 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
-        if (c > 0) {
-          if (ok) ok = wwait(bar(bS + p), (c - 1) & 1, abort_flag, nullptr, 0);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t r[QC];
-          tm_ld(la + kColS + c0, r);
-          tmem_wait_ld();
+        if (c > 0 && ok) ok = wwait(bar(bS + p), (c - 1) & 1, abort_flag, nullptr, 0);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[QC];
+        tm_ld(la + kColS + c0, r);
+        tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < QC / 2; ++e) S[p][e] = pair_of(r + 2 * e);
-        } else {
-#pragma unroll
-          for (int e = 0; e < QC / 4; ++e) {
-            const float4 v = first(c0 + 4 * e);
-            S[p][2 * e] = f2(v.x, v.y);
-            S[p][2 * e + 1] = f2(v.z, v.w);
-          }
-        }
+        for (int e = 0; e < QC / 2; ++e) S[p][e] = pair_of(r + 2 * e);
         uint32_t hi[QC / 2], lo[QC / 2];
         split_pairs(S[p], hi, lo);
         tm_st(la + kColSh + c0 / 2, hi);
@@ -386,7 +404,14 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       ok = wwait(bar(bS), (n_chunks - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n_chunks - 1) & 1, abort_flag, nullptr, 0);
       tc_fence_after();
     }
+    int ul, segl;
+    unit_seg(ul, segl);
+    float* dst = KIND == kStateOnly ? (hom ? a.seg_x + ((long long)ul * (a.segs - 2) + segl - 1) * DK * DK
+                                           : a.seg_n + ((long long)ul * (a.segs - 1) + segl) * DV * DK)
+                 : a.s_out != nullptr && (PIECES ? segl == 0 || n_chunks > 0 : segl == a.segs - 1)
+                     ? a.s_out + (long long)ul * DV * DK : nullptr;
     if (dst != nullptr) {
+      dst += row * DK;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
@@ -398,25 +423,24 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           for (int e = 0; e < QC / 4; ++e) {
             float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-            if (n_chunks == 0) v = first(c0 + 4 * e);
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
             *reinterpret_cast<float4*>(dst + c0 + 4 * e) = v;
           }
         }
       }
+      if (PIECES) piece_done(a.done + ul, segl, 2, 256);
     }
   } else if (warp < 12) {
     // ==================================================== O, or the images
     regs_inc<144>();
     const int quad = warp - 8, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    __nv_bfloat16* op = a.o + b * a.os.b + h * a.os.h;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
       ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0);
       if (!OUT && !ok) break;                                  // (O: the warps meet at the vote below)
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
-      const long long img = (long long)u * a.chunks + cb + c;
+      const long long img = KIND == kImages ? (long long)u * a.chunks + cb + c : 0;
       if (KIND == kStateOnly) {
         if (lane == 0) mbar_arrive(bar(bEmpty + s));
       } else if (OUT) {
@@ -470,11 +494,18 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           fence_proxy_async();
           bar_sync(1, 128);
           if (tid == 256) {
+            int u, seg;                                        // (not kept in registers over the chunks)
+            unit_seg(u, seg);
+            const int b = u / a.H, h = u % a.H, cb = seg * a.seg_chunks;
             for (int i = 0; i < kHV; ++i) tma_store_4d(&tm_o, s0 + kOut + i * kHalf, 64 * i, h, (cb + c) * L, b);
             bulk_commit();
           }
         } else {
           bar_sync(1, 128);
+          int u, seg;
+          unit_seg(u, seg);
+          const int cb = seg * a.seg_chunks;
+          __nv_bfloat16* op = a.o + (u / a.H) * a.os.b + (u % a.H) * a.os.h;
           for (int i = tid - 256; i < n * (DV / 8); i += 128) {
             const int t = i / (DV / 8), cc = i % (DV / 8);
             *reinterpret_cast<uint4*>(op + (long long)((cb + c) * L + t) * a.os.t + cc * 8) =
@@ -526,7 +557,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
     }
   }
-  if (OUT && tid == 256) bulk_wait_all();                      // output stores complete before exit
+  if (OUT && tid == 256) bulk_wait_read();                     // output stores have left shared memory
   // copies in flight land before exit (only after a wait gave up)
   if (warp == 12 && *abort_flag) {
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
@@ -601,12 +632,12 @@ delta_join_kernel(const ChunkArgs a) {
   }
 }
 
-template <int DK, int DV, int KIND>
+template <int DK, int DV, int KIND, bool PIECES = false>
 cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, KIND, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
-  delta_chain_tc_kernel<DK, DV, KIND><<<(unsigned)(B * a.H * per), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
+  delta_chain_tc_kernel<DK, DV, KIND, PIECES><<<(unsigned)(B * a.H * per * a.pieces), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
   return cudaGetLastError();
 }
 template <int DK, int DV>
@@ -620,7 +651,7 @@ cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t st
     if (f != cudaSuccess) return f;
     delta_join_kernel<DK><<<(unsigned)(B * a.H * (DV / 16)), 256, smem, stream>>>(a);
   }
-  return launch<DK, DV, kO>(m, a, B, stream);
+  return a.pieces > 1 ? launch<DK, DV, kO, true>(m, a, B, stream) : launch<DK, DV, kO>(m, a, B, stream);
 }
 
 }  // namespace chaintc
@@ -633,6 +664,24 @@ cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream
     return cudaErrorNotSupported;
   if (dk == 128) return a.dv == 128 ? chaintc::run<128, 128>(m, a, B, stream) : chaintc::run<128, 64>(m, a, B, stream);
   return a.dv == 128 ? chaintc::run<64, 128>(m, a, B, stream) : chaintc::run<64, 64>(m, a, B, stream);
+}
+
+// Pieces of the sequences, in chunk steps (2.6 us each): units over 148 come in
+// waves, and the last wave is the shorter the shorter its CTAs.  A CTA costs three
+// steps beside its chunks, and one with a state to hand over four and a half.  64
+// chunks: 512 heads 690 us whole, 653 in two pieces, 702 in three; 160 heads 339,
+// 275, 258, and 259 in four.  16 chunks of 512 heads: 193 whole, 220 in two.
+int chain_pieces(long long units, int chunks) {
+  int best = 1;
+  double least = (double)((units + 147) / 148) * (chunks + 3);
+  for (int p = 2; p <= (units > 148 ? 8 : 1) && p <= chunks; ++p) {
+    const double t = (double)((units * p + 147) / 148) * ((chunks + p - 1) / p + 4.5);
+    if (t < 0.98 * least) {
+      least = t;
+      best = p;
+    }
+  }
+  return best;
 }
 
 // Segments of a sequence, by the time of both passes in chunk steps (2.3 us

@@ -94,6 +94,25 @@ __device__ __forceinline__ void zero_rows(uint8_t* half, int r0, int lane) {
   for (int i = lane; i < (L - r0) * 8; i += 32) *reinterpret_cast<uint4*>(half + r0 * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// Pieces of a sequence (chain_pieces): the number of a unit's pieces that are done.
+// Every lane of a warp waits (half as long as the waits behind this one may take),
+// so each has acquired what was written before the number.
+__device__ __forceinline__ bool piece_ready(const int* done, int want, volatile int* abort_flag) {
+  const unsigned long long t0 = gtime();
+  int v;
+  do {
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+  } while (v < want && *abort_flag == 0 && gtime() - t0 < kWaitNs / 2);
+  if (v < want) *abort_flag = 1;
+  return __all_sync(0xffffffffu, v >= want);
+}
+// by the warps that wrote the state (`threads` threads, all of which get here)
+__device__ __forceinline__ void piece_done(int* done, int seg, int id, int threads) {
+  __threadfence();
+  bar_sync(id, threads);
+  if (threadIdx.x == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(done), "r"(seg + 1) : "memory");
+}
+
 // [channels, heads, T, B] with the tensor's strides; boxes of 64 tokens x 64 channels
 inline bool map_of(CUtensorMap* m, const void* p, int D, int heads, int T, int B, Strides4 s) {
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};

@@ -101,6 +101,9 @@ struct ChunkArgs {
   // segments (forward only; segs = 1: the sequence in one piece): chunks of each,
   // n [units][segs - 1][dv][dk], X [units][segs - 2][dk][dk], states [units][segs][dv][dk]
   int segs, seg_chunks;
+  // or pieces that follow one another (pieces = 1: one; seg_chunks: chunks of each): the
+  // next piece's number and, per unit, its pieces that are done (prepare sets all to zero)
+  int pieces, *turn, *done;
   float *seg_n, *seg_x, *seg_s;
 };
 
@@ -123,6 +126,7 @@ cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t s
 // delta_chain_tc.cu: the chain of states with O; with s0 and u, writes their images instead of O
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
 int chain_segments(long long units, int chunks);
+int chain_pieces(long long units, int chunks);
 // delta_back_tc.cu: the backward chain
 cudaError_t back_chain(const GradArgs& a, int B, int dk, cudaStream_t stream);
 

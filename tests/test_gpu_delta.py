@@ -394,6 +394,20 @@ def test_segments_in_a_graph_over_their_own_state(layer):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [1500, 4100])
+def test_more_heads_than_processors(layer, T):
+    """160 states, whose sequences are cut into pieces that hand the state on: as the same sequences
+    in two calls of 80, which are not cut, bit by bit; the state in its own place, lengths from none
+    to all with the ends of pieces among them."""
+    x = inputs(66, 40, T, 4, 2, 64, 64, lens=[T, 0, 1, 64, T // 2, 768, 769, T - 1] * 5)
+    names = ("q", "k", "v", "g", "beta")
+    st = x["state"].clone()
+    o, S = layer.delta_prefill(*(x[n] for n in names), state=st, state_out=st, lens=x["lens"])
+    for half in (slice(0, 20), slice(20, 40)):
+        o1, S1 = layer.delta_prefill(*(x[n][half] for n in names), state=x["state"][half], lens=x["lens"][half])
+        assert torch.equal(o[half], o1) and torch.equal(S[half], S1)
+
+
 def test_gradients_on_two_streams_at_once(layer):
     """Two gradient passes that run side by side give what each gives alone."""
     names = ("q", "k", "v", "g", "beta")
