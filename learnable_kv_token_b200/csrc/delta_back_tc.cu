@@ -18,7 +18,8 @@
 // issues the MMAs.  Registers: 112 for the chain, 104 for the sums, 48 for the rest;
 // one spilled costs a trip to L2.
 // The products of dO with Q run while the chain warps turn F, so the chain of a
-// chunk is P -> dU -> F -> dS as in the forward pass.  64 chunks of 128 heads of
+// chunk is P -> dU -> F -> dS as in the forward pass.  Sequences of more heads than
+// SMs are cut into pieces as there; dS goes from one to the next by `hand`.  64 chunks of 128 heads of
 // 128 channels (one wave): 495 us, 7.7 us a chunk; 160 KB of images and dV
 // per chunk beside 97 KB of inputs (2.1 GB, 4.3 TB/s) make memory latency the bound.
 #include <math.h>
@@ -82,7 +83,7 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
   return r;
 }
 
-template <int DK, int DV>
+template <int DK, int DV, bool PIECES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_v,
@@ -91,13 +92,12 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const ChunkArgs& a = ga.f;
   constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
   constexpr int kHK = DK / 64, kHV = DV / 64, kStrips = DV / 16;
-  const int u = blockIdx.x, b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t s0 = sa(sm), bars = s0 + kBars;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
+  volatile int* ticket = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return bars + 8 * i; };
-  const int len = seq_len(a.lens, b, a.T), n = (len + L - 1) / L;
 
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
@@ -106,6 +106,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
+    if (PIECES) *ticket = atomicAdd(a.turn + 1, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   write_identity(sm + kIdent, kThreads);
@@ -119,6 +120,12 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the unit, and its chunks cb .. cb + n - 1 (pieces from the last to the first)
+  const int units = PIECES ? gridDim.x / a.pieces : 1, u = PIECES ? *ticket % units : (int)blockIdx.x;
+  const int piece = PIECES ? *ticket / units : 0, cb = PIECES ? (a.pieces - 1 - piece) * a.seg_chunks : 0;
+  const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
+  const int len = seq_len(a.lens, b, a.T);
+  const int n = PIECES ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
   bool ok = true, issued = false;
   int loaded = 0;
 
@@ -127,7 +134,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // ================================================================ loads
     const uint8_t* recs = a.rec + (long long)u * a.chunks * rec_bytes(true);
     for (int i = 0; i < n; ++i) {
-      const int s = i & 1, c = n - 1 - i;
+      const int s = i & 1, c = cb + n - 1 - i;
       if (i >= 2 && !(ok = wwait(bar(bEmpty + s), ((i >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
       const uint32_t d = s0 + s * kStage;
       const bool tail = c * L + L > len;                       // the first one to come
@@ -280,11 +287,28 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(j));
     };
-    auto first = [&](int col) {
-      return ga.ds_out != nullptr && row < DV ? *reinterpret_cast<const float4*>(ga.ds_out + srow + col)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    for (int i = 0; i < n; ++i) {
+    {                                                          // the gradient behind, while the last chunk loads
+      const bool later = PIECES && n > 0 && (cb + n) * L < len;
+      if (later) ok = piece_ready(a.done + units + u, piece, abort_flag);
+      const float* src = later ? ga.hand : ga.ds_out;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c0 = QC * (2 * p + hc);
+        uint32_t r[QC];
+#pragma unroll
+        for (int e = 0; e < QC / 4; ++e) {
+          const float4 v = src != nullptr && row < DV ? __ldcg(reinterpret_cast<const float4*>(src + srow + c0 + 4 * e))
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          r[4 * e] = __float_as_uint(v.x);
+          r[4 * e + 1] = __float_as_uint(v.y);
+          r[4 * e + 2] = __float_as_uint(v.z);
+          r[4 * e + 3] = __float_as_uint(v.w);
+        }
+        tm_st(la + kColS + c0, r);
+      }
+      tmem_wait_st();
+    }
+    for (int i = 0; ok && i < n; ++i) {
       const int s = i & 1, ph = i & 1;
       if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
@@ -296,22 +320,15 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
         uint64_t S[QC / 2];
-        if (i > 0) {
-          if (ok) ok = wwait(bar(bS + p), (i - 1) & 1, abort_flag, nullptr, 0);
-          if (!ok) break;
-          tc_fence_after();
+        if (i > 0 && ok) ok = wwait(bar(bS + p), (i - 1) & 1, abort_flag, nullptr, 0);
+        if (!ok) break;
+        tc_fence_after();
+        {
           uint32_t r[QC];
           tm_ld(la + kColS + c0, r);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < QC / 2; ++e) S[e] = pair_of(r + 2 * e);
-        } else {
-#pragma unroll
-          for (int e = 0; e < QC / 4; ++e) {
-            const float4 v = first(c0 + 4 * e);
-            S[2 * e] = f2(v.x, v.y);
-            S[2 * e + 1] = f2(v.z, v.w);
-          }
         }
         {
           uint32_t hi[QC / 2], lo[QC / 2];
@@ -404,7 +421,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
       tc_fence_after();
     }
-    if (ga.ds_in != nullptr) {
+    float* dst = cb == 0 ? ga.ds_in : n > 0 ? ga.hand : nullptr;
+    if (dst != nullptr) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
@@ -416,12 +434,12 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int e = 0; e < QC / 4; ++e) {
             float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-            if (n == 0) v = first(c0 + 4 * e);
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
-            *reinterpret_cast<float4*>(ga.ds_in + srow + c0 + 4 * e) = v;
+            *reinterpret_cast<float4*>(dst + srow + c0 + 4 * e) = v;
           }
         }
       }
+      if (PIECES && cb > 0) piece_done(a.done + units + u, piece, 2, 256);
     }
   } else if (warp < 16) {
     // ================================================= the two output groups
@@ -447,7 +465,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
       };
       for (int i = 0; i < n; ++i) {
-        const int s = i & 1, ph = i & 1, c = n - 1 - i;
+        const int s = i & 1, ph = i & 1, c = cb + n - 1 - i;
         if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
         const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
         // the state of the chunk behind, hi and lo, 16 key channels at a time, asked for
@@ -541,7 +559,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!ok) break;
         if (i > 0) put_inner(c + 1, in);
       }
-      // the gradient of the initial state with that state
+      // the gradient of the (piece's) initial state with that state
       if (ok && n > 0 && wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) &&
           wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0)) {
         tc_fence_after();
@@ -557,11 +575,20 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               float x[8];
 #pragma unroll
               for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(r[8 * e + f]);
-              in = dot8(load_once(s_img + (2 * j + e) * 128), load_once(s_img + DV * DK * 2 + (2 * j + e) * 128), x, in);
+              if (PIECES && cb > 0)                            // as the next chunk of the piece would see it
+#pragma unroll
+                for (int f = 0; f < 8; f += 2) {
+                  uint32_t hi, lo;
+                  split_pair(f2(x[f], x[f + 1]), hi, lo);
+                  x[f] = bf_lo(hi) + bf_lo(lo);
+                  x[f + 1] = bf_hi(hi) + bf_hi(lo);
+                }
+              const uint8_t* p = s_img + (long long)cb * (DV * DK * 4) + (2 * j + e) * 128;
+              in = dot8(load_once(p), load_once(p + DV * DK * 2), x, in);
             }
           }
         }
-        put_inner(0, in);
+        put_inner(cb, in);
       }
     } else {
       regs_dec<88>();
@@ -572,7 +599,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const uint32_t colv = (uint32_t)(row >> 6) * kHalf + (row & 7) * 2;
       const int cv = (row & 63) >> 3;
       for (int i = 0; i < n; ++i) {
-        const int s = i & 1, ph = i & 1, c = n - 1 - i;
+        const int s = i & 1, ph = i & 1, c = cb + n - 1 - i;
         const long long img = (long long)u * a.chunks + c;
         // (a warp whose wait gave up still meets the others at the vote below)
         ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
@@ -656,11 +683,11 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
     }
   }
-  if (tid == 384) bulk_wait_all();                             // output stores complete before exit
+  if (tid == 384) bulk_wait_read();                            // output stores have left shared memory
   // copies in flight land before exit (only after a wait gave up)
   if (warp == 16 && *abort_flag) {
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
-      if ((n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
+      if ((cb + n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
       else mbar_drain(bar(bTail), 0);
     if (DK == 128 && loaded > 1) mbar_drain(bar(bSt), (loaded - 2) & 1);
   }
@@ -670,12 +697,16 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
+template <int DK, int DV, bool PIECES>
+cudaError_t launch_as(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  delta_back_tc_kernel<DK, DV, PIECES><<<(unsigned)(B * a.f.H * a.f.pieces), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
+  return cudaGetLastError();
+}
 template <int DK, int DV>
 cudaError_t launch(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  delta_back_tc_kernel<DK, DV><<<(unsigned)(B * a.f.H), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
-  return cudaGetLastError();
+  return a.f.pieces > 1 ? launch_as<DK, DV, true>(m, a, B, stream) : launch_as<DK, DV, false>(m, a, B, stream);
 }
 
 }  // namespace backtc

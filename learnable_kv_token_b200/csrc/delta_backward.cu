@@ -370,9 +370,12 @@ cudaError_t grad(const GradArgs& a, int B, cudaStream_t stream) {
 
 // workspace: records, then the images and partial sums, each rounded up to 256 bytes
 struct BackwardLayout {
-  size_t rec, s0, u, f, ds, x, inner, total;
+  size_t rec, s0, u, f, ds, x, inner, hand, turn, total;
+  int pieces;
   explicit BackwardLayout(const lte_gdr_dims* d) {
-    const size_t n = (size_t)d->B * d->H * ((d->T + L - 1) / L), dv = d->dv, dk = d->dk;
+    const size_t units = (size_t)d->B * d->H, n = units * ((d->T + L - 1) / L), dv = d->dv, dk = d->dk;
+    // (a chunk takes both chains 10 us together: a CTA's start and end cost less of one)
+    pieces = chain_pieces((long long)units, (d->T + L - 1) / L, 1.5, 2);
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += (bytes + 255) & ~(size_t)255; return r; };
     rec = take(n * rec_bytes(true));
@@ -382,6 +385,8 @@ struct BackwardLayout {
     ds = take(n * dv * dk * 2);
     x = take(n * (dv / 16) * 2 * L * 4);
     inner = take(n * (dv / 16) * 4);
+    hand = take(pieces > 1 ? units * dv * dk * 4 : 0);
+    turn = take(pieces > 1 ? piece_bytes(units) : 0);
     total = at;
   }
 };
@@ -400,7 +405,9 @@ cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStre
   c.qs = a.qs; c.ks = a.ks; c.vs = a.vs; c.g = a.g; c.beta = a.beta; c.lens = a.lens; c.s_in = a.s_in;
   c.rec = ws + w.rec; c.s0 = (uint32_t*)(ws + w.s0); c.u = (uint32_t*)(ws + w.u);
   c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = (d->T + delta::L - 1) / delta::L;
-  c.scale = d->scale; c.segs = c.pieces = 1; c.seg_chunks = c.chunks;
+  c.scale = d->scale; c.segs = 1; c.pieces = w.pieces; c.seg_chunks = (c.chunks + w.pieces - 1) / w.pieces;
+  if (w.pieces > 1) c.s_out = n.hand = (float*)(ws + w.hand);
+  c.turn = (int*)(ws + w.turn); c.done = c.turn + 2;
   n.dO = (const __nv_bfloat16*)ga.dO; n.dos = ga.dos; n.ds_out = ga.ds_out; n.ds_in = ga.ds_in;
   n.dq = (__nv_bfloat16*)ga.dq; n.dk = (__nv_bfloat16*)ga.dk; n.dv = (__nv_bfloat16*)ga.dv;
   n.dg = ga.dg; n.db = ga.db; n.ds = (uint32_t*)(ws + w.ds); n.fimg = (uint32_t*)(ws + w.f);

@@ -642,7 +642,8 @@ cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t
 }
 template <int DK, int DV>
 cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
-  if (a.s0 != nullptr) return launch<DK, DV, kImages>(m, a, B, stream);
+  if (a.s0 != nullptr)
+    return a.pieces > 1 ? launch<DK, DV, kImages, true>(m, a, B, stream) : launch<DK, DV, kImages>(m, a, B, stream);
   if (a.segs > 1) {
     const cudaError_t e = launch<DK, DV, kStateOnly>(m, a, B, stream);
     if (e != cudaSuccess) return e;
@@ -666,16 +667,16 @@ cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream
   return a.dv == 128 ? chaintc::run<64, 128>(m, a, B, stream) : chaintc::run<64, 64>(m, a, B, stream);
 }
 
-// Pieces of the sequences, in chunk steps (2.6 us each): units over 148 come in
-// waves, and the last wave is the shorter the shorter its CTAs.  A CTA costs three
-// steps beside its chunks, and one with a state to hand over four and a half.  64
-// chunks: 512 heads 690 us whole, 653 in two pieces, 702 in three; 160 heads 339,
-// 275, 258, and 259 in four.  16 chunks of 512 heads: 193 whole, 220 in two.
-int chain_pieces(long long units, int chunks) {
+// Pieces of the sequences, in chunk steps: units over 148 come in waves, and the
+// last wave is the shorter the shorter its CTAs.  Forwards a step is 2.6 us, and a
+// CTA costs three more, or four and a half with a state to hand over.  64 chunks:
+// 512 heads 690 us whole, 653 in two pieces, 702 in three; 160 heads 339, 275, 258,
+// and 259 in four.  16 chunks of 512 heads: 193 whole, 220 in two.
+int chain_pieces(long long units, int chunks, double whole, double cut) {
   int best = 1;
-  double least = (double)((units + 147) / 148) * (chunks + 3);
+  double least = (double)((units + 147) / 148) * (chunks + whole);
   for (int p = 2; p <= (units > 148 ? 8 : 1) && p <= chunks; ++p) {
-    const double t = (double)((units * p + 147) / 148) * ((chunks + p - 1) / p + 4.5);
+    const double t = (double)((units * p + 147) / 148) * ((chunks + p - 1) / p + cut);
     if (t < 0.98 * least) {
       least = t;
       best = p;

@@ -24,13 +24,13 @@ struct PrefillLayout {
     const size_t units = (size_t)d->B * d->H, state = (size_t)d->dv * d->dk * 4;
     chunks = (d->T + delta::L - 1) / delta::L;
     segs = delta::chain_segments((long long)units, chunks);
-    pieces = segs > 1 ? 1 : delta::chain_pieces((long long)units, chunks);
+    pieces = segs > 1 ? 1 : delta::chain_pieces((long long)units, chunks, 3, 4.5);
     size_t at = units * chunks * delta::rec_bytes(false);
     auto take = [&](size_t bytes) { const size_t r = (at + 255) & ~(size_t)255; at = r + bytes; return r; };
     n = take(segs > 1 ? units * (segs - 1) * state : 0);
     x = take(segs > 1 ? units * (segs - 2) * d->dk * d->dk * 4 : 0);
     s = take(segs > 1 ? units * segs * state : 0);
-    turn = take(pieces > 1 ? (units + 1) * 4 : 0);
+    turn = take(pieces > 1 ? delta::piece_bytes(units) : 0);
     total = at;
   }
 };
@@ -51,7 +51,7 @@ cudaError_t delta_prefill(const DeltaArgs& a, cudaStream_t stream) {
   c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = w.chunks;
   c.scale = d->scale;
   c.segs = w.segs; c.pieces = w.pieces; c.seg_chunks = (w.chunks + w.segs * w.pieces - 1) / (w.segs * w.pieces);
-  c.turn = (int*)(ws + w.turn); c.done = c.turn + 1;
+  c.turn = (int*)(ws + w.turn); c.done = c.turn + 2;
   c.seg_n = (float*)(ws + w.n); c.seg_x = (float*)(ws + w.x); c.seg_s = (float*)(ws + w.s);
   cudaError_t e = delta::prepare(c, d->B, d->dk, false, stream);
   if (e == cudaSuccess) e = delta::forward_chain(c, d->B, d->dk, stream);

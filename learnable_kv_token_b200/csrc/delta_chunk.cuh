@@ -102,7 +102,8 @@ struct ChunkArgs {
   // n [units][segs - 1][dv][dk], X [units][segs - 2][dk][dk], states [units][segs][dv][dk]
   int segs, seg_chunks;
   // or pieces that follow one another (pieces = 1: one; seg_chunks: chunks of each): the
-  // next piece's number and, per unit, its pieces that are done (prepare sets all to zero)
+  // next piece's number and, per unit, its pieces that are done, each for the forward and
+  // the backward chain (prepare sets all to zero)
   int pieces, *turn, *done;
   float *seg_n, *seg_x, *seg_s;
 };
@@ -116,6 +117,7 @@ struct GradArgs {
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg, *db;
   uint32_t *ds, *fimg;       // images of dS (hi) and F (hi) per chunk
+  float* hand;               // [units][dv][dk]: dS between pieces (forward: S, as s_out)
   float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
 };
 
@@ -126,7 +128,9 @@ cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t s
 // delta_chain_tc.cu: the chain of states with O; with s0 and u, writes their images instead of O
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
 int chain_segments(long long units, int chunks);
-int chain_pieces(long long units, int chunks);
+// `whole`, `cut`: what a CTA costs beside its chunks, in chunk steps, without and with a state to hand over
+int chain_pieces(long long units, int chunks, double whole, double cut);
+inline size_t piece_bytes(size_t units) { return (2 + 2 * units) * 4; }   // turn, then done
 // delta_back_tc.cu: the backward chain
 cudaError_t back_chain(const GradArgs& a, int B, int dk, cudaStream_t stream);
 

@@ -87,8 +87,8 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = seq_len(a.lens, b, a.T), t0 = c * L;
   if (a.pieces > 1 && c == 0 && tid == 0) {
-    a.done[u] = 0;
-    if (u == 0) *a.turn = 0;
+    a.done[u] = a.done[gridDim.x / a.chunks + u] = 0;
+    if (u == 0) a.turn[0] = a.turn[1] = 0;
   }
   if (t0 >= len) return;
   const uint32_t s0 = sa(sm), bar_in = sa(&bars[0]), bar_mma = sa(&bars[1]);

@@ -408,6 +408,22 @@ def test_more_heads_than_processors(layer, T):
         assert torch.equal(o[half], o1) and torch.equal(S[half], S1)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_of_more_heads_than_processors(layer, D):
+    """The same for the gradients, whose pieces also hand on the state's gradient."""
+    T = 1500
+    x = inputs(67, 40, T, 4, 2, D, D, lens=[T, 0, 1, 64, T // 2, 512, 513, T - 1] * 5)
+    names = ("q", "k", "v", "g", "beta")
+    g = torch.Generator().manual_seed(5)
+    do, ds = torch.randn(x["v"].shape, generator=g).bfloat16().cuda(), torch.randn(x["state"].shape, generator=g).cuda()
+    got = layer.delta_backward(*(x[n] for n in names), do, state=x["state"], dstate=ds, lens=x["lens"])
+    for half in (slice(0, 20), slice(20, 40)):
+        part = layer.delta_backward(*(x[n][half] for n in names), do[half], state=x["state"][half], dstate=ds[half],
+                                    lens=x["lens"][half])
+        for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "dstate"), got, part):
+            assert torch.equal(a[half], b), name
+
+
 def test_gradients_on_two_streams_at_once(layer):
     """Two gradient passes that run side by side give what each gives alone."""
     names = ("q", "k", "v", "g", "beta")
