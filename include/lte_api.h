@@ -556,6 +556,13 @@ lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k,
                             void* dk, void* dv, float* dg, float* dbeta, float* dstate_in,
                             void* workspace, size_t ws_bytes, void* stream);
 
+/* lte_gdr_zero_padding -- zeros in the rows behind each sequence's length, which
+ * the calls above leave as they were, of n (1 .. 8) contiguous tensors
+ * [B,T,row_bytes] in one launch; nothing else is touched.  row_bytes: multiples
+ * of 4; tensors 4-byte aligned.  lens as above. */
+lte_status lte_gdr_zero_padding(int32_t B, int32_t T, const int32_t* lens, int32_t n,
+                                void* const* tensors, const int64_t* row_bytes, void* stream);
+
 /* lte_gdr_decode_step -- one token per sequence (d->T is ignored): q_t, k_t
  * [B,Hk,dk], v_t, o_t [B,H,dv], g_t, beta_t fp32 [B,H], all contiguous; state is
  * updated in place.  fp32 arithmetic for both dtypes. */

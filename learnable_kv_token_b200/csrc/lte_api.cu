@@ -617,6 +617,15 @@ lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k,
   return e == cudaErrorNotSupported ? LTE_ERR_UNSUPPORTED : from_cuda(e);
 }
 
+lte_status lte_gdr_zero_padding(int32_t B, int32_t T, const int32_t* lens, int32_t n,
+                                void* const* tensors, const int64_t* row_bytes, void* stream) {
+  if (B < 1 || T < 1 || n < 1 || n > 8 || !lens || !tensors || !row_bytes) return LTE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (tensors[i] == nullptr || reinterpret_cast<uintptr_t>(tensors[i]) % 4 || row_bytes[i] < 1 || row_bytes[i] % 4)
+      return LTE_ERR_INVALID_ARG;
+  return from_cuda(lte::delta_zero_padding(B, T, lens, n, tensors, row_bytes, as_stream(stream)));
+}
+
 lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,
                                const void* v_t, const float* g_t, const float* beta_t, void* o_t,
                                float* state, void* stream) {

@@ -164,6 +164,8 @@ struct DeltaGradArgs {
 };
 size_t delta_backward_bytes(const lte_gdr_dims* d);
 cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStream_t stream);
+cudaError_t delta_zero_padding(int B, int T, const int32_t* lens, int n, void* const* x, const int64_t* row_bytes,
+                               cudaStream_t stream);
 cudaError_t delta_step(const lte_gdr_dims* d, const void* q, const void* k, const void* v, const float* g,
                        const float* beta, void* o, float* state, cudaStream_t stream);
 

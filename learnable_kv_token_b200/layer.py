@@ -337,9 +337,8 @@ def _on_device(fn):
     return call
 
 
-def _new(x, lens=None):
-    """A contiguous tensor like x, zeros if some of its rows lie behind a sequence's length."""
-    return (torch.empty_like if lens is None else torch.zeros_like)(x, memory_format=torch.contiguous_format)
+def _new(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _workspace(x, n):
@@ -424,7 +423,9 @@ def delta_prefill(q, k, v, g, beta, state=None, lens=None, scale=None, state_out
         state_out = g.new_empty(shape)
     else:
         _check(state_out, "state_out", shape, torch.float32, q.device)
-    o = _new(v, lens)
+    o = _new(v)
+    if lens is not None:
+        L.lte_gdr_zero_padding(lens, [o])
     ws = _workspace(q, L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_PREFILL))
     L.lte_gdr_prefill(d, q, k, v, g, beta, o, state_out, ws, state, lens)
     return o, state_out
@@ -443,7 +444,9 @@ def delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lens=None, sca
         _check(dstate, "dstate", shape, torch.float32, q.device)
     if do.shape != v.shape or do.dtype is not v.dtype or do.device != v.device:
         raise ValueError("do has v's shape, dtype and device")
-    grads = [_new(x, lens) for x in (q, k, v, g, beta)]
+    grads = [_new(x) for x in (q, k, v, g, beta)]
+    if lens is not None:
+        L.lte_gdr_zero_padding(lens, grads)
     ds = g.new_empty(shape)
     ws = _workspace(q, L.lte_gdr_workspace_bytes(d, L.LTE_GDR_WS_BACKWARD))
     L.lte_gdr_backward(d, q, k, v, g, beta, do, *grads, ws, state, lens, dstate, ds)

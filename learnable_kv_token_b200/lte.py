@@ -106,6 +106,7 @@ _SIG = {
                        + [_P] * 5 + [C.POINTER(lte_strides), _P, _P, C.c_size_t, _P],
     "lte_gdr_backward": [C.POINTER(lte_gdr_dims), _P, _P, _P] + [C.POINTER(lte_strides)] * 3
                         + [_P] * 5 + [C.POINTER(lte_strides)] + [_P] * 8 + [C.c_size_t, _P],
+    "lte_gdr_zero_padding": [_I, _I, _P, _I, C.POINTER(_P), C.POINTER(C.c_int64), _P],
     "lte_gdr_decode_step": [C.POINTER(lte_gdr_dims)] + [_P] * 8,
     "lte_qk_norm_rope": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2 + [_P] * 4,
     "lte_qk_norm_rope_backward": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2
@@ -382,6 +383,15 @@ def lte_gdr_backward(dims, q, k, v, g, beta, do, dq, dk, dv, dg, dbeta, workspac
         _ref_strides(do), _addr(dstate_out), _addr(dq), _addr(dk), _addr(dv), _addr(dg),
         _addr(dbeta), _addr(dstate_in), _addr(workspace),
         _ws_bytes(workspace), _raw(stream)))
+
+
+def lte_gdr_zero_padding(lens, tensors, stream=None):
+    """tensors: contiguous [B,T,...]."""
+    B, T = tensors[0].shape[:2]
+    n = len(tensors)
+    _check_status("lte_gdr_zero_padding", _lib.lte_gdr_zero_padding(
+        B, T, _addr(lens), n, (_P * n)(*(t.data_ptr() for t in tensors)),
+        (C.c_int64 * n)(*(t.stride(1) * t.element_size() for t in tensors)), _raw(stream)))
 
 
 def lte_gdr_decode_step(dims, q_t, k_t, v_t, g_t, beta_t, o_t, state, stream=None):

@@ -135,3 +135,12 @@ def test_norm_pointers_and_workspace(L):
     f = norm(L, dtype=L.LTE_F32)
     assert bwd([*good[:7], L.LTE_BF16, *good[8:]], f) == INVALID              # fp32 rows, bf16 gradients
     assert bwd(good, norm(L, kind=L.LTE_NORM_NONE)) == INVALID                # a weight gradient without a norm
+
+
+def test_zero_padding(L):
+    one, rows = (C.c_void_p * 9)(*[1 << 20] * 9), (C.c_int64 * 9)(*[64] * 9)
+    call = lambda B=2, T=8, lens=P, n=2, x=one, r=rows: L._lib.lte_gdr_zero_padding(B, T, lens, n, x, r, None)  # noqa: E731
+    odd = (C.c_void_p * 2)(1 << 20, (1 << 20) + 2)
+    for bad in (dict(B=0), dict(T=0), dict(lens=None), dict(n=0), dict(n=9), dict(x=None), dict(r=None), dict(x=odd),
+                dict(x=(C.c_void_p * 2)(1 << 20, None)), dict(r=(C.c_int64 * 2)(64, 6)), dict(r=(C.c_int64 * 2)(0, 64))):
+        assert call(**bad) == INVALID

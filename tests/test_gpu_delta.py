@@ -160,6 +160,21 @@ def test_broadcast_and_padded_views(layer):
     check_backward(layer, y)
 
 
+@pytest.mark.parametrize("lens", [[0, 5, 33], [-7, 99, 32]], ids=str)
+def test_zero_padding(layer, lens):
+    """Rows behind the lengths (which are clamped) become zero, all else stays: rows of 4, 12, 130 * 4 and
+    20 * 2 bytes, so that stretches begin and end anywhere in a group of 16."""
+    T, n = 33, torch.tensor(lens, dtype=torch.int32).cuda()
+    store = [torch.full((3 * T * w + 9,), 7.0, dtype=t, device="cuda")
+             for w, t in ((1, torch.float32), (3, torch.float32), (130, torch.float32), (20, torch.bfloat16))]
+    x = [s[4:-5].view(3, T, -1) for s in store]
+    layer.L.lte_gdr_zero_padding(n, x)
+    for s, t in zip(store, x):
+        assert (s[:4] == 7).all() and (s[-5:] == 7).all()
+        for b, m in enumerate(min(max(m, 0), T) for m in lens):
+            assert (t[b, :m] == 7).all() and (t[b, m:] == 0).all()
+
+
 def test_prefill_continues(layer):
     """A prompt in three calls, in place on one state, equals the prompt in one call."""
     x = inputs(4, 2, 300, 4, 4, 128, 128)
