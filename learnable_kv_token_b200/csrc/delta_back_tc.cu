@@ -19,7 +19,10 @@
 // one spilled costs a trip to L2.
 // The products of dO with Q run while the chain warps turn F, so the chain of a
 // chunk is P -> dU -> F -> dS as in the forward pass.  Sequences of more heads than
-// SMs are cut into pieces as there; dS goes from one to the next by `hand`.  64 chunks of 128 heads of
+// SMs are cut into pieces as there; dS goes from one to the next by `hand`.  Long
+// sequences of few heads are cut into segments as there: dS goes back through a
+// segment by the transpose of its X, so a first pass finds the chains from zero,
+// the join carries them, and a second pass runs every segment from its dS.  64 chunks of 128 heads of
 // 128 channels (one wave): 495 us, 7.7 us a chunk; 160 KB of images and dV
 // per chunk beside 97 KB of inputs (2.1 GB, 4.3 TB/s) make memory latency the bound.
 #include <math.h>
@@ -83,7 +86,10 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
   return r;
 }
 
-template <int DK, int DV, bool PIECES>
+// a unit whole, in pieces, in segments, or segments' chains of dS alone
+enum : int { kWhole = 0, kPieces = 1, kSegments = 2, kSegState = 3 };
+
+template <int DK, int DV, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_v,
@@ -92,6 +98,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const ChunkArgs& a = ga.f;
   constexpr uint32_t kColSh = DK, kColSl = DK + DK / 2;
   constexpr int kHK = DK / 64, kHV = DV / 64, kStrips = DV / 16;
+  constexpr bool PIECES = KIND == kPieces, STATE = KIND == kSegState, SEG = KIND == kSegments || STATE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t s0 = sa(sm), bars = s0 + kBars;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
@@ -120,12 +127,14 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // the unit, and its chunks cb .. cb + n - 1 (pieces from the last to the first)
-  const int units = PIECES ? gridDim.x / a.pieces : 1, u = PIECES ? *ticket % units : (int)blockIdx.x;
-  const int piece = PIECES ? *ticket / units : 0, cb = PIECES ? (a.pieces - 1 - piece) * a.seg_chunks : 0;
+  // the unit, and its chunks cb .. cb + n - 1 (pieces from the last to the first; dS alone of segments 1 on)
+  const int units = PIECES ? gridDim.x / a.pieces : 1, per = STATE ? a.segs - 1 : SEG ? a.segs : 1;
+  const int u = PIECES ? *ticket % units : (int)blockIdx.x / per;
+  const int piece = PIECES ? *ticket / units : 0, seg = SEG ? (int)blockIdx.x % per + STATE : 0;
+  const int cb = PIECES ? (a.pieces - 1 - piece) * a.seg_chunks : seg * a.seg_chunks;
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int len = seq_len(a.lens, b, a.T);
-  const int n = PIECES ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
+  const int n = PIECES || SEG ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
   bool ok = true, issued = false;
   int loaded = 0;
 
@@ -140,24 +149,24 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const bool tail = c * L + L > len;                       // the first one to come
       const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
       if (elect_one()) {
-        mbar_expect_tx(fb, 2 * (kHK + kHV) * kHalf + 4 * kImg + kScal);
+        mbar_expect_tx(fb, (2 * kHK + (STATE ? 1 : 2) * kHV) * kHalf + 4 * kImg + kScal);
         for (int j = 0; j < kHK; ++j) {
           tma_load_4d(d + kK + j * kHalf, &tm_k, fb, 64 * j, hk, c * L, b);
           tma_load_4d(d + kQ + j * kHalf, &tm_q, fb, 64 * j, hk, c * L, b);
         }
         for (int j = 0; j < kHV; ++j) {
           tma_load_4d(d + kD + j * kHalf, &tm_d, fb, 64 * j, h, c * L, b);
-          tma_load_4d(d + kV + j * kHalf, &tm_v, fb, 64 * j, h, c * L, b);
+          if (!STATE) tma_load_4d(d + kV + j * kHalf, &tm_v, fb, 64 * j, h, c * L, b);
         }
         bulk_load(d + kR, recs + (long long)c * rec_bytes(true), 4 * kImg + kScal, fb);
       }
-      {                                                        // the images that the output warps read: to L2, a piece per lane
+      if (!STATE) {                                            // the images that the output warps read: to L2, a piece per lane
         const long long img = (long long)u * a.chunks + c;
         prefetch_l2(reinterpret_cast<const uint8_t*>(a.u + img * DV * L) + lane * (DV * L / 8), DV * L / 8);
         prefetch_l2(reinterpret_cast<const uint8_t*>(a.s0 + img * DV * DK) + lane * (DV * DK / 8), DV * DK / 8);
       }
       ++loaded;
-      if (DK == 128 && i > 0) {                                // the state of the chunk behind, key channels 96 on
+      if (DK == 128 && !STATE && i > 0) {                      // the state of the chunk behind, key channels 96 on
         if (i > 1 && !(ok = wwait(bar(bStFree), i & 1, abort_flag, nullptr, 0))) break;
         if (lane == 0) mbar_expect_tx(bar(bSt), DV / 8 * 2 * 512);
         __syncwarp();
@@ -177,7 +186,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         for (int j = 0; j < kHV; ++j) {
           zero_rows(st + kD + j * kHalf, r0, lane);
-          zero_rows(st + kV + j * kHalf, r0, lane);
+          if (!STATE) zero_rows(st + kV + j * kHalf, r0, lane);
         }
         fence_proxy_async();
         __syncwarp();
@@ -213,7 +222,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       if (!ok) break;
       // (X's columns still hold the F of the chunk before until its sums have been taken)
-      if (i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!STATE && i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
       tc_fence_after();
       if (elect_one()) {                                       // X = dO^T A, and dO^T
 #pragma unroll
@@ -290,14 +299,16 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     {                                                          // the gradient behind, while the last chunk loads
       const bool later = PIECES && n > 0 && (cb + n) * L < len;
       if (later) ok = piece_ready(a.done + units + u, piece, abort_flag);
-      const float* src = later ? ga.hand : ga.ds_out;
+      const float* src = later ? ga.hand + srow : STATE && seg < a.segs - 1 ? nullptr : ga.ds_out;
+      if (SEG && !STATE) src = a.seg_s + ((long long)u * a.segs + a.segs - 1 - seg) * DV * DK + (row < DV ? row : 0) * DK;
+      else if (!later && src != nullptr) src += srow;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
         uint32_t r[QC];
 #pragma unroll
         for (int e = 0; e < QC / 4; ++e) {
-          const float4 v = src != nullptr && row < DV ? __ldcg(reinterpret_cast<const float4*>(src + srow + c0 + 4 * e))
+          const float4 v = src != nullptr && row < DV ? __ldcg(reinterpret_cast<const float4*>(src + c0 + 4 * e))
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
           r[4 * e] = __float_as_uint(v.x);
           r[4 * e + 1] = __float_as_uint(v.y);
@@ -313,7 +324,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       // ---- dS as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
-      if (i > 0 && !(ok = wwait(bar(bSread), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!STATE && i > 0 && !(ok = wwait(bar(bSread), (i - 1) & 1, abort_flag, nullptr, 0))) break;
       const float el = scal[kEG * L + L - 1];
       const uint64_t el2 = f2(el, el);
 #pragma unroll
@@ -405,6 +416,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tmem_st16(la + kColF + 32 * hc + 16, lo);
         arrive(bFr);
         if (lane == 0) mbar_arrive(bar(bEmpty + s));           // the scalars have been read
+        if (STATE) continue;
         uint32_t x[32];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -421,7 +433,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
       tc_fence_after();
     }
-    float* dst = cb == 0 ? ga.ds_in : n > 0 ? ga.hand : nullptr;
+    float* dst = cb == 0 ? ga.ds_in : PIECES && n > 0 ? ga.hand : nullptr;
+    if (STATE) dst = a.seg_n + ((long long)u * (a.segs - 1) + a.segs - 1 - seg) * DV * DK + (row < DV ? row : 0) * DK;
+    else if (dst != nullptr) dst += srow;
     if (dst != nullptr) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -435,7 +449,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
-            *reinterpret_cast<float4*>(dst + srow + c0 + 4 * e) = v;
+            *reinterpret_cast<float4*>(dst + c0 + 4 * e) = v;
           }
         }
       }
@@ -471,7 +485,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // the state of the chunk behind, hi and lo, 16 key channels at a time, asked for
         // kAhead pieces ahead of their use: as much in flight as registers hold
         uint4 st[kAhead + 1][4];
-        const bool inner = mine && i > 0;
+        const bool inner = !STATE && mine && i > 0;
         auto fetch_state = [&](int j) {
           const uint8_t* p = s_img + (long long)(c + 1) * (DV * DK * 4) + j * 256;
 #pragma unroll
@@ -511,6 +525,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           mbar_arrive(bar(bDr));
           mbar_arrive(bar(bEmpty + s));
         }
+        if (STATE) continue;
         // dS: its image (hi), and <dS, S_0> with the state of the chunk behind
         if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0))) break;
         tc_fence_after();
@@ -560,7 +575,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (i > 0) put_inner(c + 1, in);
       }
       // the gradient of the (piece's) initial state with that state
-      if (ok && n > 0 && wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) &&
+      if (!STATE && ok && n > 0 && wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) &&
           wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0)) {
         tc_fence_after();
         float in = 0.f;
@@ -575,7 +590,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               float x[8];
 #pragma unroll
               for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(r[8 * e + f]);
-              if (PIECES && cb > 0)                            // as the next chunk of the piece would see it
+              if (cb > 0)                                      // as the next chunk of the piece would see it
 #pragma unroll
                 for (int f = 0; f < 8; f += 2) {
                   uint32_t hi, lo;
@@ -603,6 +618,11 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const long long img = (long long)u * a.chunks + c;
         // (a warp whose wait gave up still meets the others at the vote below)
         ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
+        if (STATE) {
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(bar(bEmpty + s));
+          continue;
+        }
         const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
         uint4 uw[2][4];
         auto fetch_u = [&](int j) {                            // 16 tokens, hi and lo
@@ -689,7 +709,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
       if ((cb + n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
       else mbar_drain(bar(bTail), 0);
-    if (DK == 128 && loaded > 1) mbar_drain(bar(bSt), (loaded - 2) & 1);
+    if (DK == 128 && !STATE && loaded > 1) mbar_drain(bar(bSt), (loaded - 2) & 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -697,16 +717,22 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <int DK, int DV, bool PIECES>
+template <int DK, int DV, int KIND>
 cudaError_t launch_as(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  delta_back_tc_kernel<DK, DV, PIECES><<<(unsigned)(B * a.f.H * a.f.pieces), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
+  const int per = KIND == kSegState ? a.f.segs - 1 : a.f.segs * a.f.pieces;
+  delta_back_tc_kernel<DK, DV, KIND><<<(unsigned)(B * a.f.H * per), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
   return cudaGetLastError();
 }
 template <int DK, int DV>
 cudaError_t launch(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
-  return a.f.pieces > 1 ? launch_as<DK, DV, true>(m, a, B, stream) : launch_as<DK, DV, false>(m, a, B, stream);
+  if (a.f.segs > 1) {
+    cudaError_t e = launch_as<DK, DV, kSegState>(m, a, B, stream);
+    if (e == cudaSuccess) e = join_states(a.f, a.ds_out, true, B, DK, stream);
+    return e == cudaSuccess ? launch_as<DK, DV, kSegments>(m, a, B, stream) : e;
+  }
+  return a.f.pieces > 1 ? launch_as<DK, DV, kPieces>(m, a, B, stream) : launch_as<DK, DV, kWhole>(m, a, B, stream);
 }
 
 }  // namespace backtc

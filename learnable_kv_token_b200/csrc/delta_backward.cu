@@ -368,14 +368,38 @@ cudaError_t grad(const GradArgs& a, int B, cudaStream_t stream) {
   return a.f.H == a.f.Hk ? grad_as<DK, DV, false>(a, B, stream) : grad_as<DK, DV, true>(a, B, stream);
 }
 
+// Segments of a sequence for both chains, by an estimate in us as in the forward pass
+// (chain_segments): a chunk takes 2.6 forwards, 2.5 for dS alone and from 5.3 to 7.7
+// backwards, the more CTAs run.  Both chains and all that segments add, 16 heads of
+// 16384 tokens: 2153 us in one piece, 661 in six, 640 in eight, 817 in twelve; 2 heads
+// of 4096: 518, 154 in eight, 142 in twelve; one head of 1536: 206, 91 in six.
+int grad_segments(long long units, int chunks, long long join_ctas) {
+  auto waves = [](long long ctas) { return (double)((ctas + 147) / 148); };
+  auto chunk = [](long long ctas) { return 7.9 + 2.4 * (ctas < 148 ? ctas : 148) / 148; };    // forwards and backwards
+  int best = 1;
+  double least = 0.95 * waves(units) * (chunk(units) * chunks + 14);
+  for (int g = 3; g <= 64 && g * 2 <= chunks; ++g) {
+    const int per = (chunks + g - 1) / g;
+    const double t = waves(units * (2 * g - 3)) * (2.3 * per + 6) + waves(units * (g - 1)) * (2.5 * per + 6) +
+                     waves(units * g) * (chunk(units * g) * per + 14) + 3.2 * (g - 1) * waves(join_ctas) + 20;
+    if (t < least) {
+      least = t;
+      best = g;
+    }
+  }
+  return best;
+}
+
 // workspace: records, then the images and partial sums, each rounded up to 256 bytes
 struct BackwardLayout {
-  size_t rec, s0, u, f, ds, x, inner, hand, turn, total;
-  int pieces;
+  size_t rec, s0, u, f, ds, x, inner, hand, turn, seg_n, seg_x, seg_xt, seg_s, total;
+  int segs, pieces;
   explicit BackwardLayout(const lte_gdr_dims* d) {
     const size_t units = (size_t)d->B * d->H, n = units * ((d->T + L - 1) / L), dv = d->dv, dk = d->dk;
+    const int chunks = (d->T + L - 1) / L;
+    segs = grad_segments((long long)units, chunks, (long long)(units * dv * dk / 1024));
     // (a chunk takes both chains 10 us together: a CTA's start and end cost less of one)
-    pieces = chain_pieces((long long)units, (d->T + L - 1) / L, 1.5, 2);
+    pieces = segs > 1 ? 1 : chain_pieces((long long)units, chunks, 1.5, 2);
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += (bytes + 255) & ~(size_t)255; return r; };
     rec = take(n * rec_bytes(true));
@@ -387,6 +411,10 @@ struct BackwardLayout {
     inner = take(n * (dv / 16) * 4);
     hand = take(pieces > 1 ? units * dv * dk * 4 : 0);
     turn = take(pieces > 1 ? piece_bytes(units) : 0);
+    seg_n = take(segs > 1 ? units * (segs - 1) * dv * dk * 4 : 0);
+    seg_x = take(segs > 1 ? units * (segs - 2) * dk * dk * 4 : 0);
+    seg_xt = take(segs > 1 ? units * (segs - 2) * dk * dk * 4 : 0);
+    seg_s = take(segs > 1 ? units * segs * dv * dk * 4 : 0);
     total = at;
   }
 };
@@ -405,7 +433,9 @@ cudaError_t delta_backward(const DeltaArgs& a, const DeltaGradArgs& ga, cudaStre
   c.qs = a.qs; c.ks = a.ks; c.vs = a.vs; c.g = a.g; c.beta = a.beta; c.lens = a.lens; c.s_in = a.s_in;
   c.rec = ws + w.rec; c.s0 = (uint32_t*)(ws + w.s0); c.u = (uint32_t*)(ws + w.u);
   c.T = d->T; c.H = d->H; c.Hk = d->Hk; c.dv = d->dv; c.chunks = (d->T + delta::L - 1) / delta::L;
-  c.scale = d->scale; c.segs = 1; c.pieces = w.pieces; c.seg_chunks = (c.chunks + w.pieces - 1) / w.pieces;
+  c.scale = d->scale; c.segs = w.segs; c.pieces = w.pieces; c.seg_chunks = (c.chunks + w.segs * w.pieces - 1) / (w.segs * w.pieces);
+  c.a_lo = true; c.seg_n = (float*)(ws + w.seg_n); c.seg_x = (float*)(ws + w.seg_x);
+  c.seg_xt = (float*)(ws + w.seg_xt); c.seg_s = (float*)(ws + w.seg_s);
   if (w.pieces > 1) c.s_out = n.hand = (float*)(ws + w.hand);
   c.turn = (int*)(ws + w.turn); c.done = c.turn + 2;
   n.dO = (const __nv_bfloat16*)ga.dO; n.dos = ga.dos; n.ds_out = ga.ds_out; n.ds_in = ga.ds_in;

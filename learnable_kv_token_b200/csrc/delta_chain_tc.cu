@@ -82,8 +82,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
   volatile int* ticket = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return bars + 8 * i; };
-  constexpr int kRecBytes = rec_bytes(KIND == kImages);
-  constexpr bool kRecHasALo = KIND == kImages;
+  const bool a_lo = KIND == kImages || (KIND == kStateOnly && a.a_lo);      // the records hold A's lo
 
   if (tid == 0) {
     for (int i = 0; i < kBarCount; ++i) {
@@ -131,7 +130,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   if (warp >= 12) regs_dec<80>();
   if (warp == 12) {
     // ================================================================ loads
-    const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * kRecBytes;
+    const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * rec_bytes(a_lo);
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1;
       if (c >= 2 && !(ok = wwait(bar(bEmpty + s), ((c >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
@@ -139,7 +138,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       const bool tail = c * L + L > len;
       const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
       if (elect_one()) {
-        const uint8_t* r = recs + (long long)c * kRecBytes;
+        const uint8_t* r = recs + (long long)c * rec_bytes(a_lo);
         mbar_expect_tx(fb, (OUT ? 2 * kHK + kHV : kHK + kHV) * kHalf + (OUT ? 3 : 2) * kImg + kScal);
         for (int i = 0; i < kHK; ++i) {
           tma_load_4d(d + kK + i * kHalf, &tm_k, fb, 64 * i, hk, (cb + c) * L, b);
@@ -150,7 +149,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           bulk_load(d + kR, r, 3 * kImg + kScal, fb);
         } else {
           bulk_load(d + kR, r, 2 * kImg, fb);
-          bulk_load(d + kScalOff, r + (kRecHasALo ? 4 : 3) * kImg, kScal, fb);
+          bulk_load(d + kScalOff, r + (a_lo ? 4 : 3) * kImg, kScal, fb);
         }
       }
       ++loaded;
@@ -270,7 +269,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int rows = hom ? DK : DV;
     {                                                          // the state, while the first chunk loads
-      const bool joined = KIND == kO && a.segs > 1;            // (s_out may be s_in: that was read by the join)
+      const bool joined = KIND != kStateOnly && a.segs > 1;            // (s_out may be s_in: that was read by the join)
       const float* src = joined ? a.seg_s + seg * DV * DK : seg == 0 ? a.s_in : PIECES ? a.s_out : nullptr;
       if (PIECES && seg > 0 && n_chunks > 0) ok = piece_ready(a.done + u, seg, abort_flag);
       if (src != nullptr) src += (long long)u * (joined ? a.segs : 1) * DV * DK + row * DK;
@@ -425,6 +424,13 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                                    __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
             if (!ok) v = make_float4(NAN, NAN, NAN, NAN);
             *reinterpret_cast<float4*>(dst + c0 + 4 * e) = v;
+            if (KIND == kStateOnly && hom && a.seg_xt != nullptr) {
+              float* t = a.seg_xt + ((long long)ul * (a.segs - 2) + segl - 1) * DK * DK + (c0 + 4 * e) * DK + row;
+              t[0] = v.x;
+              t[DK] = v.y;
+              t[2 * DK] = v.z;
+              t[3 * DK] = v.w;
+            }
           }
         }
       }
@@ -571,19 +577,26 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 }
 
 // The states that the segments start from: S_0 as given, S_1 = n_0, S_{g+1} = S_g
-// X_g + n_g, in fp32.  One CTA per 16 rows of a unit's state: rows do not mix.
-// The next segment's X comes in by cp.async while this one's is in use.
+// X_g + n_g, in fp32 (the gradients: from the last segment to the first, with X
+// transposed).  Rows do not mix, so a CTA takes 1024 entries of a unit's state; each
+// of its eight warps takes an eighth of the sum over k for all of them, eight rows
+// and four columns to a lane, so that what shared memory gives is used 32 times.
+// The next segment's X comes in by cp.async meanwhile.  1.6 us a segment of 128 x
+// 128 for up to 148 CTAs (9 units); 12.6 for eight segments.
 template <int DK>
 __global__ void __launch_bounds__(256)
-delta_join_kernel(const ChunkArgs a) {
-  constexpr int CT = DK / 16;                                  // columns per thread
-  extern __shared__ __align__(128) float jsm[];                // two X, then 16 rows of S
+delta_join_kernel(const ChunkArgs a, const float* given, const float* xs, bool reverse) {
+  constexpr int ROWS = 1024 / DK, KW = DK / 8;                 // k of a warp
+  extern __shared__ __align__(128) float jsm[];                // two X, the rows of S by k, the warps' sums
   float* S = jsm + 2 * DK * DK;
-  const int slices = a.dv / 16, u = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 16;
-  const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 4; // columns c0 + 64 j .. + 3
+  float* part = S + DK * ROWS;
+  const int slices = a.dv / ROWS, u = blockIdx.x / slices, r0 = (blockIdx.x % slices) * ROWS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cl = 4 * (lane % (DK / 4)), rl = 8 * (lane / (DK / 4));        // sums: this lane's columns and rows
+  const int col = threadIdx.x % DK, row = 4 * (threadIdx.x / DK);          // results: four rows of a column
   auto fetch = [&](int g) {                                    // X of segment g
     if (g >= 1 && g + 1 < a.segs) {
-      const float* x = a.seg_x + ((long long)u * (a.segs - 2) + g - 1) * DK * DK;
+      const float* x = xs + ((long long)u * (a.segs - 2) + (reverse ? a.segs - 2 - g : g - 1)) * DK * DK;
       const uint32_t d = smem_u32(jsm + (g & 1) * DK * DK);
 #pragma unroll
       for (int i = 0; i < DK * DK / 4 / 256; ++i)
@@ -593,43 +606,69 @@ delta_join_kernel(const ChunkArgs a) {
   };
   fetch(1);
 #pragma unroll
-  for (int j = 0; j < CT; j += 4)
-    *reinterpret_cast<float4*>(a.seg_s + ((long long)u * a.segs * a.dv + r0 + r) * DK + c0 + 16 * j) =
-        a.s_in == nullptr ? make_float4(0.f, 0.f, 0.f, 0.f)
-                          : *reinterpret_cast<const float4*>(a.s_in + ((long long)u * a.dv + r0 + r) * DK + c0 + 16 * j);
+  for (int r = 0; r < 4; ++r)
+    a.seg_s[((long long)u * a.segs * a.dv + r0 + row + r) * DK + col] =
+        given == nullptr ? 0.f : given[((long long)u * a.dv + r0 + row + r) * DK + col];
   for (int g = 0; g + 1 < a.segs; ++g) {
-    float y[CT];
-    const float* n = a.seg_n + (((long long)u * (a.segs - 1) + g) * a.dv + r0 + r) * DK + c0;
+    float y[4];
+    const float* n = a.seg_n + (((long long)u * (a.segs - 1) + g) * a.dv + r0 + row) * DK + col;
 #pragma unroll
-    for (int j = 0; j < CT; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(n + 16 * j);
-      y[j] = v.x; y[j + 1] = v.y; y[j + 2] = v.z; y[j + 3] = v.w;
-    }
+    for (int r = 0; r < 4; ++r) y[r] = n[r * DK];
     if (g > 0) {
       fetch(g + 1);
       cp_async_wait<1>();
       __syncthreads();                                         // X of g has landed; S is complete
-      const float* x = jsm + (g & 1) * DK * DK + c0;
-#pragma unroll 8
-      for (int k = 0; k < DK; ++k) {
-        const float s = S[r * DK + k];
+      const float* x = jsm + (g & 1) * DK * DK + cl;
+      uint64_t acc[4][4];                                      // [row pair][column]
 #pragma unroll
-        for (int j = 0; j < CT; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(x + k * DK + 16 * j);
-          y[j] = fmaf(s, v.x, y[j]); y[j + 1] = fmaf(s, v.y, y[j + 1]);
-          y[j + 2] = fmaf(s, v.z, y[j + 2]); y[j + 3] = fmaf(s, v.w, y[j + 3]);
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[p][c] = 0;
+#pragma unroll 4
+      for (int k = warp * KW; k < warp * KW + KW; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(x + k * DK);
+        const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(S + k * ROWS + rl);
+        const ulonglong2 s1 = *reinterpret_cast<const ulonglong2*>(S + k * ROWS + rl + 4);
+        const uint64_t s[4] = {s0.x, s0.y, s1.x, s1.y};
+        const float vc[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t vv = f2(vc[c], vc[c]);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) acc[p][c] = fma2(s[p], vv, acc[p][c]);
         }
       }
-      __syncthreads();                                         // S and X of g have been read
-    }
-    float* out = a.seg_s + (((long long)u * a.segs + g + 1) * a.dv + r0 + r) * DK + c0;
+      float* w = part + warp * (ROWS * DK) + rl * DK + cl;
 #pragma unroll
-    for (int j = 0; j < CT; j += 4) {
-      const float4 v = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-      *reinterpret_cast<float4*>(out + 16 * j) = v;
-      *reinterpret_cast<float4*>(&S[r * DK + c0 + 16 * j]) = v;
+      for (int p = 0; p < 4; ++p) {
+        float4 e, o;
+        unf2(acc[p][0], e.x, o.x);
+        unf2(acc[p][1], e.y, o.y);
+        unf2(acc[p][2], e.z, o.z);
+        unf2(acc[p][3], e.w, o.w);
+        *reinterpret_cast<float4*>(w + 2 * p * DK) = e;
+        *reinterpret_cast<float4*>(w + (2 * p + 1) * DK) = o;
+      }
+      __syncthreads();                                         // sums are complete; S and X of g have been read
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] += part[i * (ROWS * DK) + (row + r) * DK + col];
     }
+    float* out = a.seg_s + (((long long)u * a.segs + g + 1) * a.dv + r0 + row) * DK + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) out[r * DK] = y[r];
+    *reinterpret_cast<float4*>(&S[col * ROWS + row]) = make_float4(y[0], y[1], y[2], y[3]);
   }
+}
+
+template <int DK>
+cudaError_t join_as(const ChunkArgs& a, const float* given, bool reverse, int B, cudaStream_t stream) {
+  constexpr int smem = (2 * DK * DK + 9 * 1024) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  delta_join_kernel<DK><<<(unsigned)(B * a.H * (a.dv * DK / 1024)), 256, smem, stream>>>(a, given, reverse ? a.seg_xt : a.seg_x, reverse);
+  return cudaGetLastError();
 }
 
 template <int DK, int DV, int KIND, bool PIECES = false>
@@ -642,20 +681,21 @@ cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t
 }
 template <int DK, int DV>
 cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
+  if (a.segs > 1) {
+    cudaError_t e = launch<DK, DV, kStateOnly>(m, a, B, stream);
+    if (e == cudaSuccess) e = join_states(a, a.s_in, false, B, DK, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (a.s0 != nullptr)
     return a.pieces > 1 ? launch<DK, DV, kImages, true>(m, a, B, stream) : launch<DK, DV, kImages>(m, a, B, stream);
-  if (a.segs > 1) {
-    const cudaError_t e = launch<DK, DV, kStateOnly>(m, a, B, stream);
-    if (e != cudaSuccess) return e;
-    constexpr int smem = (2 * DK * DK + 16 * DK) * 4;
-    const cudaError_t f = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (f != cudaSuccess) return f;
-    delta_join_kernel<DK><<<(unsigned)(B * a.H * (DV / 16)), 256, smem, stream>>>(a);
-  }
   return a.pieces > 1 ? launch<DK, DV, kO, true>(m, a, B, stream) : launch<DK, DV, kO>(m, a, B, stream);
 }
 
 }  // namespace chaintc
+
+cudaError_t join_states(const ChunkArgs& a, const float* given, bool reverse, int B, int dk, cudaStream_t stream) {
+  return dk == 128 ? chaintc::join_as<128>(a, given, reverse, B, stream) : chaintc::join_as<64>(a, given, reverse, B, stream);
+}
 
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream) {
   CUtensorMap m[4];
@@ -685,17 +725,19 @@ int chain_pieces(long long units, int chunks, double whole, double cut) {
   return best;
 }
 
-// Segments of a sequence, by the time of both passes in chunk steps (2.3 us
-// each): a wave of CTAs per 148 units and segments, about one step per segment
-// for the join, six for two more launches.  One sequence of 16384 tokens and 16
-// heads: 637 us in one piece, 245 us in six (103 + 23 + 120).
-int chain_segments(long long units, int chunks) {
+// Segments of a sequence, by an estimate in us: a wave of CTAs is 148, a chunk takes
+// 2.3 us for the maps and 2.6 for O, a CTA 6 beside its chunks, a segment 1.6 in the
+// join, the two more launches 6.  One sequence of 16384 tokens: 16 heads 650 us in
+// one piece, 238 in six (104 + 16 + 119), 271 in eight (two waves of maps); of 4096
+// tokens: 2 heads 171 us in one, 65 in eight, 60 in twelve.
+int chain_segments(long long units, int chunks, long long join_ctas) {
+  auto waves = [](long long ctas) { return (double)((ctas + 147) / 148); };
   int best = 1;
-  double least = 0.9 * chunks;
+  double least = 0.95 * waves(units) * (2.6 * chunks + 6);
   for (int g = 3; g <= 64 && g * 2 <= chunks; ++g) {
     const int per = (chunks + g - 1) / g;
-    const long long w1 = (units * (2 * g - 3) + 147) / 148, w2 = (units * g + 147) / 148;
-    const double t = per * (0.9 * w1 + w2) + g + 6;
+    const double t = waves(units * (2 * g - 3)) * (2.3 * per + 6) + waves(units * g) * (2.6 * per + 6) +
+                     1.6 * (g - 1) * waves(join_ctas) + 6;
     if (t < least) {
       least = t;
       best = g;

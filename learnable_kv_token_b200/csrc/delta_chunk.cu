@@ -23,7 +23,7 @@ struct PrefillLayout {
   explicit PrefillLayout(const lte_gdr_dims* d) {
     const size_t units = (size_t)d->B * d->H, state = (size_t)d->dv * d->dk * 4;
     chunks = (d->T + delta::L - 1) / delta::L;
-    segs = delta::chain_segments((long long)units, chunks);
+    segs = delta::chain_segments((long long)units, chunks, (long long)units * d->dv * d->dk / 1024);
     pieces = segs > 1 ? 1 : delta::chain_pieces((long long)units, chunks, 3, 4.5);
     size_t at = units * chunks * delta::rec_bytes(false);
     auto take = [&](size_t bytes) { const size_t r = (at + 255) & ~(size_t)255; at = r + bytes; return r; };

@@ -98,14 +98,17 @@ struct ChunkArgs {
   uint32_t *s0, *u;      // images of S_0 (hi, lo) and U (hi, lo) per chunk, for the gradients
   int T, H, Hk, dv, chunks;
   float scale;
-  // segments (forward only; segs = 1: the sequence in one piece): chunks of each,
-  // n [units][segs - 1][dv][dk], X [units][segs - 2][dk][dk], states [units][segs][dv][dk]
+  // segments (segs = 1: the sequence in one piece): chunks of each, n [units][segs - 1][dv][dk],
+  // X [units][segs - 2][dk][dk], states [units][segs][dv][dk], each in the chain's order
+  // (backward: n of the last segment first); for the gradients X transposed too, and the
+  // records hold A's lo
   int segs, seg_chunks;
+  bool a_lo;
   // or pieces that follow one another (pieces = 1: one; seg_chunks: chunks of each): the
   // next piece's number and, per unit, its pieces that are done, each for the forward and
   // the backward chain (prepare sets all to zero)
   int pieces, *turn, *done;
-  float *seg_n, *seg_x, *seg_s;
+  float *seg_n, *seg_x, *seg_xt, *seg_s;
 };
 
 struct GradArgs {
@@ -127,7 +130,10 @@ struct GradArgs {
 cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t stream);
 // delta_chain_tc.cu: the chain of states with O; with s0 and u, writes their images instead of O
 cudaError_t forward_chain(const ChunkArgs& a, int B, int dk, cudaStream_t stream);
-int chain_segments(long long units, int chunks);
+// join_ctas: of the join of all units (units dv dk / 1024)
+int chain_segments(long long units, int chunks, long long join_ctas);
+// the states that the segments start from (seg_s), by n, X and the one given; reverse: the gradients, by X transposed
+cudaError_t join_states(const ChunkArgs& a, const float* given, bool reverse, int B, int dk, cudaStream_t stream);
 // `whole`, `cut`: what a CTA costs beside its chunks, in chunk steps, without and with a state to hand over
 int chain_pieces(long long units, int chunks, double whole, double cut);
 inline size_t piece_bytes(size_t units) { return (2 + 2 * units) * 4; }   // turn, then done

@@ -258,6 +258,14 @@ def test_backward(layer, shape):
     check_backward(layer, inputs(100 + sum(shape), *shape, init=shape[1] % 2 == 1), dstate=shape[0] == 1)
 
 
+@pytest.mark.parametrize("shape,lens", [((1, 2100, 2, 1, 128, 64), None), ((2, 1601, 1, 1, 64, 128), [1601, 700]),
+                                        ((4, 2048, 1, 1, 128, 128), [2048, 0, 1, 1025]),
+                                        ((3, 2000, 2, 2, 64, 64), [256, 257, 2000])], ids=str)
+def test_backward_long_few_heads(layer, shape, lens):
+    """Sequences that are cut into segments, which end in any of them."""
+    check_backward(layer, inputs(110 + shape[1], *shape, lens=lens))
+
+
 @pytest.mark.parametrize("lens", [[0, 1, 130], [64, 130, 63], [129, 0, 65]], ids=str)
 def test_backward_padded_batch(layer, lens):
     x = inputs(10, 3, 130, 4, 2, 128, 128, lens=lens, fused=True)
