@@ -113,7 +113,10 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 17 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
-    if (PIECES) *ticket = atomicAdd(a.turn + 1, 1);
+    if (PIECES) {
+      after_previous();
+      *ticket = atomicAdd(a.turn + 1, 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   write_identity(sm + kIdent, kThreads);
@@ -126,6 +129,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = *tmem_slot;
   // the unit, and its chunks cb .. cb + n - 1 (pieces from the last to the first; dS alone of segments 1 on)
   const int units = PIECES ? gridDim.x / a.pieces : 1, per = STATE ? a.segs - 1 : SEG ? a.segs : 1;
@@ -719,11 +723,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
 template <int DK, int DV, int KIND>
 cudaError_t launch_as(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<DK, DV, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
   const int per = KIND == kSegState ? a.f.segs - 1 : a.f.segs * a.f.pieces;
-  delta_back_tc_kernel<DK, DV, KIND><<<(unsigned)(B * a.f.H * per), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
-  return cudaGetLastError();
+  return launch_after(delta_back_tc_kernel<DK, DV, KIND>, (unsigned)(B * a.f.H * per), kThreads, kSmem, stream, m[0], m[1], m[2],
+                      m[3], m[4], a);
 }
 template <int DK, int DV>
 cudaError_t launch(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {

@@ -91,7 +91,10 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       mbar_init(bar(i), i == bEmpty || i == bEmpty + 1 ? 13 : chain ? 8 : out ? 4 : 1);
     }
     *abort_flag = 0;
-    if (PIECES) *ticket = atomicAdd(a.turn, 1);
+    if (PIECES) {
+      after_previous();
+      *ticket = atomicAdd(a.turn, 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   write_identity(sm + kIdent, kThreads);
@@ -104,6 +107,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = *tmem_slot;
   // the unit's segment: for kStateOnly first n of segments 0 .. G - 2, then X of 1 .. G - 2;
   // or its piece, all first pieces before all second ones
@@ -604,6 +608,7 @@ delta_join_kernel(const ChunkArgs a, const float* given, const float* xs, bool r
     }
     cp_async_commit();
   };
+  after_previous();
   fetch(1);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -665,19 +670,15 @@ delta_join_kernel(const ChunkArgs a, const float* given, const float* xs, bool r
 template <int DK>
 cudaError_t join_as(const ChunkArgs& a, const float* given, bool reverse, int B, cudaStream_t stream) {
   constexpr int smem = (2 * DK * DK + 9 * 1024) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  delta_join_kernel<DK><<<(unsigned)(B * a.H * (a.dv * DK / 1024)), 256, smem, stream>>>(a, given, reverse ? a.seg_xt : a.seg_x, reverse);
-  return cudaGetLastError();
+  const float* x = reverse ? a.seg_xt : a.seg_x;
+  return launch_after(delta_join_kernel<DK>, (unsigned)(B * a.H * (a.dv * DK / 1024)), 256, smem, stream, a, given, x, reverse);
 }
 
 template <int DK, int DV, int KIND, bool PIECES = false>
 cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_chain_tc_kernel<DK, DV, KIND, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
   const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
-  delta_chain_tc_kernel<DK, DV, KIND, PIECES><<<(unsigned)(B * a.H * per * a.pieces), kThreads, kSmem, stream>>>(m[0], m[1], m[2], m[3], a);
-  return cudaGetLastError();
+  return launch_after(delta_chain_tc_kernel<DK, DV, KIND, PIECES>, (unsigned)(B * a.H * per * a.pieces), kThreads, kSmem, stream,
+                      m[0], m[1], m[2], m[3], a);
 }
 template <int DK, int DV>
 cudaError_t run(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {

@@ -86,6 +86,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = seq_len(a.lens, b, a.T), t0 = c * L;
+  if (gridDim.x <= 6 * 74) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.pieces > 1 && c == 0 && tid == 0) {
     a.done[u] = a.done[gridDim.x / a.chunks + u] = 0;
     if (u == 0) a.turn[0] = a.turn[1] = 0;
