@@ -464,6 +464,26 @@ def test_gradients_on_two_streams_at_once(layer):
             assert torch.equal(i, j)
 
 
+@pytest.mark.parametrize("shape", [(1, 2000, 2, 1, 64, 64), (40, 1500, 4, 2, 64, 64)], ids=str)
+def test_segments_and_pieces_of_gradients_in_a_graph(layer, shape):
+    """Captured once, replayed twice with other inputs: the pieces' counters start anew every time."""
+    x, y = inputs(68, *shape), inputs(69, *shape)
+    names = ("q", "k", "v", "g", "beta")
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    first, want = (layer.delta_backward(*(z[n] for n in names), do, state=z["state"]) for z in (x, y))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer.delta_backward(*(x[n] for n in names), do, state=x["state"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, first))
+    for n in (*names, "state"):
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_offsets_past_32_bits(layer):
     """A sequence whose tensors have over 2^31 elements: its last tokens, and the state, equal those of
     the same tokens in a call of their own behind the state of the others."""
