@@ -39,7 +39,7 @@ constexpr int kThreads = 640;
 // a stage: K, Q, dO, V (two halves each), the record's T hi, T lo, A hi, A lo, scalars
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kD = 4 * kHalf, kV = 6 * kHalf, kR = 8 * kHalf;
 constexpr uint32_t kScalOff = kR + 4 * kImg;
-constexpr uint32_t kStage = (kScalOff + kScal + 1023) / 1024 * 1024;
+constexpr uint32_t kStage = (kScalOff + kGradScal + 1023) / 1024 * 1024;
 // then the identity and the last 32 of 128 key channels of a state (128 rows, hi and lo)
 constexpr uint32_t kIdent = 2 * kStage, kState = kIdent + kImg, kBars = kState + 2 * 128 * 64, kSmem = kBars + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -153,7 +153,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const bool tail = c * L + L > len;                       // the first one to come
       const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
       if (elect_one()) {
-        mbar_expect_tx(fb, (2 * kHK + (STATE ? 1 : 2) * kHV) * kHalf + 4 * kImg + kScal);
+        mbar_expect_tx(fb, (2 * kHK + (STATE ? 1 : 2) * kHV) * kHalf + 4 * kImg + kGradScal);
         for (int j = 0; j < kHK; ++j) {
           tma_load_4d(d + kK + j * kHalf, &tm_k, fb, 64 * j, hk, c * L, b);
           tma_load_4d(d + kQ + j * kHalf, &tm_q, fb, 64 * j, hk, c * L, b);
@@ -162,7 +162,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tma_load_4d(d + kD + j * kHalf, &tm_d, fb, 64 * j, h, c * L, b);
           if (!STATE) tma_load_4d(d + kV + j * kHalf, &tm_v, fb, 64 * j, h, c * L, b);
         }
-        bulk_load(d + kR, recs + (long long)c * rec_bytes(true), 4 * kImg + kScal, fb);
+        bulk_load(d + kR, recs + (long long)c * rec_bytes(true), 4 * kImg + kGradScal, fb);
       }
       if (!STATE) {                                            // the images that the output warps read: to L2, a piece per lane
         const long long img = (long long)u * a.chunks + c;
@@ -668,8 +668,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const uint32_t a0 = colv + t * 128 + ((cv ^ (t & 7)) << 4), a1 = colv + (t + 1) * 128 + ((cv ^ ((t + 1) & 7)) << 4);
                 const uint32_t v0 = *reinterpret_cast<const uint16_t*>(sm + s * kStage + kV + a0);
                 const uint32_t v1 = *reinterpret_cast<const uint16_t*>(sm + s * kStage + kV + a1);
-                z[k] = f0 * (bf_lo(wh[f]) + bf_lo(wl[f]));
-                z[k + 1] = f1 * (bf_hi(wh[f]) + bf_hi(wl[f]));
+                const float2 ib = *reinterpret_cast<const float2*>(scal + kInvB * L + t);
+                z[k] = (f0 * ib.x) * (bf_lo(wh[f]) + bf_lo(wl[f]));
+                z[k + 1] = (f1 * ib.y) * (bf_hi(wh[f]) + bf_hi(wl[f]));
                 z[16 + k] = f0 * bf_lo(v0);
                 z[17 + k] = f1 * bf_lo(v1);
                 w[f] = pack_bf16(f0, f1);
@@ -679,9 +680,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               }
               *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            const float sum = lane_sums(z, lane);              // lanes 0-15: u.F, 16-31: v.F of token lane mod 16
+            const float sum = lane_sums(z, lane);              // lanes 0-15: u.F / b, 16-31: v.F of token lane mod 16
             const int t = 16 * j + (lane & 15);
-            xp[(lane >> 4) * L + t] = lane < 16 ? sum / scal[kBeta * L + t] : sum;
+            xp[(lane >> 4) * L + t] = sum;
             xp[2 * L + (lane >> 4) * L + t] = 0.f;             // the warp's second strip of 16
           }
         }

@@ -32,15 +32,19 @@ constexpr int L = 64;
 // diagonal is b; T's rows act on R mostly through it, so it stays in fp32 and
 // the bf16 pairs' error falls on the rest), A as hi (and lo, for the gradients),
 // each a [64][64] bf16 image in the swizzled order in which it lies in shared
-// memory, then five rows of 64 floats.
+// memory, then five rows of 64 floats, and a sixth for the gradients.
 constexpr int kImg = L * L * 2;
 constexpr int kScal = 5 * L * 4;
 constexpr int kEG = 0, kLam = 1, kBeta = 2, kGhi = 3, kGlo = 4;   // e^G, e^{G_L - G}, b, G as a float pair
-__host__ __device__ constexpr int rec_bytes(bool a_lo) { return (a_lo ? 4 : 3) * kImg + kScal; }
+constexpr int kInvB = 5;                                          // 1 / b
+constexpr int kGradScal = kScal + L * 4;
+__host__ __device__ constexpr int rec_bytes(bool a_lo) { return a_lo ? 4 * kImg + kGradScal : 3 * kImg + kScal; }
 
 // A correction of b = 0 is exactly zero; it is carried as u = 2^-60 e instead,
 // far below what fp32 sums beside it can see, so that e = u / b always exists
-// (the gradient of b is y.e).
+// (the gradient of b is y.e).  F = b y is as small, so it is divided by b before it
+// meets u: a product of both would be 2^-120 y e, and gradients of 1e-6 would
+// leave the range of fp32's digits.
 __device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-60f ? 0x1p-60f : b; }
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }

@@ -145,6 +145,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     out[kEG * 32] = make_float2(expf((float)G0), expf((float)G1));
     out[kLam * 32] = make_float2(expf((float)(last - G0)), expf((float)(last - G1)));
     out[kBeta * 32] = make_float2(b0, b1);
+    if (A_LO) out[kInvB * 32] = make_float2(1.f / b0, 1.f / b1);
     out[kGhi * 32] = make_float2((float)G0, (float)G1);
     out[kGlo * 32] = make_float2((float)(G0 - (float)G0), (float)(G1 - (float)G1));
   }
@@ -319,7 +320,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   } else {
     // a wait gave up: the chunk's scalars turn everything behind them into NaN;
     // the copies in flight land before exit
-    for (int i = tid; i < 5 * L; i += kPrepThreads) scal[i] = NAN;
+    for (int i = tid; i < (A_LO ? kGradScal : kScal) / 4; i += kPrepThreads) scal[i] = NAN;
     if (tid == 0) mbar_drain(bar_in, 0);
   }
   tc_fence_before();

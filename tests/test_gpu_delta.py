@@ -288,6 +288,29 @@ def test_backward_extreme_gates(layer, kind):
     check_backward(layer, x)
 
 
+@pytest.mark.parametrize("size", [1e-6, 1e-9])
+@pytest.mark.parametrize("beta", ["0", "1e-20", "1e-15", "some-0"])
+def test_small_gradients_of_small_betas(layer, beta, size):
+    """Gradients behind a mean loss are small, and a token that writes nothing has one all the same: they
+    scale with dO and dstate, so the bounds are those of gradients of order one."""
+    x = inputs(23, 2, 150, 4, 2, 128, 128)
+    if beta == "some-0":
+        x["beta"][:, ::3] = 0
+    else:
+        x["beta"][:] = float(beta)
+    g = torch.Generator().manual_seed(7)
+    do = (torch.randn(x["v"].shape, generator=g) * size).bfloat16().cuda()
+    dS = (torch.randn(x["state"].shape, generator=g) * 0.2 * size).cuda()
+    args = (x["q"], x["k"], x["v"], x["g"], x["beta"], do)
+    got = layer.delta_backward(*args, state=x["state"], dstate=dS)
+    ref = DO.delta_backward(*(f64(t) for t in args), f64(x["state"]), f64(dS))
+    # (dk and dv of tokens that write next to nothing are next to nothing: not held to a share of themselves)
+    tols = dict(dq=GRAD_TOL, dk=GRAD_TOL, dv=BF16_TOL, dg=GATE_TOL, dbeta=GATE_TOL, dstate=STATE_TOL)
+    for a, r, name in zip(got, ref, tols):
+        if beta == "some-0" or name not in ("dk", "dv"):
+            assert rel(a, r) <= tols[name], f"{name}: {rel(a, r):.3g} > {tols[name]:.3g}"
+
+
 def test_backward_by_differences(layer):
     """The gradient of every input along a random direction against a central difference of the
     forward pass, with steps of h = 0.05 of the input's norm along the gradient.
