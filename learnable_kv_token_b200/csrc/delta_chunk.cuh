@@ -40,9 +40,10 @@ constexpr int kInvB = 5;                                          // 1 / b
 constexpr int kGradScal = kScal + L * 4;
 __host__ __device__ constexpr int rec_bytes(bool a_lo) { return a_lo ? 4 * kImg + kGradScal : 3 * kImg + kScal; }
 
-// A correction of b = 0 is exactly zero; it is carried as u = 2^-60 e instead,
-// far below what fp32 sums beside it can see, so that e = u / b always exists
-// (the gradient of b is y.e).  F = b y is as small, so it is divided by b before it
+// A correction of b = 0 is exactly zero.  The gradients carry it as u = 2^-60 e
+// instead, far below what fp32 sums beside it can see, so that e = u / b always
+// exists (the gradient of b is y.e); the prompt takes b as it is, so that a token
+// of b = 0 writes nothing at all.  F = b y is as small, so it is divided by b before it
 // meets u: a product of both would be 2^-120 y e, and gradients of 1e-6 would
 // leave the range of fp32's digits.
 __device__ __forceinline__ float live_beta(float b) { return fabsf(b) < 0x1p-60f ? 0x1p-60f : b; }

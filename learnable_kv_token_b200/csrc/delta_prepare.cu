@@ -120,12 +120,12 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (t0 + 2 * lane < len) {
       const float x = a.g[gi];
       x0 = x < -104.f ? -104.f : x;                       // e^-104 is 0 in fp32
-      b0 = live_beta(a.beta[gi]);
+      b0 = A_LO ? live_beta(a.beta[gi]) : a.beta[gi];
     }
     if (t0 + 2 * lane + 1 < len) {
       const float x = a.g[gi + a.H];
       x1 = x < -104.f ? -104.f : x;
-      b1 = live_beta(a.beta[gi + a.H]);
+      b1 = A_LO ? live_beta(a.beta[gi + a.H]) : a.beta[gi + a.H];
     }
     double sum = x0 + x1;
 #pragma unroll

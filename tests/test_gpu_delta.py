@@ -136,6 +136,21 @@ def test_prefill_extreme_gates(layer, dtype, kind):
     check_prefill(layer, x, scale)
 
 
+@pytest.mark.parametrize("init", [False, True])
+def test_tokens_of_beta_0_write_nothing(layer, init):
+    """As in the step and in the walk by tokens: the state only decays, and stays exactly zero from zero."""
+    x = inputs(24, 2, 150, 4, 2, 128, 64, init=init)
+    x["beta"][:] = 0.0
+    o, S = layer.delta_prefill(*(x[n] for n in ("q", "k", "v", "g", "beta")), state=x["state"])
+    if not init:
+        assert (o == 0).all() and (S == 0).all()
+    else:
+        # per chunk the decay's factor, with two units in its last place of the exponential (4 x 2^-24) and its
+        # argument's rounding (the states that are not gone by then have |G| < 1: 2^-24), and the product's
+        want = f64(x["state"]) * np.exp(f64(x["g"]).sum(1))[..., None, None]
+        assert rel(S, want) <= 2.0 ** -24 * 6 * 3
+
+
 @pytest.mark.parametrize("shape,lens", [((1, 2600, 2, 1, 128, 128), None), ((2, 3000, 1, 1, 64, 128), [2999, 700]),
                                         ((1, 1500, 1, 1, 128, 64), None), ((3, 1100, 1, 1, 64, 64), [0, 1100, 64])],
                          ids=str)
