@@ -563,6 +563,27 @@ lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k,
 lte_status lte_gdr_zero_padding(int32_t B, int32_t T, const int32_t* lens, int32_t n,
                                 void* const* tensors, const int64_t* row_bytes, void* stream);
 
+/* lte_gdr_withhold -- diagnostic: shows on the live device what a wait that runs
+ * out leaves.  In later calls' launches of the given kinds (LTE_GDR_LAUNCH_* or'd;
+ * 0 = none) every CTA leaves out the loads of the chunk that it takes as number
+ * `chunk` (>= 0), and waits give up after limit_ns (1e3 .. 1e9) instead of one
+ * second.  Process-wide, not for use beside calls of other threads; a captured call
+ * keeps what it was captured with.
+ * A wait that runs out, for whatever reason, ends its CTA and leaves NaN in
+ * everything that is not as it would have been: the rows of o of its sequence, head
+ * and stretch of chunks; the state if that is not final; every gradient of its
+ * chunks, and of those that they reach.  Errors: INVALID_ARG. */
+enum {
+  LTE_GDR_LAUNCH_PREPARE = 1,        /* what depends on no state */
+  LTE_GDR_LAUNCH_SEGMENTS = 2,       /* maps of the segments */
+  LTE_GDR_LAUNCH_CHAIN = 4,          /* states, with o or what the gradients need */
+  LTE_GDR_LAUNCH_BACK_SEGMENTS = 8,  /* the segments' gradients of states */
+  LTE_GDR_LAUNCH_BACK = 16,          /* gradients of states, and of v */
+  LTE_GDR_LAUNCH_PASS = 32,          /* gradients of q, k, g and beta */
+  LTE_GDR_LAUNCH_ALL = 63
+};
+lte_status lte_gdr_withhold(int32_t launches, int32_t chunk, int64_t limit_ns);
+
 /* lte_gdr_decode_step -- one token per sequence (d->T is ignored): q_t, k_t
  * [B,Hk,dk], v_t, o_t [B,H,dv], g_t, beta_t fp32 [B,H], all contiguous; state is
  * updated in place.  fp32 arithmetic for both dtypes. */

@@ -104,6 +104,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
   volatile int* ticket = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* flight = ticket + 1;                           // chunks and states requested; MMAs issued
   auto bar = [&](int i) { return bars + 8 * i; };
 
   if (tid == 0) {
@@ -139,16 +140,17 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
   const int len = seq_len(a.lens, b, a.T);
   const int n = PIECES || SEG ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
-  bool ok = true, issued = false;
-  int loaded = 0;
+  bool ok = true;
 
   if (warp >= 16) regs_dec<48>();
   if (warp == 16) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + (long long)u * a.chunks * rec_bytes(true);
-    for (int i = 0; i < n; ++i) {
+    const int n_load = (unsigned)a.withhold < (unsigned)n ? a.withhold : n;
+    int loaded = 0, states = 0;
+    for (int i = 0; i < n_load; ++i) {
       const int s = i & 1, c = cb + n - 1 - i;
-      if (i >= 2 && !(ok = wwait(bar(bEmpty + s), ((i >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (i >= 2 && !(ok = wwait(bar(bEmpty + s), ((i >> 1) - 1) & 1, a.wait_ns, abort_flag))) break;
       const uint32_t d = s0 + s * kStage;
       const bool tail = c * L + L > len;                       // the first one to come
       const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
@@ -171,7 +173,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       ++loaded;
       if (DK == 128 && !STATE && i > 0) {                      // the state of the chunk behind, key channels 96 on
-        if (i > 1 && !(ok = wwait(bar(bStFree), i & 1, abort_flag, nullptr, 0))) break;
+        if (i > 1 && !(ok = wwait(bar(bStFree), i & 1, a.wait_ns, abort_flag))) break;
         if (lane == 0) mbar_expect_tx(bar(bSt), DV / 8 * 2 * 512);
         __syncwarp();
         const int rb = lane & 15, p = lane >> 4;               // a lane per eight rows of hi or lo
@@ -179,9 +181,10 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           bulk_load(s0 + kState + p * (128 * 64) + rb * 512,
                     reinterpret_cast<const uint8_t*>(a.s0) + ((long long)u * a.chunks + c + 1) * (DV * DK * 4) + p * (DV * DK * 2) +
                         rb * (DK / 8) * 128 + 12 * 128, 512, bar(bSt));
+        ++states;
       }
       if (tail) {
-        if (!(ok = wwait(fb, 0, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(fb, 0, a.wait_ns, abort_flag))) break;
         const int r0 = len - c * L;
         uint8_t* st = sm + s * kStage;
         for (int j = 0; j < kHK; ++j) {
@@ -197,21 +200,26 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (lane == 0) mbar_arrive(bar(bFull + s));
       }
     }
+    if (lane == 0) {
+      flight[kFlightLoads] = loaded;
+      flight[kFlightStates] = states;
+    }
   } else if (warp == 17) {
     // ================================================================= MMAs
     const uint32_t id_tok = idesc2(128, L, false, false), id_dt = idesc2(128, L, true, false);
     const uint32_t id_s = idesc2(128, 64, false, true);
     const uint64_t ident = sdesc(s0 + kIdent, 16, 1024);
+    int issued = 0;
     for (int i = 0; i < n; ++i) {
       const int s = i & 1, ph = i & 1;
       const uint32_t d = s0 + s * kStage;
-      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, a.wait_ns, abort_flag))) break;
       tc_fence_after();
-      issued = true;
+      issued = 1;
       const uint64_t dk = sdesc(d + kK, 16, 1024), dd = sdesc(d + kD, kHalf, 1024), dt = sdesc(d + kR, kHalf, 1024);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {                            // P = dS K^T, by halves of dS's columns
-        if (ok) ok = wwait(bar(bSr + p), ph, abort_flag, nullptr, 0);
+        if (ok) ok = wwait(bar(bSr + p), ph, a.wait_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -226,7 +234,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       if (!ok) break;
       // (X's columns still hold the F of the chunk before until its sums have been taken)
-      if (!STATE && i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!STATE && i > 0 && !(ok = wwait(bar(bXf), (i - 1) & 1, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // X = dO^T A, and dO^T
 #pragma unroll
@@ -241,7 +249,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           mma_f16(tmem + kColD, dd + ((ks * 2048) >> 4), ident + ((ks * 32) >> 4), id_dt, ks > 0);
         mma_commit(bar(bD));
       }
-      if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bUr), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // F = dU T, columns s < 16 (ks + 1)
 #pragma unroll
@@ -252,7 +260,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                        idesc2(128, 16 * (ks + 1), false, true), !(p == 0 && ks == L / 16 - 1));
         mma_commit(bar(bF));
       }
-      if (!(ok = wwait(bar(bDr), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bDr), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // dS += (scale e^G dO)^T Q
 #pragma unroll
@@ -264,7 +272,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               mma_f16_ts(tmem + kColS + 64 * m, tmem + kColD + pair_col(ks, p),
                          sdesc(d + kQ + m * kHalf, kHalf, 1024) + ((ks * 2048) >> 4), id_s, 1u);
       }
-      if (!(ok = wwait(bar(bFr), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bFr), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // dS -= (e^G F)^T K, by halves of its columns
 #pragma unroll
@@ -281,12 +289,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (i + 2 < n) mma_commit(bar(bEmpty + s));            // the stage is loaded once more
       }
     }
-    if (!ok && issued) {                                       // MMAs in flight end before exit
-      __syncwarp();
-      if (elect_one()) mma_commit(bar(bDrain));
-      __syncwarp();
-      mbar_drain(bar(bDrain), 0);
-    }
+    if (lane == 0) flight[kFlightMma] = issued;
   } else if (warp < 8) {
     // ========================================================== chain warps
     regs_inc<112>();
@@ -302,7 +305,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     };
     {                                                          // the gradient behind, while the last chunk loads
       const bool later = PIECES && n > 0 && (cb + n) * L < len;
-      if (later) ok = piece_ready(a.done + units + u, piece, abort_flag);
+      if (later) ok = piece_ready(a.done + units + u, piece, a.wait_ns, abort_flag);
       const float* src = later ? ga.hand + srow : STATE && seg < a.segs - 1 ? nullptr : ga.ds_out;
       if (SEG && !STATE) src = a.seg_s + ((long long)u * a.segs + a.segs - 1 - seg) * DV * DK + (row < DV ? row : 0) * DK;
       else if (!later && src != nullptr) src += srow;
@@ -325,17 +328,17 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     for (int i = 0; ok && i < n; ++i) {
       const int s = i & 1, ph = i & 1;
-      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, a.wait_ns, abort_flag))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       // ---- dS as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
-      if (!STATE && i > 0 && !(ok = wwait(bar(bSread), (i - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!STATE && i > 0 && !(ok = wwait(bar(bSread), (i - 1) & 1, a.wait_ns, abort_flag))) break;
       const float el = scal[kEG * L + L - 1];
       const uint64_t el2 = f2(el, el);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
         uint64_t S[QC / 2];
-        if (i > 0 && ok) ok = wwait(bar(bS + p), (i - 1) & 1, abort_flag, nullptr, 0);
+        if (i > 0 && ok) ok = wwait(bar(bS + p), (i - 1) & 1, a.wait_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         {
@@ -366,7 +369,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (!ok) break;
       // ---- dU = P diag(e^{G_L - G}) + X, tokens 32 hc .. + 31
       uint64_t U[16];
-      if (!(ok = wwait(bar(bX), ph, abort_flag, nullptr, 0) && wwait(bar(bP), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bX), ph, a.wait_ns, abort_flag) && wwait(bar(bP), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       {
         uint32_t hi[16], lo[16];
@@ -396,7 +399,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         U[2 * e] = mul2(U[2 * e], f2(g.x, g.y));
         U[2 * e + 1] = mul2(U[2 * e + 1], f2(g.z, g.w));
       }
-      if (!(ok = wwait(bar(bF), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bF), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       {
         uint32_t hi[16], lo[16];
@@ -434,7 +437,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
     }
     if (ok && n > 0) {
-      ok = wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0);
+      ok = wwait(bar(bS), (n - 1) & 1, a.wait_ns, abort_flag) && wwait(bar(bS + 1), (n - 1) & 1, a.wait_ns, abort_flag);
       tc_fence_after();
     }
     float* dst = cb == 0 ? ga.ds_in : PIECES && n > 0 ? ga.hand : nullptr;
@@ -457,7 +460,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
         }
       }
-      if (PIECES && cb > 0) piece_done(a.done + units + u, piece, 2, 256);
+      if (PIECES && cb > 0) piece_done(a.done + units + u, piece, ok, 2, 256);
     }
   } else if (warp < 16) {
     // ================================================= the two output groups
@@ -484,7 +487,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       };
       for (int i = 0; i < n; ++i) {
         const int s = i & 1, ph = i & 1, c = cb + n - 1 - i;
-        if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bFull + s), (i >> 1) & 1, a.wait_ns, abort_flag))) break;
         const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
         // the state of the chunk behind, hi and lo, 16 key channels at a time, asked for
         // kAhead pieces ahead of their use: as much in flight as registers hold
@@ -502,7 +505,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) fetch_state(j);
         // scale e^G dO^T as hi and lo
-        if (!(ok = wwait(bar(bD), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bD), ph, a.wait_ns, abort_flag))) break;
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -531,7 +534,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         if (STATE) continue;
         // dS: its image (hi), and <dS, S_0> with the state of the chunk behind
-        if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bSr), ph, a.wait_ns, abort_flag) && wwait(bar(bSr + 1), ph, a.wait_ns, abort_flag))) break;
         tc_fence_after();
         float in = 0.f;
         uint8_t* im = d_img + (long long)c * (DV * DK * 2);
@@ -552,7 +555,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             for (int e = 0; e < 2; ++e)
               *reinterpret_cast<uint4*>(im + (2 * j + e) * 128) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
           }
-          if (j == kPieces && i > 0 && ok) ok = wwait(bar(bSt), (i - 1) & 1, abort_flag, nullptr, 0);
+          if (j == kPieces && i > 0 && ok) ok = wwait(bar(bSt), (i - 1) & 1, a.wait_ns, abort_flag);
           if (inner) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -579,8 +582,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (i > 0) put_inner(c + 1, in);
       }
       // the gradient of the (piece's) initial state with that state
-      if (!STATE && ok && n > 0 && wwait(bar(bS), (n - 1) & 1, abort_flag, nullptr, 0) &&
-          wwait(bar(bS + 1), (n - 1) & 1, abort_flag, nullptr, 0)) {
+      if (!STATE && ok && n > 0 && wwait(bar(bS), (n - 1) & 1, a.wait_ns, abort_flag) &&
+          wwait(bar(bS + 1), (n - 1) & 1, a.wait_ns, abort_flag)) {
         tc_fence_after();
         float in = 0.f;
 #pragma unroll
@@ -621,7 +624,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int s = i & 1, ph = i & 1, c = cb + n - 1 - i;
         const long long img = (long long)u * a.chunks + c;
         // (a warp whose wait gave up still meets the others at the vote below)
-        ok = wwait(bar(bFull + s), (i >> 1) & 1, abort_flag, nullptr, 0);
+        ok = wwait(bar(bFull + s), (i >> 1) & 1, a.wait_ns, abort_flag);
         if (STATE) {
           if (!ok) break;
           if (lane == 0) mbar_arrive(bar(bEmpty + s));
@@ -638,7 +641,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
         };
         if (mine) fetch_u(0);
-        ok = ok && wwait(bar(bFx), ph, abort_flag, nullptr, 0);
+        ok = ok && wwait(bar(bFx), ph, a.wait_ns, abort_flag);
         tc_fence_after();
         if (!(ok = bar_and(1, 128, ok))) break;
         uint8_t* im = f_img + (long long)c * (DV * L * 2);
@@ -709,21 +712,43 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
   }
   if (tid == 384) bulk_wait_read();                            // output stores have left shared memory
-  // copies in flight land before exit (only after a wait gave up)
-  if (warp == 16 && *abort_flag) {
-    for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
-      if ((cb + n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
-      else mbar_drain(bar(bTail), 0);
-    if (DK == 128 && !STATE && loaded > 1) mbar_drain(bar(bSt), (loaded - 2) & 1);
-  }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {                                           // a wait gave up: as in the forward chain
+    const int id = PIECES ? *ticket : block_again(), units = PIECES ? gridDim.x / a.pieces : 1;
+    const int per = STATE ? a.segs - 1 : SEG ? a.segs : 1, u = PIECES ? id % units : id / per;
+    const int cb = PIECES ? (a.pieces - 1 - id / units) * a.seg_chunks : SEG ? (id % per + STATE) * a.seg_chunks : 0;
+    const int b = u / a.H, h = u % a.H, len = seq_len(a.lens, b, a.T);
+    const int n = PIECES || SEG ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
+    if (warp == 17 && flight[kFlightMma]) {
+      if (elect_one()) mma_commit(bar(bDrain));
+      __syncwarp();
+      mbar_drain(bar(bDrain), 0);
+    }
+    if (warp == 16) {
+      for (int m = flight[kFlightLoads], i = max(m - 2, 0); i < m; ++i)
+        if ((cb + n - 1 - i) * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
+        else mbar_drain(bar(bTail), 0);
+      if (flight[kFlightStates] > 0) mbar_drain(bar(bSt), (flight[kFlightStates] - 1) & 1);
+    }
+    if (tid == 384) bulk_wait_all();
+    __syncthreads();
+    if (!STATE) {
+      const long long t0 = (long long)cb * L;
+      nan_rows<DV>(ga.dv + ((b * (long long)a.T + t0) * a.H + h) * DV, (long long)a.H * DV, min(len - cb * L, n * L), tid, kThreads);
+      nan_records(a.rec + ((long long)u * a.chunks + cb) * rec_bytes(true), n, kThreads);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == 17)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 template <int DK, int DV, int KIND>
-cudaError_t launch_as(const CUtensorMap* m, const GradArgs& a, int B, cudaStream_t stream) {
+cudaError_t launch_as(const CUtensorMap* m, const GradArgs& args, int B, cudaStream_t stream) {
+  GradArgs a = args;
+  set_waits(a.f, KIND == kSegState ? LTE_GDR_LAUNCH_BACK_SEGMENTS : LTE_GDR_LAUNCH_BACK);
   const int per = KIND == kSegState ? a.f.segs - 1 : a.f.segs * a.f.pieces;
   return launch_after(delta_back_tc_kernel<DK, DV, KIND>, (unsigned)(B * a.f.H * per), kThreads, kSmem, stream, m[0], m[1], m[2],
                       m[3], m[4], a);

@@ -71,12 +71,12 @@ delta_grad_kernel(const GradArgs ga, int items) {
     }
     return it;
   };
-  auto load_half = [&](int it, int r, int hv, int buf) {
+  auto load_half = [&](int it, int r, int hv, uint32_t n) {   // the CTA's n-th
     const int c = it % a.chunks, bh = it / a.chunks, b = bh / a.Hk, h = (bh % a.Hk) * rep + r;
     const long long img = ((long long)b * a.H + h) * a.chunks + c;
-    const uint32_t d = s0 + buf * SM::kStage;
+    const uint32_t buf = n & 1, d = s0 + buf * SM::kStage;
     load_rows<kHV, kGradThreads>(d + SM::kD, ga.dO + b * ga.dos.b + h * ga.dos.h + hv * kHV, ga.dos.t, c * L, len_of(it));
-    if (tid != 0) return;
+    if (tid != 0 || (int)n == a.withhold) return;
     const uint32_t bar = s0 + SM::kBar + 8 * buf;
     chaintc::mbar_expect_tx(bar, SM::kStage - SM::kU);
     const uint8_t* us = reinterpret_cast<const uint8_t*>(a.u) + img * (2 * DV * L * 2) + hv * (kHV * L * 2);
@@ -127,7 +127,7 @@ delta_grad_kernel(const GradArgs ga, int items) {
       for (int hv = 0; hv < NH; ++hv) {
         const int buf = halves & 1;
         cp_async_wait<0>();
-        ok = chaintc::mbar_wait(s0 + SM::kBar + 8 * buf, (halves >> 1) & 1, abort_flag, nullptr, 0);
+        ok = chaintc::mbar_wait(s0 + SM::kBar + 8 * buf, (halves >> 1) & 1, a.wait_ns, abort_flag);
         ++halves;
         // this half has landed; the one before has been read
         if (!(ok = __syncthreads_and(ok))) break;
@@ -141,9 +141,9 @@ delta_grad_kernel(const GradArgs ga, int items) {
           load_linear<(DV / 16) * 4, kGradThreads>(s0 + SM::kI, reinterpret_cast<const uint8_t*>(ga.inner) + img * ((DV / 16) * 4));
           if (NH == 1) cp_async_commit();
         }
-        if (hv + 1 < NH) load_half(it, r, hv + 1, buf ^ 1);
-        else if (r + 1 < rep) load_half(it, r + 1, 0, buf ^ 1);
-        else if (it1 < items) load_half(it1, 0, 0, buf ^ 1);
+        if (hv + 1 < NH) load_half(it, r, hv + 1, halves);
+        else if (r + 1 < rep) load_half(it, r + 1, 0, halves);
+        else if (it1 < items) load_half(it1, 0, 0, halves);
         cp_async_commit();
         const uint32_t d = s0 + buf * SM::kStage;
 #pragma unroll
@@ -343,18 +343,25 @@ delta_grad_kernel(const GradArgs ga, int items) {
     it = it1;
   }
   cp_async_wait<0>();
-  if (!ok && it < items) {                                 // a copy did not land: visible in the gates' gradients
-    if (tid == 0) {
-      const int b = it / a.chunks / a.Hk;
-      ga.dg[((long long)b * a.T + (it % a.chunks) * L) * a.H + (it / a.chunks % a.Hk) * rep] = __int_as_float(0x7fc00000);
-      chaintc::mbar_drain(s0 + SM::kBar + 8 * ((halves - 1) & 1), ((halves - 1) >> 1) & 1);
+  if (!ok) {                                               // a copy did not land: NaN in all that is not done
+    if (tid == 0 && (int)halves - 1 != a.withhold) chaintc::mbar_drain(s0 + SM::kBar + 8 * ((halves - 1) & 1), ((halves - 1) >> 1) & 1);
+    for (; it < items; it = next(it)) {
+      const int bh = it / a.chunks, b = bh / a.Hk, hk = bh % a.Hk, t0 = (it % a.chunks) * L, n = min(len_of(it) - t0, L);
+      const long long row = (long long)b * a.T + t0;
+      chaintc::nan_rows<DK>(ga.dq + (row * a.Hk + hk) * DK, (long long)a.Hk * DK, n, tid, kGradThreads);
+      chaintc::nan_rows<DK>(ga.dk + (row * a.Hk + hk) * DK, (long long)a.Hk * DK, n, tid, kGradThreads);
+      for (int i = tid; i < n * rep; i += kGradThreads)
+        ga.dg[(row + i / rep) * a.H + hk * rep + i % rep] = ga.db[(row + i / rep) * a.H + hk * rep + i % rep] =
+            __int_as_float(0x7fffffff);
     }
     __syncthreads();
   }
 }
 
 template <int DK, int DV, bool SHARED>
-cudaError_t grad_as(const GradArgs& a, int B, cudaStream_t stream) {
+cudaError_t grad_as(const GradArgs& args, int B, cudaStream_t stream) {
+  GradArgs a = args;
+  set_waits(a.f, LTE_GDR_LAUNCH_PASS);
   constexpr int smem = GradSmem<DK>::kTotal;
   const int items = B * a.f.Hk * a.f.chunks;
   const cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<DK, DV, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

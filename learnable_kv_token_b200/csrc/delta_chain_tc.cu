@@ -40,7 +40,9 @@
 //
 // Rows of the last chunk behind the sequence's length are set to zero in shared
 // memory before use, so what lies there (NaN, another sequence) does not enter.
-// Every mbarrier wait is bounded; a CTA that gives up writes NaN to its state.
+// Every wait is bounded; what a CTA that gives up has not finished is NaN: its state (or
+// n, X), its rows of o, or, for the gradients, its chunks' records, and with them all
+// that is made of those.
 #include <math.h>
 
 #include "delta_chain_tc.cuh"
@@ -81,6 +83,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBars + 8 * kBarCount);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBars + 8 * kBarCount + 8);
   volatile int* ticket = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* flight = ticket + 1;                         // chunks requested; MMAs issued
   auto bar = [&](int i) { return bars + 8 * i; };
   const bool a_lo = KIND == kImages || (KIND == kStateOnly && a.a_lo);      // the records hold A's lo
 
@@ -111,15 +114,16 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   const uint32_t tmem = *tmem_slot;
   // the unit's segment: for kStateOnly first n of segments 0 .. G - 2, then X of 1 .. G - 2;
   // or its piece, all first pieces before all second ones
-  auto unit_seg = [&](int& u, int& seg) {
+  auto unit_of = [&](int i, int& u, int& seg) {
     const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
-    const int units = PIECES ? gridDim.x / a.pieces : 1, i = PIECES ? *ticket : (int)blockIdx.x;
+    const int units = PIECES ? gridDim.x / a.pieces : 1;
     u = PIECES ? i % units : i / per;
     seg = PIECES ? i / units : i % per;
     const bool hom = KIND == kStateOnly && seg >= a.segs - 1;
     if (hom) seg -= a.segs - 2;
     return hom;
   };
+  auto unit_seg = [&](int& u, int& seg) { return unit_of(PIECES ? *ticket : (int)blockIdx.x, u, seg); };
   int u, seg;
   const bool hom = unit_seg(u, seg);
   const int b = u / a.H, h = u % a.H, hk = h / (a.H / a.Hk);
@@ -128,16 +132,16 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   const int len = max(seq_len(a.lens, b, a.T) - cb * L, 0);
   const int n_chunks = min((len + L - 1) / L, a.seg_chunks);
   bool ok = true;
-  int loaded = 0;                                            // chunks requested (producer)
-  bool issued = false;                                       // MMAs issued (MMA warp)
 
   if (warp >= 12) regs_dec<80>();
   if (warp == 12) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * rec_bytes(a_lo);
-    for (int c = 0; c < n_chunks; ++c) {
+    const int n_load = (unsigned)a.withhold < (unsigned)n_chunks ? a.withhold : n_chunks;
+    int loaded = 0;
+    for (int c = 0; c < n_load; ++c) {
       const int s = c & 1;
-      if (c >= 2 && !(ok = wwait(bar(bEmpty + s), ((c >> 1) - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (c >= 2 && !(ok = wwait(bar(bEmpty + s), ((c >> 1) - 1) & 1, a.wait_ns, abort_flag))) break;
       const uint32_t d = s0 + s * kStage;
       const bool tail = c * L + L > len;
       const uint32_t fb = tail ? bar(bTail) : bar(bFull + s);
@@ -158,7 +162,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       ++loaded;
       if (tail) {                                            // the last chunk: zeros behind the sequence
-        if (!(ok = wwait(fb, 0, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(fb, 0, a.wait_ns, abort_flag))) break;
         const int r0 = len - c * L;
         for (int j = 0; j < kHK; ++j) zero_rows(sm + s * kStage + kK + j * kHalf, r0, lane);
         for (int j = 0; j < kHV; ++j) zero_rows(sm + s * kStage + kV + j * kHalf, r0, lane);
@@ -167,18 +171,20 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (lane == 0) mbar_arrive(bar(bFull + s));
       }
     }
+    if (lane == 0) flight[kFlightLoads] = loaded;
   } else if (warp == 13) {
     // ================================================================= MMAs
     const uint32_t id_tok = idesc2(128, L, false, false);      // N = tokens, B [n][k]
     const uint32_t id_vt = idesc2(128, L, true, false);        // V^T from [token][channel]
     const uint32_t id_s = idesc2(128, 64, false, true);        // N = 64 key channels, B [k][n]
     const uint64_t ident = sdesc(s0 + kIdent, 16, 1024);
+    int issued = 0;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
       const uint32_t d = s0 + s * kStage;
-      if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, a.wait_ns, abort_flag))) break;
       tc_fence_after();
-      issued = true;
+      issued = 1;
       const uint64_t dk = sdesc(d + kK, 16, 1024), dq = sdesc(d + kQ, 16, 1024), dt = sdesc(d + kR, 16, 1024);
       if (elect_one()) {                                       // V^T
         const uint64_t dv = sdesc(d + kV, kHalf, 1024);
@@ -188,7 +194,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {                            // P^T = S K^T, by halves of S's columns
-        if (ok) ok = wwait(bar(bSr + p), ph, abort_flag, nullptr, 0);
+        if (ok) ok = wwait(bar(bSr + p), ph, a.wait_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -203,7 +209,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       if (!ok) break;
       if (OUT) {                                               // S Q^T
-        if (c > 0 && !(ok = wwait(bar(bOf), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+        if (c > 0 && !(ok = wwait(bar(bOf), (c - 1) & 1, a.wait_ns, abort_flag))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -215,7 +221,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mma_commit(bar(bQS));
         }
       }
-      if (!(ok = wwait(bar(bRr), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bRr), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // U^T = R^T T^T: columns t >= 16 ks
 #pragma unroll
@@ -227,7 +233,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                        p + ks > 0);
         mma_commit(bar(bU));
       }
-      if (!(ok = wwait(bar(bUr), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bUr), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {                                       // S += (U diag(e^{G_L - G}))^T K, by halves of its columns
         constexpr int kN = DK == 128 ? 2 : 1;
@@ -244,8 +250,8 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (kN == 1) mma_commit(bar(bS + 1));
       }
       if (OUT) {                                               // O^T += U^T A^T, columns t >= 16 ks
-        if (!(ok = wwait(bar(bUh), ph, abort_flag, nullptr, 0))) break;
-        if (!(ok = wwait(bar(bOs), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bUh), ph, a.wait_ns, abort_flag))) break;
+        if (!(ok = wwait(bar(bOs), ph, a.wait_ns, abort_flag))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -259,12 +265,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       if (c + 2 < n_chunks && elect_one()) mma_commit(bar(bEmpty + s));   // the stage is loaded once more
     }
-    if (!ok && issued) {                                       // MMAs in flight end before exit
-      __syncwarp();
-      if (elect_one()) mma_commit(bar(bDrain));
-      __syncwarp();
-      mbar_drain(bar(bDrain), 0);
-    }
+    if (lane == 0) flight[kFlightMma] = issued;
   } else if (warp < 8) {
     // ========================================================== chain warps
     regs_inc<144>();
@@ -275,7 +276,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     {                                                          // the state, while the first chunk loads
       const bool joined = KIND != kStateOnly && a.segs > 1;            // (s_out may be s_in: that was read by the join)
       const float* src = joined ? a.seg_s + seg * DV * DK : seg == 0 ? a.s_in : PIECES ? a.s_out : nullptr;
-      if (PIECES && seg > 0 && n_chunks > 0) ok = piece_ready(a.done + u, seg, abort_flag);
+      if (PIECES && seg > 0 && n_chunks > 0) ok = piece_ready(a.done + u, seg, a.wait_ns, abort_flag);
       if (src != nullptr) src += (long long)u * (joined ? a.segs : 1) * DV * DK + row * DK;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -304,15 +305,15 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     };
     for (int c = 0; ok && c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
-      if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bFull + s), (c >> 1) & 1, a.wait_ns, abort_flag))) break;
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       // ---- the state as bf16 hi and lo (columns QC (2 p + hc) .. + QC - 1)
-      if (KIND == kImages && c > 0 && !(ok = wwait(bar(bSread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+      if (KIND == kImages && c > 0 && !(ok = wwait(bar(bSread), (c - 1) & 1, a.wait_ns, abort_flag))) break;
       uint64_t S[2][QC / 2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int c0 = QC * (2 * p + hc);
-        if (c > 0 && ok) ok = wwait(bar(bS + p), (c - 1) & 1, abort_flag, nullptr, 0);
+        if (c > 0 && ok) ok = wwait(bar(bS + p), (c - 1) & 1, a.wait_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint32_t r[QC];
@@ -352,7 +353,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         gm[2 * e] = f2(-g.x, -g.y);
         gm[2 * e + 1] = f2(-g.z, -g.w);
       }
-      if (!(ok = wwait(bar(bP), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bP), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       uint64_t R[16];
       {
@@ -379,7 +380,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         gm[2 * e + 1] = f2(l.z, l.w);
       }
       if (lane == 0) mbar_arrive(bar(bEmpty + s));             // the scalars have been read
-      if (!(ok = wwait(bar(bU), ph, abort_flag, nullptr, 0))) break;
+      if (!(ok = wwait(bar(bU), ph, a.wait_ns, abort_flag))) break;
       tc_fence_after();
       {
         uint32_t x[32], hi[16], lo[16];
@@ -397,14 +398,14 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         arrive(bUr);
         if (KIND == kStateOnly) continue;
         split_pairs(R, hi, lo);
-        if (KIND == kImages && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, abort_flag, nullptr, 0))) break;
+        if (KIND == kImages && c > 0 && !(ok = wwait(bar(bUread), (c - 1) & 1, a.wait_ns, abort_flag))) break;
         tmem_st16(la + kColUH + 16 * hc, hi);
         tmem_st16(la + kColUL + 16 * hc, lo);
         arrive(bUh);
       }
     }
     if (ok && n_chunks > 0) {
-      ok = wwait(bar(bS), (n_chunks - 1) & 1, abort_flag, nullptr, 0) && wwait(bar(bS + 1), (n_chunks - 1) & 1, abort_flag, nullptr, 0);
+      ok = wwait(bar(bS), (n_chunks - 1) & 1, a.wait_ns, abort_flag) && wwait(bar(bS + 1), (n_chunks - 1) & 1, a.wait_ns, abort_flag);
       tc_fence_after();
     }
     int ul, segl;
@@ -438,23 +439,26 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
         }
       }
-      if (PIECES) piece_done(a.done + ul, segl, 2, 256);
+      if (PIECES && !piece_done(a.done + ul, segl, ok, 2, 256) && row < rows)
+        for (int i = 0; i < DK / 8; ++i)
+          *reinterpret_cast<float4*>(dst + QC * 2 * hc + 4 * i) = make_float4(NAN, NAN, NAN, NAN);
     }
   } else if (warp < 12) {
     // ==================================================== O, or the images
     regs_inc<144>();
     const int quad = warp - 8, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
-    for (int c = 0; c < n_chunks; ++c) {
+    int c = 0;
+    for (; c < n_chunks; ++c) {
       const int s = c & 1, ph = c & 1;
-      ok = wwait(bar(bFull + s), (c >> 1) & 1, abort_flag, nullptr, 0);
+      ok = wwait(bar(bFull + s), (c >> 1) & 1, a.wait_ns, abort_flag);
       if (!OUT && !ok) break;                                  // (O: the warps meet at the vote below)
       const float* scal = reinterpret_cast<const float*>(sm + s * kStage + kScalOff);
       const long long img = KIND == kImages ? (long long)u * a.chunks + cb + c : 0;
       if (KIND == kStateOnly) {
         if (lane == 0) mbar_arrive(bar(bEmpty + s));
       } else if (OUT) {
-        ok = ok && wwait(bar(bQS), ph, abort_flag, nullptr, 0);
+        ok = ok && wwait(bar(bQS), ph, a.wait_ns, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -478,7 +482,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mbar_arrive(bar(bEmpty + s));
           mbar_arrive(bar(bOs));
         }
-        ok = ok && wwait(bar(bO), ph, abort_flag, nullptr, 0);
+        ok = ok && wwait(bar(bO), ph, a.wait_ns, abort_flag);
         tc_fence_after();
         uint32_t r[2][32];
         tmem_ld32(la + kColO, r[0]);
@@ -524,7 +528,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
       } else {
         if (lane == 0) mbar_arrive(bar(bEmpty + s));
-        if (!(ok = wwait(bar(bSr), ph, abort_flag, nullptr, 0) && wwait(bar(bSr + 1), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bSr), ph, a.wait_ns, abort_flag) && wwait(bar(bSr + 1), ph, a.wait_ns, abort_flag))) break;
         tc_fence_after();
         // images in 8 x 8 blocks: a row's 16 bytes of each column block
         const int rb = row >> 3, r7 = row & 7;
@@ -546,7 +550,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bSread));
-        if (!(ok = wwait(bar(bUh), ph, abort_flag, nullptr, 0))) break;
+        if (!(ok = wwait(bar(bUh), ph, a.wait_ns, abort_flag))) break;
         tc_fence_after();
         uint32_t r[2][32];
         tmem_ld32(la + kColUH, r[0]);
@@ -566,16 +570,37 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
       }
     }
+    if (OUT && !ok) {                                          // the rows from this chunk on
+      int u, seg;
+      unit_seg(u, seg);
+      const int first = (seg * a.seg_chunks + c) * L, rows = min((seg + 1) * a.seg_chunks * L, seq_len(a.lens, u / a.H, a.T)) - first;
+      nan_rows<DV>(a.o + (u / a.H) * a.os.b + (u % a.H) * a.os.h + (long long)first * a.os.t, a.os.t, rows, tid - 256, 128);
+    }
   }
   if (OUT && tid == 256) bulk_wait_read();                     // output stores have left shared memory
-  // copies in flight land before exit (only after a wait gave up)
-  if (warp == 12 && *abort_flag) {
-    for (int i = loaded - 2 > 0 ? loaded - 2 : 0; i < loaded; ++i)
-      if (i * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
-      else mbar_drain(bar(bTail), 0);
-  }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {                                           // a wait gave up (every warp is past its last one)
+    int u, seg;
+    unit_of(PIECES ? *ticket : block_again(), u, seg);
+    const int cb = seg * a.seg_chunks, len = max(seq_len(a.lens, u / a.H, a.T) - cb * L, 0);
+    const int n_chunks = min((len + L - 1) / L, a.seg_chunks);
+    // MMAs and copies in flight end before the memory that they use goes
+    if (warp == 13 && flight[kFlightMma]) {
+      if (elect_one()) mma_commit(bar(bDrain));
+      __syncwarp();
+      mbar_drain(bar(bDrain), 0);
+    }
+    if (warp == 12)
+      for (int n = flight[kFlightLoads], i = max(n - 2, 0); i < n; ++i)
+        if (i * L + L <= len) mbar_drain(bar(bFull + (i & 1)), (i >> 1) & 1);
+        else mbar_drain(bar(bTail), 0);
+    __syncthreads();
+    // (the maps' n and X, every state and the rows of o are NaN by the warps that did not finish them)
+    if (KIND == kImages) nan_records(a.rec + ((long long)u * a.chunks + cb) * rec_bytes(true), n_chunks, kThreads);
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == 13)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
@@ -675,7 +700,9 @@ cudaError_t join_as(const ChunkArgs& a, const float* given, bool reverse, int B,
 }
 
 template <int DK, int DV, int KIND, bool PIECES = false>
-cudaError_t launch(const CUtensorMap* m, const ChunkArgs& a, int B, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap* m, const ChunkArgs& args, int B, cudaStream_t stream) {
+  ChunkArgs a = args;
+  set_waits(a, KIND == kStateOnly ? LTE_GDR_LAUNCH_SEGMENTS : LTE_GDR_LAUNCH_CHAIN);
   const int per = KIND == kStateOnly ? 2 * a.segs - 3 : a.segs;
   return launch_after(delta_chain_tc_kernel<DK, DV, KIND, PIECES>, (unsigned)(B * a.H * per * a.pieces), kThreads, kSmem, stream,
                       m[0], m[1], m[2], m[3], a);

@@ -120,23 +120,65 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, int s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Pieces of a sequence (chain_pieces): the number of a unit's pieces that are done.
+// The delta rule's waits: for at most `limit` ns, then the CTA gives up (*abort_flag)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned limit, volatile int* abort_flag) {
+  return mbar_wait_bounded(bar, parity, limit, abort_flag, nullptr, 0);
+}
+__device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, unsigned limit, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort_flag));
+}
+// What a CTA that gave up marks, so that nothing it left as it was is taken for a result:
+// NaN in `rows` token rows, and in the scalars of `chunks` records, which turns all that
+// the later launches make of those chunks into NaN.
+// (The block's number is read anew there, and what is in flight is counted in shared
+// memory: nothing for this end is kept in registers over the chunks.)
+__device__ __forceinline__ int block_again() {
+  int i;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(i));
+  return i;
+}
+enum : int { kFlightLoads = 0, kFlightStates = 1, kFlightMma = 2 };
+template <int COLS>
+__device__ __forceinline__ void nan_rows(__nv_bfloat16* p, long long stride, int rows, int thread, int threads) {
+  for (int i = thread; i < rows * (COLS / 8); i += threads)
+    *reinterpret_cast<uint4*>(p + (i / (COLS / 8)) * stride + i % (COLS / 8) * 8) =
+        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+}
+__device__ __forceinline__ void nan_records(uint8_t* rec, int chunks, int threads) {
+  for (int c = 0; c < chunks; ++c)
+    for (int i = threadIdx.x; i < kGradScal / 4; i += threads)
+      reinterpret_cast<uint32_t*>(rec + (long long)c * rec_bytes(true) + 4 * kImg)[i] = 0x7fffffffu;
+}
+
+// Pieces of a sequence (chain_pieces): the number of a unit's pieces that are done, or
+// kPieceFailed once one of them has given up: those behind it give up too, and a piece
+// before it that was only slow must not leave its state where NaN belongs.
+constexpr int kPieceFailed = 1 << 30;
 // Every lane of a warp waits (half as long as the waits behind this one may take),
 // so each has acquired what was written before the number.
-__device__ __forceinline__ bool piece_ready(const int* done, int want, volatile int* abort_flag) {
+__device__ __forceinline__ bool piece_ready(const int* done, int want, unsigned limit, volatile int* abort_flag) {
   const unsigned long long t0 = gtime();
   int v;
   do {
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
-  } while (v < want && *abort_flag == 0 && gtime() - t0 < kWaitNs / 2);
-  if (v < want) *abort_flag = 1;
-  return __all_sync(0xffffffffu, v >= want);
+  } while (v < want && *abort_flag == 0 && gtime() - t0 < limit / 2);
+  const bool ok = v >= want && v < kPieceFailed;
+  if (!ok) *abort_flag = 1;
+  return __all_sync(0xffffffffu, ok);
 }
-// by the warps that wrote the state (`threads` threads, all of which get here)
-__device__ __forceinline__ void piece_done(int* done, int seg, int id, int threads) {
+// By the warps that wrote the state (`threads` threads, all of which get here), `ok` where
+// it is as it should be.  False: the unit's state has to become NaN.  (Whoever comes
+// second to the counter sees the other, and writes after it: a piece that fails sets the
+// counter before its NaN, one that is done has written its state before it looks.)
+__device__ __forceinline__ bool piece_done(int* done, int seg, bool ok, int id, int threads) {
   __threadfence();
-  bar_sync(id, threads);
-  if (threadIdx.x == 0) asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(done), "r"(seg + 1) : "memory");
+  ok = bar_and(id, threads, ok);
+  bool stands = true;
+  if (threadIdx.x == 0) {
+    stands = atomicMax(done, ok ? seg + 1 : kPieceFailed) < kPieceFailed && ok;
+    __threadfence();
+  }
+  return bar_and(id, threads, stands);
 }
 
 // [channels, heads, T, B] with the tensor's strides; boxes of 64 tokens x 64 channels

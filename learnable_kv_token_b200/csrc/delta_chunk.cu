@@ -2,7 +2,10 @@
 // (formulas and precision: delta_chunk.cuh): which form a call takes, its
 // workspace and its launches.  Everything that depends on no state, for all
 // chunks at once (delta_prepare.cu), then the chain of states (delta_chain_tc.cu).
+#include <atomic>
+
 #include "delta_chunk.cuh"
+#include "tc_ptx.cuh"
 
 namespace lte {
 
@@ -13,6 +16,21 @@ namespace lte {
 bool delta_chunked(const lte_gdr_dims* d) {
   const long long strips = (long long)d->B * d->H * (d->dv / 16);
   return d->dtype == LTE_BF16 && d->T > (strips <= 148 ? 40 : strips <= 512 ? 28 : 15);
+}
+
+namespace {
+std::atomic<int> g_withheld{0}, g_chunk{0};
+std::atomic<unsigned> g_limit_ns{0};
+}  // namespace
+void delta_withhold(int launches, int chunk, unsigned limit_ns) {
+  g_chunk = chunk;
+  g_limit_ns = limit_ns;
+  g_withheld = launches;
+}
+void delta::set_waits(ChunkArgs& a, int launch) {
+  const bool on = g_withheld & launch;
+  a.wait_ns = on ? g_limit_ns.load() : (unsigned)tc::kWaitNs;
+  a.withhold = on ? g_chunk.load() : -1;
 }
 
 namespace {

@@ -114,6 +114,8 @@ struct ChunkArgs {
   // the backward chain (prepare sets all to zero)
   int pieces, *turn, *done;
   float *seg_n, *seg_x, *seg_xt, *seg_s;
+  unsigned wait_ns;      // the launch's waits give up after this
+  int withhold;          // the chunk, in the order in which a CTA takes them, whose loads are left out; -1
 };
 
 struct GradArgs {
@@ -128,6 +130,9 @@ struct GradArgs {
   float* hand;               // [units][dv][dk]: dS between pieces (forward: S, as s_out)
   float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
 };
+
+// Sets wait_ns and withhold of a launch (LTE_GDR_LAUNCH_*): one second and none, but for lte_gdr_withhold
+void set_waits(ChunkArgs& a, int launch);
 
 // Each returns cudaErrorNotSupported, without a launch, for tensors whose strides
 // TMA does not take.

@@ -100,8 +100,8 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(bar_mma, 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    mbar_expect_tx(bar_in, 2 * kHK * kHalf);
-    for (int i = 0; i < kHK; ++i) {                       // half i: 64 rows of K, then 64 of Q
+    if (c != a.withhold) mbar_expect_tx(bar_in, 2 * kHK * kHalf);
+    for (int i = 0; i < (c != a.withhold ? kHK : 0); ++i) {                       // half i: 64 rows of K, then 64 of Q
       tma_load_4d(s0 + 2 * i * kHalf, &tm_k, bar_in, 64 * i, hk, t0, b);
       tma_load_4d(s0 + (2 * i + 1) * kHalf, &tm_q, bar_in, 64 * i, hk, t0, b);
     }
@@ -153,17 +153,18 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  bool ok = true;
+  bool ok = true, issued = false;
   if (t0 + L > len) {                                     // rows behind the sequence are not data
-    ok = mbar_wait(bar_in, 0, &abort_flag, nullptr, 0);
+    ok = mbar_wait(bar_in, 0, a.wait_ns, &abort_flag);
     const int r0 = len - t0;
     for (int i = warp; i < 2 * kHK; i += 4) zero_rows(sm + i * kHalf, r0, lane);
     fence_proxy_async();
     ok = __syncthreads_and(ok);
   }
   if (warp == 0) {                                        // [K; Q] K^T
-    ok = ok && wwait(bar_in, 0, &abort_flag, nullptr, 0);
+    ok = ok && wwait(bar_in, 0, a.wait_ns, &abort_flag);
     tc_fence_after();
+    issued = ok;
     if (ok && elect_one()) {
       const uint64_t d = sdesc(s0, 16, 1024);
 #pragma unroll
@@ -174,7 +175,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mma_commit(bar_mma);
     }
   }
-  ok = ok && mbar_wait(bar_mma, 0, &abort_flag, nullptr, 0);
+  ok = ok && mbar_wait(bar_mma, 0, a.wait_ns, &abort_flag);
   // all or none: also, every thread is past the product before its operands are overwritten
   ok = __syncthreads_and(ok);
   if (ok) {
@@ -318,10 +319,11 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       bulk_wait_all();
     }
   } else {
-    // a wait gave up: the chunk's scalars turn everything behind them into NaN;
-    // the copies in flight land before exit
+    // a wait gave up: the chunk's scalars turn everything behind them into NaN; the
+    // product and the copies in flight end before the memory that they use goes
     for (int i = tid; i < (A_LO ? kGradScal : kScal) / 4; i += kPrepThreads) scal[i] = NAN;
-    if (tid == 0) mbar_drain(bar_in, 0);
+    if (tid == 0 && c != a.withhold) mbar_drain(bar_in, 0);
+    if (issued) mbar_drain(bar_mma, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -339,7 +341,9 @@ cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const ChunkArgs
 
 }  // namespace prep
 
-cudaError_t prepare(const ChunkArgs& a, int B, int dk, bool a_lo, cudaStream_t stream) {
+cudaError_t prepare(const ChunkArgs& args, int B, int dk, bool a_lo, cudaStream_t stream) {
+  ChunkArgs a = args;
+  set_waits(a, LTE_GDR_LAUNCH_PREPARE);
   CUtensorMap q, k;
   if (!chaintc::map_of(&q, a.q, dk, a.Hk, a.T, B, a.qs) || !chaintc::map_of(&k, a.k, dk, a.Hk, a.T, B, a.ks))
     return cudaErrorNotSupported;

@@ -626,6 +626,13 @@ lte_status lte_gdr_zero_padding(int32_t B, int32_t T, const int32_t* lens, int32
   return from_cuda(lte::delta_zero_padding(B, T, lens, n, tensors, row_bytes, as_stream(stream)));
 }
 
+lte_status lte_gdr_withhold(int32_t launches, int32_t chunk, int64_t limit_ns) {
+  if (launches < 0 || launches > LTE_GDR_LAUNCH_ALL || chunk < 0 || limit_ns < 1000 || limit_ns > 1000000000)
+    return LTE_ERR_INVALID_ARG;
+  lte::delta_withhold(launches, chunk, (unsigned)limit_ns);
+  return LTE_OK;
+}
+
 lte_status lte_gdr_decode_step(const lte_gdr_dims* d, const void* q_t, const void* k_t,
                                const void* v_t, const float* g_t, const float* beta_t, void* o_t,
                                float* state, void* stream) {

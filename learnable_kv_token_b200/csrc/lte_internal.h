@@ -152,6 +152,7 @@ struct DeltaArgs {
   void* scratch;              // workspace
 };
 cudaError_t delta_recurrent(const DeltaArgs& a, cudaStream_t stream);
+void delta_withhold(int launches, int chunk, unsigned limit_ns);
 size_t delta_prefill_bytes(const lte_gdr_dims* d);
 cudaError_t delta_prefill(const DeltaArgs& a, cudaStream_t stream);
 // delta_backward.cu

@@ -24,6 +24,9 @@ LTE_F32, LTE_BF16 = 0, 1
 LTE_CAP_RECENT, LTE_CAP_FIRST, LTE_CAP_LOWEST = 0, 1, 2
 LTE_WS_PREFILL, LTE_WS_DECODE, LTE_WS_BACKWARD, LTE_WS_RELAXED = 0, 1, 2, 3
 LTE_GDR_WS_PREFILL, LTE_GDR_WS_BACKWARD = 0, 1
+(LTE_GDR_LAUNCH_PREPARE, LTE_GDR_LAUNCH_SEGMENTS, LTE_GDR_LAUNCH_CHAIN, LTE_GDR_LAUNCH_BACK_SEGMENTS,
+ LTE_GDR_LAUNCH_BACK, LTE_GDR_LAUNCH_PASS) = (1 << i for i in range(6))
+LTE_GDR_LAUNCH_ALL = 63
 LTE_NORM_NONE, LTE_NORM_RMS, LTE_NORM_L2 = 0, 1, 2
 LTE_KERNEL_TCGEN05, LTE_KERNEL_MMA_SYNC, LTE_KERNEL_SIMT = 1, 2, 3
 STATUS = {0: "LTE_OK", 1: "LTE_ERR_INVALID_ARG", 2: "LTE_ERR_UNSUPPORTED", 3: "LTE_ERR_CUDA",
@@ -107,6 +110,7 @@ _SIG = {
     "lte_gdr_backward": [C.POINTER(lte_gdr_dims), _P, _P, _P] + [C.POINTER(lte_strides)] * 3
                         + [_P] * 5 + [C.POINTER(lte_strides)] + [_P] * 8 + [C.c_size_t, _P],
     "lte_gdr_zero_padding": [_I, _I, _P, _I, C.POINTER(_P), C.POINTER(C.c_int64), _P],
+    "lte_gdr_withhold": [_I, _I, C.c_int64],
     "lte_gdr_decode_step": [C.POINTER(lte_gdr_dims)] + [_P] * 8,
     "lte_qk_norm_rope": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2 + [_P] * 4,
     "lte_qk_norm_rope_backward": [C.POINTER(lte_qk_norm), _P, _P] + [C.POINTER(lte_strides)] * 2
@@ -392,6 +396,12 @@ def lte_gdr_zero_padding(lens, tensors, stream=None):
     _check_status("lte_gdr_zero_padding", _lib.lte_gdr_zero_padding(
         B, T, _addr(lens), n, (_P * n)(*(t.data_ptr() for t in tensors)),
         (C.c_int64 * n)(*(t.stride(1) * t.element_size() for t in tensors)), _raw(stream)))
+
+
+def lte_gdr_withhold(launches: int, chunk: int = 0, limit_ns: int = 1_000_000_000):
+    """Diagnostic: in later calls' `launches` (LTE_GDR_LAUNCH_* or'd; 0 = none) the loads of each CTA's
+    chunk number `chunk` are left out, and waits give up after limit_ns."""
+    _check_status("lte_gdr_withhold", _lib.lte_gdr_withhold(launches, chunk, limit_ns))
 
 
 def lte_gdr_decode_step(dims, q_t, k_t, v_t, g_t, beta_t, o_t, state, stream=None):

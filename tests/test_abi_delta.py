@@ -144,3 +144,9 @@ def test_zero_padding(L):
     for bad in (dict(B=0), dict(T=0), dict(lens=None), dict(n=0), dict(n=9), dict(x=None), dict(r=None), dict(x=odd),
                 dict(x=(C.c_void_p * 2)(1 << 20, None)), dict(r=(C.c_int64 * 2)(64, 6)), dict(r=(C.c_int64 * 2)(0, 64))):
         assert call(**bad) == INVALID
+
+
+def test_withhold(L):
+    for bad in ((-1, 0, 10000), (64, 0, 10000), (1, -1, 10000), (1, 0, 999), (1, 0, 1_000_000_001)):
+        assert L._lib.lte_gdr_withhold(*bad) == INVALID
+    assert L._lib.lte_gdr_withhold(0, 0, 1_000_000_000) == 0
