@@ -4,8 +4,8 @@
 // Row x of D channels (one token, one head), weight w, c = 1/D (RMS) or 1 (L2):
 //   r = (c sum x^2 + eps)^(-1/2),  n = x r w,  y = rotation of n by the row's
 //   position (channel pairs (i, i + R/2) or (2i, 2i + 1), i < R/2).
-// Gradient, with dn the rotation back of dy (the rotation is orthogonal):
-//   dx = r w dn - x c r^3 <w dn, x>,   dw = sum over rows of dn x r.
+// Gradient, with dn the rotation back of dy (the rotation is orthogonal) and z = x r:
+//   dx = r (w dn - z c r <w dn, x>),   dw = sum over rows of dn z.
 //
 // Both are bound by memory: every row is read once and written once.  D / 8
 // lanes hold a row, two groups of 4 channels each, chosen so that both members
@@ -255,11 +255,13 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_backward_kernel(const Arg
           in = fmaf(dn[e] * w[e], v[e], in);
         }
         const float r = rsqrtf(fmaf(a.c, row_sum<LPR>(ss), a.eps));
-        const float m = a.c * r * r * r * row_sum<LPR>(in);
+        // x r is bounded; r^3 is not (eps below 1e-25, rows of zeros): the sum takes one r, x another
+        const float m = a.c * (r * row_sum<LPR>(in));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dw[e] += on ? dn[e] * (v[e] * r) : 0.f;
-          dn[e] = fmaf(r * w[e], dn[e], -m * v[e]);
+          const float z = v[e] * r;
+          dw[e] += on ? dn[e] * z : 0.f;
+          dn[e] = r * fmaf(w[e], dn[e], -m * z);
         }
       }
       if (on) store8((T*)a.y[which] + at + i * D, cols, dn);

@@ -113,6 +113,27 @@ def test_zero_rows_and_large_values(layer):
     close(ok, DO.qk_norm(f64(k), f64(p.wk), "rms", EPS, ang, 64, False), 64, torch.float32, "large")
 
 
+@pytest.mark.parametrize("kind", ["rms", "l2"])
+@pytest.mark.parametrize("eps", [1e-6, 1e-24, 1e-30, 1e-36])
+def test_gradients_of_zero_and_tiny_rows(layer, kind, eps):
+    """1 / sqrt(eps) to the third power leaves fp32 for eps below 2e-26; the gradient of a row of zeros is
+    w dy / sqrt(eps) all the same.  Bounds as in test_forward_and_gradient."""
+    q, k, p, pos, ang = setup(layer, 12, 1, 6, 2, 2, 64, torch.float32, kind, 0, False, 0, False)
+    p.eps = eps
+    q[0, 2] = 0
+    k[0, 3] *= 1e-14
+    dy = [torch.randn(x.shape, generator=torch.Generator().manual_seed(3)).cuda() for x in (q, k)]
+    dq, dk, dwq, dwk = layer.qk_norm_rope_backward(q, k, *dy, p)
+    m = 1 / 64 if kind == "rms" else 1.0
+    for x, w, d, dx, dw in ((q, p.wq, dy[0], dq, dwq), (k, p.wk, dy[1], dk, dwk)):
+        rx, rw = DO.qk_norm_backward(f64(x), f64(w), f64(d), kind, eps)
+        r = 1 / np.sqrt(m * (f64(x) ** 2).sum(-1, keepdims=True) + eps)
+        size = np.abs(r * f64(w) * f64(d)).max(-1, keepdims=True)
+        assert (np.abs(f64(dx) - rx) <= 2.0 ** -24 * 2 * (64 + 16) * size).all()
+        terms = np.sqrt(((f64(d) * f64(x) * r) ** 2).sum((0, 1, 2)))
+        assert (np.abs(f64(dw) - rw) <= 2.0 ** -24 * (12 ** 0.5 + 64 + 16) * terms).all()
+
+
 def test_position_outside_the_table(layer):
     """Those rows come out as NaN on the rotated channels, the others as ever; nothing is read out of
     the table."""
