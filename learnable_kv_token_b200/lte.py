@@ -393,9 +393,12 @@ def lte_gdr_zero_padding(lens, tensors, stream=None):
     """tensors: contiguous [B,T,...]."""
     B, T = tensors[0].shape[:2]
     n = len(tensors)
+    # (a row's bytes from the shape: the stride of an extent of 1 may be anything)
+    if any(t.shape[:2] != (B, T) or not t.is_contiguous() for t in tensors) or lens.shape != (B,) or lens.dtype is not torch.int32:
+        raise ValueError("contiguous tensors [B,T,...] and lens int32 [B]")
     _check_status("lte_gdr_zero_padding", _lib.lte_gdr_zero_padding(
         B, T, _addr(lens), n, (_P * n)(*(t.data_ptr() for t in tensors)),
-        (C.c_int64 * n)(*(t.stride(1) * t.element_size() for t in tensors)), _raw(stream)))
+        (C.c_int64 * n)(*(t.numel() // max(B * T, 1) * t.element_size() for t in tensors)), _raw(stream)))
 
 
 def lte_gdr_withhold(launches: int, chunk: int = 0, limit_ns: int = 1_000_000_000):

@@ -150,3 +150,26 @@ def test_withhold(L):
     for bad in ((-1, 0, 10000), (64, 0, 10000), (1, -1, 10000), (1, 0, 999), (1, 0, 1_000_000_001)):
         assert L._lib.lte_gdr_withhold(*bad) == INVALID
     assert L._lib.lte_gdr_withhold(0, 0, 1_000_000_000) == 0
+
+
+def test_zero_padding_takes_rows_from_the_shape(L, monkeypatch):
+    """A tensor of one token per sequence counts as contiguous whatever its token stride, which must not
+    become the length of the rows that are set to zero.  (The entry itself is replaced: no device.)"""
+    import types
+
+    import torch
+    seen = []
+    monkeypatch.setattr(L, "_lib", types.SimpleNamespace(
+        lte_gdr_zero_padding=lambda B, T, lens, n, x, r, s: seen.append((B, T, n, list(r[:n]))) or 0))
+    stream, lens = types.SimpleNamespace(cuda_stream=0), torch.zeros(2, dtype=torch.int32)
+    one = torch.zeros(100).as_strided((2, 1, 3, 4), (12, 1000, 4, 1))
+    assert one.is_contiguous() and one.stride(1) == 1000
+    L.lte_gdr_zero_padding(lens, [one, torch.zeros(2, 1, 5)], stream)
+    L.lte_gdr_zero_padding(lens, [torch.zeros(2, 7, 3, dtype=torch.bfloat16), torch.zeros(2, 7)], stream)
+    assert seen == [(2, 1, 2, [48, 20]), (2, 7, 2, [6, 4])]
+    for bad in ([torch.zeros(2, 7, 3).transpose(0, 1).contiguous().transpose(0, 1)], [torch.zeros(2, 7), torch.zeros(2, 8)]):
+        with pytest.raises(ValueError):
+            L.lte_gdr_zero_padding(lens, bad, stream)
+    for bad in (lens.long(), lens[:1]):
+        with pytest.raises(ValueError):
+            L.lte_gdr_zero_padding(bad, [torch.zeros(2, 7)], stream)
