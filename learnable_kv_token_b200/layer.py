@@ -357,11 +357,9 @@ def _norm_struct(q, k, p, positions):
 def qk_norm_rope(q, k, p: QKNorm, positions=None, q_out=None, k_out=None):
     """Normed and rotated q [B,T,Hq,D] and k [B,T,Hkv,D] (bf16 or fp32; strided views with
     contiguous channels are fine).  positions: int32 [B,T], default 0 .. T-1.  q_out and k_out may
-    be q and k if those are contiguous.  Where there is nothing to do (kind "none", no rotation), the
-    result is q and k, copied only if they are not contiguous.  Also takes `stream`."""
+    be q and k if those are contiguous; otherwise the result shares no memory with them, also where
+    there is nothing to do (kind "none", no rotation).  Also takes `stream`."""
     c = _norm_struct(q, k, p, positions)
-    if p.kind == "none" and not p.rot_dim and q_out is None and k_out is None:
-        return q.contiguous(), k.contiguous()
     if q_out is None:
         q_out = _new(q)
     else:

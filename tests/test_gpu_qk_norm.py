@@ -104,6 +104,20 @@ def test_no_weights_and_in_place(layer):
         close(x, r, 128, torch.bfloat16, "in place")
 
 
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("kind,rot", [("none", 0), ("none", 32), ("l2", 0)])
+def test_the_result_is_the_callers_own(layer, kind, rot, fused):
+    """Writing into the result changes neither q nor k, whatever the norm does and however they lie."""
+    q, k, p, pos, ang = setup(layer, 13, 2, 9, 2, 1, 64, torch.bfloat16, kind, rot, False, 0, fused)
+    before = q.clone(), k.clone()
+    out = layer.qk_norm_rope(q, k, p)
+    for x, y, b in zip((q, k), out, before):
+        if kind == "none" and not rot:
+            assert torch.equal(x, y)
+        y.fill_(3.0)
+        assert torch.equal(x, b)
+
+
 def test_zero_rows_and_large_values(layer):
     q, k, p, pos, ang = setup(layer, 9, 1, 6, 2, 2, 64, torch.float32, "rms", 64, False, 0, False)
     q[0, 2] = 0
