@@ -251,6 +251,8 @@ class Decoder:
         dt = torch.bfloat16 if dims.dtype == L.LTE_BF16 else torch.float32
         self.o = torch.empty(B, Hq, D, dtype=dt, device=device)
         self.lse = torch.empty(B, Hq, dtype=torch.float32, device=device)
+        if norm is not None:
+            self.q_n, self.k_n = (torch.empty(B, 1, h, D, dtype=dt, device=device) for h in (Hq, dims.Hkv))
         ws = L.lte_workspace_bytes(dims, L.LTE_WS_DECODE)
         self.ws = torch.zeros((ws + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
@@ -260,8 +262,8 @@ class Decoder:
             if self.norm.rot_dim and positions is None:
                 raise ValueError("a rotation needs the tokens' positions")
             pos = None if positions is None else positions[:, None]
-            q_t, k_t = (x[:, 0] for x in qk_norm_rope(q_t[:, None], k_t[:, None], self.norm,
-                                                      positions=pos, stream=stream))
+            q_t, k_t = (x[:, 0] for x in qk_norm_rope(q_t[:, None], k_t[:, None], self.norm, positions=pos,
+                                                      q_out=self.q_n, k_out=self.k_n, stream=stream))
         L.lte_decode_step(self.dims, self.cnn, self.cache.struct, q_t, k_t, v_t, self.o, self.lse,
                           self.score_batch, self.ws, stream)
         return self.o, self.lse

@@ -248,3 +248,26 @@ def test_lte_layer_behind_the_norm(layer):
         # the attention gradient's own gate (1e-2 of the 2-norm) and one rounding
         assert np.linalg.norm(f64(dx) - ex) <= (1e-2 + 2.0 ** -8) * np.linalg.norm(ex)
         assert np.linalg.norm(f64(dw) - ew) <= 1e-2 * np.linalg.norm(ew) * 3
+
+
+def test_decoder_with_a_norm_allocates_nothing(layer):
+    """A step runs over the decoder's own buffers, with a norm as without."""
+    B, T, Hq, Hkv, D = 2, 40, 8, 2, 128
+    g = LI.generator(61)
+    q, k, v = (x.cuda() for x in LI.qkv(B, T + 3, Hq, Hkv, D, torch.bfloat16, g, std=1.0))
+    cnn = tuple(x.cuda() for x in LI.cnn_weights(Hkv, D, 32, 5, 3, g, 0.1))
+    norm = layer.QKNorm("rms", EPS, rot_dim=D, table=layer.rope_table(T + 3, D))
+    lp = layer.LayerParams(sink=4, window=32, cap=8, tau=0.5)
+    cut = lambda x: x[:, :T].contiguous()  # noqa: E731
+    out = layer.prefill(cut(q), cut(k), cut(v), lp, cnn=cnn, norm=norm)
+    dims = lp.dims(B, T, Hq, Hkv, D, torch.bfloat16)
+    cache = layer.DecodeCache(B, Hkv, D, torch.bfloat16, lp.sink, lp.window, lp.cap)
+    cache.init_from_prefill(dims, out.k, cut(v), out, T)
+    dec = layer.Decoder(dims, cnn, 2, 1, cache, 4, norm=norm)
+    args = [[x[:, t].contiguous() for x in (q, k, v)] + [torch.full((B,), t, dtype=torch.int32, device="cuda")]
+            for t in range(T, T + 3)]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    for qt, kt, vt, pos in args:
+        dec.step(qt, kt, vt, positions=pos)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
