@@ -173,3 +173,10 @@ def test_zero_padding_takes_rows_from_the_shape(L, monkeypatch):
     for bad in (lens.long(), lens[:1]):
         with pytest.raises(ValueError):
             L.lte_gdr_zero_padding(bad, [torch.zeros(2, 7)], stream)
+
+
+def test_the_package_names_every_entry(L):
+    import learnable_kv_token_b200 as package
+    for n in L.EXPORTED:
+        if n.startswith(("lte_gdr_", "lte_qk_")):
+            assert getattr(package, n) is getattr(L, n), n
