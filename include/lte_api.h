@@ -529,8 +529,10 @@ size_t lte_gdr_workspace_bytes(const lte_gdr_dims* d, int32_t which);
  * state take fp32 operands as bf16 hi + lo pairs (relative error about 2^-17),
  * so the fp32 state keeps about 1e-5; o is rounded once to bf16.  fp32, bf16
  * with few tokens, and bf16 with strides that a tensor map cannot hold (2^40
- * bytes): token by token in fp32.  No atomics: results repeat
- * bit by bit.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+ * bytes): token by token in fp32.  No sum depends on an order
+ * that may change, so results repeat bit by bit.  (With more than 148 states
+ * sequences are cut into pieces that CTAs draw from a counter, and a CTA may wait,
+ * for half a second at most, for the piece before its own.)  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, const void* v,
                            const lte_strides* q_strides, const lte_strides* k_strides,
                            const lte_strides* v_strides, const float* g, const float* beta,
@@ -545,7 +547,7 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
  * dtype, contiguous; dg, dbeta fp32 [B,T,H]; dstate_in (nullable) fp32
  * [B,H,dv,dk].  Rows behind lens are left as they were.  dq, dk and dv are
  * rounded once behind bf16 products with fp32 sums; dg, dbeta and dstate_in
- * come from the hi + lo products of the forward.  No atomics.
+ * come from the hi + lo products of the forward.  Repeats bit by bit, as above.
  * Workspace: lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD).  Errors: as above;
  * UNSUPPORTED also for fp32 and for strides that a tensor map cannot hold. */
 lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k, const void* v,

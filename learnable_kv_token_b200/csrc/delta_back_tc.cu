@@ -15,8 +15,7 @@
 // Warps 0-7 keep the chain.  8-11 scale dO, write the image of dS and take <dS, S>;
 // 12-15 write dV and the image of F and take the sums over value channels u.F / b
 // and v.F per token (the sums are what the gates' gradients need).  16 loads; 17
-// issues the MMAs.  Registers: 112 for the chain, 104 for the sums, 48 for the rest;
-// one spilled costs a trip to L2.
+// issues the MMAs.
 // The products of dO with Q run while the chain warps turn F, so the chain of a
 // chunk is P -> dU -> F -> dS as in the forward pass.  Sequences of more heads than
 // SMs are cut into pieces as there; dS goes from one to the next by `hand`.  Long
@@ -36,6 +35,9 @@ namespace backtc {
 using namespace chaintc;
 
 constexpr int kThreads = 640;
+// registers of a thread: warps 0-3, 4-7 (chain), 8-11 (dO, <dS, S>), 12-15 (F, dV), 16-19 (the rest)
+constexpr int kChainRegs = 112, kStateRegs = 120, kValueRegs = 88, kRestRegs = 48;
+static_assert(2 * kChainRegs + kStateRegs + kValueRegs + kRestRegs <= kThreads / 128 * launch_regs(kThreads), "registers");
 // a stage: K, Q, dO, V (two halves each), the record's T hi, T lo, A hi, A lo, scalars
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kD = 4 * kHalf, kV = 6 * kHalf, kR = 8 * kHalf;
 constexpr uint32_t kScalOff = kR + 4 * kImg;
@@ -142,7 +144,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int n = PIECES || SEG ? min(max((len + L - 1) / L - cb, 0), a.seg_chunks) : (len + L - 1) / L;
   bool ok = true;
 
-  if (warp >= 16) regs_dec<48>();
+  if (warp >= 16) regs_dec<kRestRegs>();
   if (warp == 16) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + (long long)u * a.chunks * rec_bytes(true);
@@ -292,7 +294,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (lane == 0) flight[kFlightMma] = issued;
   } else if (warp < 8) {
     // ========================================================== chain warps
-    regs_inc<112>();
+    regs_inc<kChainRegs>();
     constexpr int QC = DK / 4;
     const int row = (warp & 3) * 32 + lane, hc = warp >> 2;
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -472,7 +474,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int at_s = rb * (DK / 8) * 128 + r7 * 16, at_t = rb * (L / 8) * 128 + r7 * 16;
     const uint8_t* s_img = reinterpret_cast<const uint8_t*>(a.s0) + (long long)u * a.chunks * (DV * DK * 4) + at_s;
     if (warp < 12) {
-      regs_inc<120>();
+      regs_inc<kStateRegs>();
       // ---- scale e^G dO, the image of dS, <dS, S>
       uint8_t* d_img = reinterpret_cast<uint8_t*>(ga.ds) + (long long)u * a.chunks * (DV * DK * 2) + at_s;
       constexpr int kAhead = 4, kPieces = DK == 128 ? 6 : DK / 16;   // (the others come to shared memory)
@@ -613,7 +615,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         put_inner(cb, in);
       }
     } else {
-      regs_dec<88>();
+      regs_dec<kValueRegs>();
       // ---- F: image, dV, u.F / b and v.F per token
       const uint8_t* u_img = reinterpret_cast<const uint8_t*>(a.u) + (long long)u * a.chunks * (DV * L * 4) + at_t;
       uint8_t* f_img = reinterpret_cast<uint8_t*>(ga.fimg) + (long long)u * a.chunks * (DV * L * 2) + at_t;

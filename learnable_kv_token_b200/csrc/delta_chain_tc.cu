@@ -52,6 +52,9 @@ namespace delta {
 namespace chaintc {
 
 constexpr int kThreads = 512;
+// registers of a thread: warps 0-3, 4-7 (chain), 8-11 (O), 12-15 (the rest)
+constexpr int kChainRegs = 144, kOutRegs = 144, kRestRegs = 80;
+static_assert(2 * kChainRegs + kOutRegs + kRestRegs <= kThreads / 128 * launch_regs(kThreads), "registers");
 // a stage: K, Q, V (two halves each), then T hi, T lo, A, scalars as in the record
 constexpr uint32_t kK = 0, kQ = 2 * kHalf, kV = 4 * kHalf, kR = 6 * kHalf;
 constexpr uint32_t kScalOff = kR + 3 * kImg;
@@ -133,7 +136,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   const int n_chunks = min((len + L - 1) / L, a.seg_chunks);
   bool ok = true;
 
-  if (warp >= 12) regs_dec<80>();
+  if (warp >= 12) regs_dec<kRestRegs>();
   if (warp == 12) {
     // ================================================================ loads
     const uint8_t* recs = a.rec + ((long long)u * a.chunks + cb) * rec_bytes(a_lo);
@@ -268,7 +271,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (lane == 0) flight[kFlightMma] = issued;
   } else if (warp < 8) {
     // ========================================================== chain warps
-    regs_inc<144>();
+    regs_inc<kChainRegs>();
     constexpr int QC = DK / 4;                                 // S columns per thread and half
     const int row = (warp & 3) * 32 + lane, hc = warp >> 2;    // value channel = TMEM lane; which columns
     const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -445,7 +448,7 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
   } else if (warp < 12) {
     // ==================================================== O, or the images
-    regs_inc<144>();
+    regs_inc<kOutRegs>();
     const int quad = warp - 8, row = quad * 32 + lane;
     const uint32_t la = tmem + ((uint32_t)(quad * 32) << 16);
     int c = 0;

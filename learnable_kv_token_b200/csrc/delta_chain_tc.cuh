@@ -25,10 +25,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
-// Registers go from the warps that load and issue to those that compute: 4 warp
-// groups of 128 registers a thread at launch, 144 + 144 + 144 + 80 after.  (With
+// Registers go from the warps that load and issue to those that compute.  (With
 // nearly all of the L1 cache as shared memory, a spilled register costs a trip to
-// L2.)  All four warps of a group call these.
+// L2.)  All four warps of a group call these.  What the groups hold together after
+// them must not exceed what the launch allocated, or regs_inc would wait for good:
+// each kernel checks its own groups against launch_regs, a thread's share of the SM's
+// 65536 registers in steps of 8.
+constexpr int launch_regs(int threads) { return 65536 / threads / 8 * 8; }
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>

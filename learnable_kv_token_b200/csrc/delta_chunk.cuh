@@ -88,9 +88,6 @@ __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int T) {
   return lens == nullptr ? T : min(max(lens[b], 0), T);
 }
 
-// Images of S_0, U, dS and F: [rows][cols] bf16 in blocks of 8 x 8 (128 bytes: row g
-// at 16 g), rows = value channels.  A thread that has a row stores 16 bytes per
-// block, eight threads a block; ldmatrix reads blocks without bank conflicts.
 struct ChunkArgs {
   const __nv_bfloat16 *q, *k, *v;
   Strides4 qs, ks, vs, os;
@@ -100,7 +97,11 @@ struct ChunkArgs {
   float* s_out;
   __nv_bfloat16* o;
   uint8_t* rec;          // [units][chunks] records
-  uint32_t *s0, *u;      // images of S_0 (hi, lo) and U (hi, lo) per chunk, for the gradients
+  // For the gradients, per chunk: images of S_0 (hi, lo) and U (hi, lo), [rows][cols] bf16
+  // in blocks of 8 x 8 (128 bytes: row g at 16 g), rows = value channels.  A thread that
+  // has a row stores 16 bytes per block, eight threads a block; ldmatrix reads blocks
+  // without bank conflicts.
+  uint32_t *s0, *u;
   int T, H, Hk, dv, chunks;
   float scale;
   // segments (segs = 1: the sequence in one piece): chunks of each, n [units][segs - 1][dv][dk],
@@ -126,7 +127,7 @@ struct GradArgs {
   float* ds_in;              // gradient of the initial state (nullable)
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg, *db;
-  uint32_t *ds, *fimg;       // images of dS (hi) and F (hi) per chunk
+  uint32_t *ds, *fimg;       // images of dS (hi) and F (hi) per chunk, laid out as S_0's and U's
   float* hand;               // [units][dv][dk]: dS between pieces (forward: S, as s_out)
   float *x, *inner;          // per chunk and strip of 16 value channels: u.y and v.dv per token; <dS_0, S_0>
 };
