@@ -263,6 +263,13 @@ delta_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             for (int ks = 0; ks < L / 16; ++ks)
               mma_f16_ts(tmem + kColO + 16 * ks, tmem + (p ? kColUL : kColUH) + 8 * ks,
                          dt + ((2 * kImg + ks * (16 * 128 + 32)) >> 4), idesc2(128, L - 16 * ks, false, false), 1u);
+          // U hi with A's lo, from where prepare put its columns of blocks
+#pragma unroll
+          for (int ks = 1; ks < L / 16; ++ks)
+            mma_f16_ts(tmem + kColO + 16 * ks, tmem + kColUH + 8 * ks, dt + ((2 * kImg + (4 - ks) * 32) >> 4),
+                       idesc2(128, L - 16 * ks, false, false), 1u);
+          mma_f16_ts(tmem + kColO, tmem + kColUH, dt + ((kImg + 2 * 32) >> 4), idesc2(128, 16, false, false), 1u);
+          mma_f16_ts(tmem + kColO + 16, tmem + kColUH, dt + ((kImg + 3 * 32) >> 4), idesc2(128, L - 16, false, false), 1u);
           mma_commit(bar(bO));
         }
       }

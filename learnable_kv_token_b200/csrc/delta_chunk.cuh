@@ -30,9 +30,10 @@ constexpr int L = 64;
 
 // Per-chunk record in the workspace: T below its diagonal as hi and lo (the
 // diagonal is b; T's rows act on R mostly through it, so it stays in fp32 and
-// the bf16 pairs' error falls on the rest), A as hi (and lo, for the gradients),
-// each a [64][64] bf16 image in the swizzled order in which it lies in shared
-// memory, then five rows of 64 floats, and a sixth for the gradients.
+// the bf16 pairs' error falls on the rest), A as hi and lo, each a [64][64] bf16
+// image in the swizzled order in which it lies in shared memory (A's lo has one for
+// the gradients only; for the prompt it lies in blocks of A's and T lo's that are not
+// used, delta_prepare.cu), then five rows of 64 floats, and a sixth for the gradients.
 constexpr int kImg = L * L * 2;
 constexpr int kScal = 5 * L * 4;
 constexpr int kEG = 0, kLam = 1, kBeta = 2, kGhi = 3, kGlo = 4;   // e^G, e^{G_L - G}, b, G as a float pair

@@ -72,6 +72,17 @@ __device__ __forceinline__ void store_c(float* p, const float* c, int lane, floa
 }
 
 
+// The prompt's record has no image for A's lo: products leave out the 16 x 16 blocks
+// above the diagonal, and there it lies, a column of blocks of it under one another for
+// the chain's operands.  Column j >= 1 in A's image from row 0 of column 4 - j on; of
+// column 0, which no column has room for, the block on the diagonal in T lo's image
+// (the second buffer) in column 2, the others there in column 3.  (Offset of token row t,
+// in bytes, and its first 16-byte piece.)
+__device__ __forceinline__ uint32_t alo_at(int t, int j) {
+  return j > 0 ? (t - 16 * j) * 128 : kImg + (t < 16 ? t : t - 16) * 128;
+}
+__device__ __forceinline__ int alo_col(int t, int j) { return j > 0 ? 2 * (4 - j) : t < 16 ? 4 : 6; }
+
 template <int DK, bool A_LO>
 __global__ void __launch_bounds__(kPrepThreads, 6)
 delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const ChunkArgs a) {
@@ -222,12 +233,17 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split2(y[2 * e], y[2 * e + 1], hi[e], lo[e]);
+          // lo: an image of its own, or in blocks above the diagonal (alo_at; t & 7 is the place's as well)
+          const uint32_t at = A_LO ? kImg + t * 128 : alo_at(t, j);
+          const int cl = A_LO ? 2 * j : alo_col(t, j);
+          if (A_LO || j <= t >> 4) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t off = t * 128 + (((2 * j + e) ^ (t & 7)) << 4);
-            *reinterpret_cast<uint4*>(img + off) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-            if (A_LO)
-              *reinterpret_cast<uint4*>(img + kImg + off) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+            for (int e = 0; e < 2; ++e) {
+              *reinterpret_cast<uint4*>(img + t * 128 + (((2 * j + e) ^ (t & 7)) << 4)) =
+                  make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+              *reinterpret_cast<uint4*>(img + at + (((cl + e) ^ (t & 7)) << 4)) =
+                  make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+            }
           }
         }
       }
@@ -296,6 +312,7 @@ delta_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll 1
     for (int it = 0; it < L * 8 / kPrepThreads; ++it) {
       const int i = it * kPrepThreads + tid, t = i >> 3, cc = i & 7;
+      if (!A_LO && cc >> 1 > t >> 4) continue;            // a block above the diagonal: A's lo, or nothing that is read
       uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
       if (8 * cc < t) {
 #pragma unroll

@@ -136,6 +136,18 @@ def test_prefill_extreme_gates(layer, dtype, kind):
     check_prefill(layer, x, scale)
 
 
+@pytest.mark.parametrize("shape", [(2, 300, 4, 2, 128, 128), (1, 2000, 2, 1, 64, 128), (3, 130, 4, 4, 128, 64)], ids=str)
+def test_outputs_are_rounded_once(layer, shape):
+    """o is the rounded result almost everywhere.  Where the sum before it is off by d of its row's size (2e-5
+    as the states), an entry z of that size comes out as the neighbour with probability 2 d 2^8 / z = c / z, c =
+    0.01; over entries with a density of at most 0.8 at any z in (0, 3): 0.8 c (1 + ln(3 / c)) = 0.054.  Twice
+    that for rows whose terms are larger than their sum.  (One operand rounded to bf16: over a third differ.)"""
+    x = inputs(25, *shape)
+    o, _ = layer.delta_prefill(*(x[n] for n in ("q", "k", "v", "g", "beta")), state=x["state"])
+    want = torch.from_numpy(oracle(x)[0]).to(torch.bfloat16)
+    assert (o.cpu() != want).double().mean() <= 0.108
+
+
 @pytest.mark.parametrize("init", [False, True])
 def test_tokens_of_beta_0_write_nothing(layer, init):
     """As in the step and in the walk by tokens: the state only decays, and stays exactly zero from zero."""
