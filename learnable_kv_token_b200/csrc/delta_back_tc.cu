@@ -22,8 +22,8 @@
 // sequences of few heads are cut into segments as there: dS goes back through a
 // segment by the transpose of its X, so a first pass finds the chains from zero,
 // the join carries them, and a second pass runs every segment from its dS.  64 chunks of 128 heads of
-// 128 channels (one wave): 483 us, 7.5 us a chunk; 160 KB of images and dV
-// per chunk beside 97 KB of inputs (2.1 GB, 4.4 TB/s) make memory latency the bound.
+// 128 channels (one wave): 490 us, 7.6 us a chunk; 160 KB of images and dV
+// per chunk beside 97 KB of inputs (2.1 GB, 4.3 TB/s) make memory latency the bound.
 #include <math.h>
 
 #include "delta_chain_tc.cuh"

@@ -33,8 +33,12 @@ namespace delta {
 // while this one is in use (images by bulk copies, token rows by cp.async).  The value heads that share a key head follow
 // one another; dQ and dK stay in registers over them and are rounded once.
 // 224 KB read per chunk and head, 176 of them images: 8 x 4096 tokens x 16 heads of
-// 128 channels in 549 us, 3.4 TB/s.  Of 19000 cycles per chunk 7200 are warp MMAs;
+// 128 channels in 545 us, 3.4 TB/s (572 for 4 key heads, each shared by four).  Of 19000 cycles per chunk 7200 are warp MMAs;
 // the rest is phases between barriers with sixteen warps to an SM.
+// What feeds dQ, and through q.dQ the gates, takes pairs (U, S_0, W).  What feeds dK
+// alone takes one bf16 of each: F and dS, which no pair of is kept, U and S_0 beside
+// them, W transposed, Z.  dK comes out 2.9e-3 off in the 2-norm, 1.7e-3 of it its own
+// rounding; with the pairs that are here (U, S_0, W) 2.3e-3, in 645 us for 545.
 constexpr int kGradThreads = 512;
 constexpr int kHV = 64;                                    // value channels of a half
 

@@ -22,8 +22,8 @@
 // (e^{G_L} S, U for O); S comes and goes in two halves of its columns, so a pass
 // over one half runs beside the product on the other; products with T and A
 // leave out the columns above the diagonal.  64 chunks of 512 heads of 128
-// channels: 650 us (seven waves of half sequences), 4400 cycles a chunk, 1300 of
-// them products; 3.0 GB moved, 4.6 TB/s, which two stages of loads cover.
+// channels: 672 us (seven waves of half sequences; 660 without A's lo), 4400 cycles a chunk, 1300 of
+// them products; 3.0 GB moved, 4.5 TB/s, which two stages of loads cover.
 //
 // Long sequences of few heads are cut into segments of chunks, one CTA each.  A
 // row of S goes through a segment by an affine map s -> s X + n that is the same

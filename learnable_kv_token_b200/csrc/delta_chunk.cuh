@@ -14,9 +14,16 @@
 // in time, so with g <= 0 no factor exceeds 1, whatever the decay.
 //
 // Precision.  q, k, v and their gradients are bf16, exact as operands.  Where a
-// state or a correction is an operand of a product that feeds the state, it
-// goes in as a bf16 pair hi + lo (two products; relative error about 2^-17),
-// so the fp32 state keeps fp32-like accuracy on the bf16 tensor path.
+// state or a correction is an operand of a product that feeds a state, it goes in as
+// a bf16 pair hi + lo (two products; relative error about 2^-18 in the mean); T's
+// product leaves out lo lo, of the same size.  States and their gradients come out
+// 3.4e-6 to 4.1e-6 off in the 2-norm, gates' gradients 5e-6 to 7e-6, where fp32
+// products give 4e-7 and 9e-7.  Nearly all of a state's share is U's split (2.8e-6 of
+// 3.1e-6 with S, R, T and U split in 64-bit arithmetic on the host; a third part of
+// each leaves 1e-7).  Third parts would be half as many products again on the chain
+// that bounds these kernels, and their columns do not fit the backward chain's TMEM,
+// which pairs fill.  What feeds bf16 outputs alone takes fewer bits where that is
+// measurably cheaper (delta_backward.cu); O takes A and U as pairs.
 #pragma once
 
 #include "lte_common.cuh"

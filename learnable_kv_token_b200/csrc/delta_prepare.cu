@@ -8,14 +8,15 @@
 // A.  X = (I + M)^{-1} in fp32, in place of M: the four 16 x 16 diagonal blocks by
 // forward substitution (a lane per column), joined in pairs twice by
 //   [A 0; C B]^{-1} = [A' 0; -B' C A' B'],
-// the products as three TF32 warp MMAs.  Forward substitution keeps X accurate
+// the products as three TF32 warp MMAs.  Decays are powers of two by the approximate
+// exponential (2 units in the last place, as expf) of float pairs.  Forward substitution keeps X accurate
 // where a series in powers of M would not (equal keys make M's powers grow; X
 // itself stays bounded).  A and T leave as images by bulk copies.
 // The launch moves 57 KB per chunk (q, k in; T, A, scalars out): 1.87 GB for 32 x
-// 4096 tokens x 16 heads in 405 us, 4.6 TB/s.  Beside that traffic it is bound by
+// 4096 tokens x 16 heads in 425 us, 4.4 TB/s (409 without A's lo).  Beside that traffic it is bound by
 // instruction issue (55 % busy) and by the barriers between its steps; loops over
 // columns are not unrolled because six CTAs in different steps miss the instruction
-// cache otherwise (434 us).
+// cache otherwise (29 us more).
 #include <math.h>
 
 #include "delta_chain_tc.cuh"
