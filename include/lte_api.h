@@ -547,7 +547,10 @@ lte_status lte_gdr_prefill(const lte_gdr_dims* d, const void* q, const void* k, 
  * dtype, contiguous; dg, dbeta fp32 [B,T,H]; dstate_in (nullable) fp32
  * [B,H,dv,dk].  Rows behind lens are left as they were.  dq, dk and dv are
  * rounded once behind bf16 products with fp32 sums; dg, dbeta and dstate_in
- * come from the hi + lo products of the forward.  Repeats bit by bit, as above.
+ * come from the hi + lo products of the forward.  dg_t is a difference of sums of
+ * q_t.dq_t and v_t.dv_t of its block: off by about 5e-6 of those, which is little of
+ * dg where states last, but all of it where a gate keeps less than that (g_t < -12);
+ * where it keeps nothing (e^{g_t} = 0 in fp32) dg_t is zero.  Repeats bit by bit, as above.
  * Workspace: lte_gdr_workspace_bytes(d, LTE_GDR_WS_BACKWARD).  Errors: as above;
  * UNSUPPORTED also for fp32 and for strides that a tensor map cannot hold. */
 lte_status lte_gdr_backward(const lte_gdr_dims* d, const void* q, const void* k, const void* v,

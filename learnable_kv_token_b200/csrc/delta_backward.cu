@@ -314,12 +314,19 @@ delta_grad_kernel(const GradArgs ga, int items) {
           if (lane >= o) sum += v;
         }
         const double first = in - (sum - y1 - y0);
+        // nothing passes a gate whose exponential is zero (-104 in the sums), and no gradient: not the
+        // rounding of a difference that should vanish
+        const float2 gh = *reinterpret_cast<const float2*>(scal + kGhi * L + 2 * lane);
+        const float2 go = *reinterpret_cast<const float2*>(scal + kGlo * L + 2 * lane);
+        const float ph = __shfl_up_sync(0xffffffffu, gh.y, 1), po = __shfl_up_sync(0xffffffffu, go.y, 1);
+        const bool shut[2] = {(gh.x - (lane ? ph : 0.f)) + (go.x - (lane ? po : 0.f)) < -103.99f,
+                              (gh.y - gh.x) + (go.y - go.x) < -103.99f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = t0 + 2 * lane + i;
           if (t < len) {
             const long long gi = ((long long)b * a.T + t) * a.H + h;
-            ga.dg[gi] = (float)(i ? first - y0 : first);
+            ga.dg[gi] = shut[i] ? 0.f : (float)(i ? first - y0 : first);
             ga.db[gi] = x[i] / scal[kBeta * L + 2 * lane + i];
           }
         }

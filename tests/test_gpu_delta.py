@@ -338,6 +338,24 @@ def test_small_gradients_of_small_betas(layer, beta, size):
             assert rel(a, r) <= tols[name], f"{name}: {rel(a, r):.3g} > {tols[name]:.3g}"
 
 
+@pytest.mark.parametrize("which", ["all", "some"])
+def test_no_gradient_of_gates_that_are_shut(layer, which):
+    """A gate of e^g = 0 lets nothing pass: its gradient is exactly zero, the others' as ever."""
+    x = inputs(26, 2, 150, 4, 2, 128, 64)
+    shut = torch.ones_like(x["g"], dtype=torch.bool)
+    if which == "some":
+        shut = torch.rand(shut.shape, generator=torch.Generator().manual_seed(9)).cuda() < 0.1
+        shut[:, :1] = shut[:, 63:66] = True
+    x["g"] = torch.where(shut, torch.where(torch.arange(4, device="cuda") % 2 == 0, float("-inf"), -104.0), x["g"])
+    do = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
+    got = layer.delta_backward(*(x[n] for n in ("q", "k", "v", "g", "beta")), do, state=x["state"])
+    assert (got[3][shut] == 0).all()
+    g = torch.where(shut, float("-inf"), x["g"])               # (in 64 bits e^-104 is not zero)
+    ref = DO.delta_backward(*(f64(y) for y in (x["q"], x["k"], x["v"], g, x["beta"], do, x["state"])))
+    for a, r, tol in zip(got, ref, (GRAD_TOL, GRAD_TOL, BF16_TOL, GATE_TOL, GATE_TOL, STATE_TOL)):
+        assert torch.isfinite(a).all() and rel(a, r) <= tol
+
+
 def test_backward_by_differences(layer):
     """The gradient of every input along a random direction against a central difference of the
     forward pass, with steps of h = 0.05 of the input's norm along the gradient.
